@@ -9,10 +9,12 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libmoefp8.so"
 
-SCALE_FMTS = {"fp32": 0, "pow2": 1, "ue8m0": 2}
+SCALE_FMTS = {"fp32": 0, "pow2": 1, "ue8m0": 2, "mxfp4": 4}
 ROUNDINGS = {"divide": 0, "reciprocal": 1}
 ACTS = {"swiglu": 0, "swiglu_clamp": 1, "swiglu_clamp_after_silu": 2}
 WEIGHT_FMTS = {"e4m3": 0, "mxfp4": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 # Row-tile geometry of the grouped GEMM (mirrors the header's macros), used to
 # interpret the tiles_visited counter.
 GEMM_TILES = {"stream_tile_m": 16, "stream_max_rows": 64, "tiled_tile_m": 256, "col_tile": 128}
@@ -64,6 +66,11 @@ class _Tensors(ctypes.Structure):
                 ("out", _vp)]
 
 
+class _Router(ctypes.Structure):
+    _fields_ = [("num_experts", _i32), ("topk", _i32), ("score", ctypes.c_int), ("renormalize", _i32),
+                ("scale", _f32), ("num_groups", _i32), ("top_groups", _i32), ("group_top", _i32)]
+
+
 class _Layout(ctypes.Structure):
     _fields_ = [("expert_counts", ctypes.c_size_t), ("expert_offsets", ctypes.c_size_t),
                 ("row_to_pair", ctypes.c_size_t), ("pair_to_row", ctypes.c_size_t),
@@ -76,6 +83,9 @@ class _Layout(ctypes.Structure):
 _SIGNATURES = {
     "moe_min_row_cap": (_i32, [_i32, _i32, _i32, _i32]),
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
+    "moe_route": (ctypes.c_int, [ctypes.POINTER(_Router), _vp, ctypes.c_int, ctypes.c_int64, _vp, _i32,
+                                 _vp, _vp, _vp, _vp]),
+    "moe_mxfp4_dequant": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, _i32, _vp, _vp]),
     "moe_align": (ctypes.c_int, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                  _vp]),
     "moe_align_batched": (ctypes.c_int, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
@@ -190,7 +200,18 @@ def _rounding(rounding):
 
 
 def _scale_dtype(fmt):
-    return torch.uint8 if fmt == "ue8m0" else torch.float32
+    return torch.uint8 if fmt in ("ue8m0", "mxfp4") else torch.float32
+
+
+def _code_cols(cols, fmt):
+    """Bytes of a row of codes (MXFP4: two columns per byte)."""
+    return cols // 2 if fmt == "mxfp4" else cols
+
+
+def _scale_shape(rows, cols, fmt):
+    """Shape of the scales of [rows, cols]: group-major per 128 columns, or
+    MXFP4's row-major bytes per 32."""
+    return (rows, cols // 32) if fmt == "mxfp4" else (cols // 128, rows)
 
 
 def _live(t_live):
@@ -214,6 +235,60 @@ def moe_min_row_cap(t_cap, topk, num_experts, align_rows):
 
 def moe_status_string(status):
     return load_library().moe_status_string(status).decode()
+
+
+def moe_route(logits, topk, score="softmax", bias=None, renormalize=True, scale=1.0, num_groups=1,
+              top_groups=1, group_top=1, t_live=None, ids=None, weights=None):
+    """Top-k routing from router logits [t_cap, E] (float32, bfloat16 or float16,
+    columns contiguous, any row stride). Returns (ids int32 [t_cap, topk],
+    weights float32 [t_cap, topk]), what moe_align and moe_forward take."""
+    lib = load_library()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a tensor")
+    if logits.dtype not in LOGIT_TYPES:
+        raise TypeError(f"logits must be one of {list(LOGIT_TYPES)}, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [t_cap, num_experts]")
+    t_cap, num_experts = logits.shape
+    ld = logits.stride(0) if t_cap > 1 else num_experts
+    if (num_experts > 1 and logits.stride(1) != 1) or ld < num_experts:
+        raise ValueError("the columns of logits must be contiguous and its rows apart")
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {list(SCORES)}")
+    if bias is not None:
+        _shape(_need(bias, "bias", torch.float32), "bias", (num_experts,))
+    if ids is None:
+        ids = torch.empty((t_cap, topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((t_cap, topk), dtype=torch.float32, device=logits.device)
+    _shape(_need(ids, "ids", torch.int32), "ids", (t_cap, topk))
+    _shape(_need(weights, "weights", torch.float32), "weights", (t_cap, topk))
+    _same_device(logits, bias, ids, weights)
+    router = _Router(num_experts, topk, SCORES[score], int(bool(renormalize)), float(scale),
+                     int(num_groups), int(top_groups), int(group_top))
+    st = lib.moe_route(ctypes.byref(router), _ptr(logits), LOGIT_TYPES[logits.dtype], ld, _ptr(bias),
+                       t_cap, _live(t_live), _ptr(ids), _ptr(weights), _stream())
+    _check("moe_route", st)
+    return ids, weights
+
+
+def moe_mxfp4_dequant(codes, scales, out=None):
+    """BF16 values of an MXFP4 tensor: codes uint8 [..., cols/2], scales uint8
+    [..., cols/32]. Returns BF16 [..., cols] (or ``out``)."""
+    lib = load_library()
+    _need(codes, "codes", torch.uint8)
+    if codes.dim() < 1 or codes.shape[-1] < 16 or codes.shape[-1] % 16:
+        raise ValueError("codes must be [..., cols / 2] with cols a multiple of 32")
+    lead, cols = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    _shape(_need(scales, "scales", torch.uint8), "scales", lead + (cols // 32,))
+    if out is None:
+        out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
+    ob = _shape(_bf16_view(out, "out"), "out", lead + (cols,))
+    _same_device(codes, scales, ob)
+    st = lib.moe_mxfp4_dequant(_ptr(codes), _ptr(scales), codes.numel() * 2 // cols, cols, _ptr(ob),
+                               _stream())
+    _check("moe_mxfp4_dequant", st)
+    return out
 
 
 def moe_align(topk_ids, num_experts, align_rows=16, row_cap=None, t_live=None, out=None,
@@ -270,18 +345,19 @@ def moe_align_batched(topk_ids, num_experts, expert_cap, t_live=None, out=None, 
 
 
 def moe_act_quant(x, fmt="fp32", t_live=None, xq=None, xs=None, rounding="divide"):
-    """Per-token 1x128 quantization. Returns (xq uint8 [t_cap, H], xs [H/128, t_cap])."""
+    """Per-token 1x128 quantization. Returns (xq uint8 [t_cap, H], xs [H/128, t_cap]);
+    with ``fmt="mxfp4"`` (xq uint8 [t_cap, H/2], xs uint8 [t_cap, H/32])."""
     lib = load_library()
     xb = _bf16_view(x, "x")
     if xb.dim() != 2:
         raise ValueError("x must be [t_cap, hidden]")
     t_cap, hidden = xb.shape
     if xq is None:
-        xq = torch.empty((t_cap, hidden), dtype=torch.uint8, device=xb.device)
+        xq = torch.empty((t_cap, _code_cols(hidden, fmt)), dtype=torch.uint8, device=xb.device)
     if xs is None:
-        xs = torch.empty((hidden // 128, t_cap), dtype=_scale_dtype(fmt), device=xb.device)
-    _shape(_need(xq, "xq", torch.uint8), "xq", (t_cap, hidden))
-    _shape(_need(xs, "xs", _scale_dtype(fmt)), "xs", (hidden // 128, t_cap))
+        xs = torch.empty(_scale_shape(t_cap, hidden, fmt), dtype=_scale_dtype(fmt), device=xb.device)
+    _shape(_need(xq, "xq", torch.uint8), "xq", (t_cap, _code_cols(hidden, fmt)))
+    _shape(_need(xs, "xs", _scale_dtype(fmt)), "xs", _scale_shape(t_cap, hidden, fmt))
     _same_device(xb, xq, xs)
     st = lib.moe_act_quant(_ptr(xb), t_cap, _live(t_live), hidden, _fmt(fmt), _rounding(rounding),
                            _ptr(xq), _ptr(xs), _stream())
@@ -332,6 +408,7 @@ def moe_grouped_gemm_mxfp4(a, a_scales, fmt, w, w_scales, counts, offsets=None, 
                            out=None):
     """Grouped GEMM with MXFP4 weights over live rows. ``w`` is uint8 [E, N, K/2]
     packed E2M1 codes, ``w_scales`` uint8 [E, N, K/32] E8M0 bytes. With
+    ``fmt="mxfp4"`` A is MXFP4 too (uint8 [a_rows, K/2] and [a_rows, K/32]). With
     ``expert_cap`` > 0 the batched layout (``counts`` = masked_m, no offsets,
     row_cap = E * expert_cap). Returns BF16 bits (int16) [row_cap, N]."""
     lib = load_library()
@@ -342,9 +419,9 @@ def moe_grouped_gemm_mxfp4(a, a_scales, fmt, w, w_scales, counts, offsets=None, 
     num_experts, n, k2 = w.shape
     k = 2 * k2
     a_rows = a.shape[0]
-    if a.shape[1] != k:
+    if a.shape[1] != _code_cols(k, fmt):
         raise ValueError("a and w disagree on K")
-    _shape(a_scales, "a_scales", (k // 128, a_rows))
+    _shape(a_scales, "a_scales", _scale_shape(a_rows, k, fmt))
     _shape(w_scales, "w_scales", (num_experts, n, k // 32))
     _shape(_need(counts, "counts", torch.int32), "counts", (num_experts,))
     if expert_cap > 0:
@@ -413,7 +490,8 @@ def moe_silu_mul_quant_masked(gate_up, masked_m, expert_cap, act="swiglu",
                               clamp_limit=float("inf"), fmt="fp32", hq=None, hs=None,
                               rounding="divide"):
     """SiLU(gate)*up + 1x128 FP8 quantization on the batched masked-M layout.
-    Returns (hq uint8 [E*cap, I], hs [I/128, E*cap])."""
+    Returns (hq uint8 [E*cap, I], hs [I/128, E*cap]); with ``fmt="mxfp4"`` (hq
+    [E*cap, I/2], hs uint8 [E*cap, I/32])."""
     lib = load_library()
     gu = _bf16_view(gate_up, "gate_up")
     _need(masked_m, "masked_m", torch.int32, ndim=1)
@@ -423,11 +501,11 @@ def moe_silu_mul_quant_masked(gate_up, masked_m, expert_cap, act="swiglu",
         raise ValueError(f"gate_up must be [{rows}, 2 * inter], got {tuple(gu.shape)}")
     inter = gu.shape[1] // 2
     if hq is None:
-        hq = torch.empty((rows, inter), dtype=torch.uint8, device=gu.device)
+        hq = torch.empty((rows, _code_cols(inter, fmt)), dtype=torch.uint8, device=gu.device)
     if hs is None:
-        hs = torch.empty((inter // 128, rows), dtype=_scale_dtype(fmt), device=gu.device)
-    _shape(_need(hq, "hq", torch.uint8), "hq", (rows, inter))
-    _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", (inter // 128, rows))
+        hs = torch.empty(_scale_shape(rows, inter, fmt), dtype=_scale_dtype(fmt), device=gu.device)
+    _shape(_need(hq, "hq", torch.uint8), "hq", (rows, _code_cols(inter, fmt)))
+    _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", _scale_shape(rows, inter, fmt))
     _same_device(gu, masked_m, hq, hs)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
@@ -441,7 +519,8 @@ def moe_silu_mul_quant_masked(gate_up, masked_m, expert_cap, act="swiglu",
 def moe_silu_mul_quant(gate_up, counts, offsets, act="swiglu", clamp_limit=float("inf"),
                        fmt="fp32", hq=None, hs=None, rounding="divide"):
     """SiLU(gate)*up + 1x128 FP8 quantization of live rows.
-    Returns (hq uint8 [row_cap, I], hs [I/128, row_cap])."""
+    Returns (hq uint8 [row_cap, I], hs [I/128, row_cap]); with ``fmt="mxfp4"``
+    (hq [row_cap, I/2], hs uint8 [row_cap, I/32])."""
     lib = load_library()
     gu = _bf16_view(gate_up, "gate_up")
     if gu.dim() != 2 or gu.shape[1] % 2:
@@ -452,11 +531,11 @@ def moe_silu_mul_quant(gate_up, counts, offsets, act="swiglu", clamp_limit=float
     num_experts = counts.shape[0]
     _shape(_need(offsets, "offsets", torch.int32), "offsets", (num_experts + 1,))
     if hq is None:
-        hq = torch.empty((row_cap, inter), dtype=torch.uint8, device=gu.device)
+        hq = torch.empty((row_cap, _code_cols(inter, fmt)), dtype=torch.uint8, device=gu.device)
     if hs is None:
-        hs = torch.empty((inter // 128, row_cap), dtype=_scale_dtype(fmt), device=gu.device)
-    _shape(_need(hq, "hq", torch.uint8), "hq", (row_cap, inter))
-    _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", (inter // 128, row_cap))
+        hs = torch.empty(_scale_shape(row_cap, inter, fmt), dtype=_scale_dtype(fmt), device=gu.device)
+    _shape(_need(hq, "hq", torch.uint8), "hq", (row_cap, _code_cols(inter, fmt)))
+    _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", _scale_shape(row_cap, inter, fmt))
     _same_device(gu, counts, offsets, hq, hs)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
@@ -560,7 +639,8 @@ def moe_forward(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="fp32", a
     """The whole expert layer. Returns (out BF16 bits int16 [t_cap, H], workspace uint8).
     ``topk_w=None`` weights every routed pair by one. ``weight_fmt="mxfp4"``:
     w1/w2 are packed E2M1 codes [E, rows, cols/2] with E8M0 scale bytes
-    [E, rows, cols/32]."""
+    [E, rows, cols/32]; with it ``fmt="mxfp4"`` quantizes both activations to
+    MXFP4."""
     lib = load_library()
     xb = _bf16_view(x, "x")
     if xb.dim() != 2:

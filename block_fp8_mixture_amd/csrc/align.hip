@@ -272,6 +272,10 @@ hipError_t launch_prep(const int32_t* ids, int t_cap, const int32_t* t_live_dev,
     hipLaunchKernelGGL(prep_kernel<kFp32Pow2>, grid, dim3(kThreads), 0, stream, ids, t_cap,
                        t_live_dev, topk, num_experts, align_rows, counts, offsets, row_to_pair,
                        pair_to_row, n_align, x, hidden, xq, xs, rounding, mode);
+  else if (fmt == kMxfp4)
+    hipLaunchKernelGGL(prep_kernel<kMxfp4>, grid, dim3(kThreads), 0, stream, ids, t_cap,
+                       t_live_dev, topk, num_experts, align_rows, counts, offsets, row_to_pair,
+                       pair_to_row, n_align, x, hidden, xq, xs, rounding, mode);
   else
     hipLaunchKernelGGL(prep_kernel<kUe8m0>, grid, dim3(kThreads), 0, stream, ids, t_cap,
                        t_live_dev, topk, num_experts, align_rows, counts, offsets, row_to_pair,

@@ -60,7 +60,10 @@ void* scratch_address() {
   return ptr;
 }
 
-bool fmt_ok(int f) { return f == MOE_SCALE_FP32 || f == MOE_SCALE_FP32_POW2 || f == MOE_SCALE_UE8M0; }
+bool fmt_ok(int f) {
+  return f == MOE_SCALE_FP32 || f == MOE_SCALE_FP32_POW2 || f == MOE_SCALE_UE8M0 || f == MOE_SCALE_MXFP4;
+}
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool act_ok(int a) {
   return a == MOE_ACT_SWIGLU || a == MOE_ACT_SWIGLU_CLAMP || a == MOE_ACT_SWIGLU_CLAMP_AFTER_SILU;
 }
@@ -72,7 +75,9 @@ bool dim128(int32_t d) { return d > 0 && d % 128 == 0; }
 bool gemm_shape_ok(int64_t a_rows, int64_t n, int64_t k) {
   return k <= 32768 && a_rows * k < (int64_t{1} << 32) && n * k < (int64_t{1} << 32);
 }
+// Bytes of the scales of 128 columns (MXFP4: one per 32 columns).
 size_t scale_bytes(int fmt) { return fmt == MOE_SCALE_UE8M0 ? 1 : 4; }
+size_t code_bytes(int fmt, size_t n) { return fmt == MOE_SCALE_MXFP4 ? n / 2 : n; }
 moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
@@ -105,6 +110,52 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_HIP: return "HIP runtime error";
   }
   return "unknown status";
+}
+
+moe_status moe_route(const moe_router* r, const void* logits, moe_logit_type type, int64_t ld,
+                     const float* bias, int32_t t_cap, const int32_t* t_live_dev, int32_t* topk_ids,
+                     float* topk_w, void* stream) {
+  if (!r || r->num_experts < 1 || r->topk < 1 || r->num_groups < 1 || r->top_groups < 1 ||
+      r->top_groups > r->num_groups || (r->group_top != 1 && r->group_top != 2) || t_cap < 0 ||
+      (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) || ld < r->num_experts ||
+      (type != MOE_LOGIT_FP32 && type != MOE_LOGIT_BF16 && type != MOE_LOGIT_FP16) ||
+      !(r->scale - r->scale == 0.0f))  // infinite or NaN
+    return MOE_ERR_INVALID_ARG;
+  if (r->num_experts > moe::kMaxExperts || r->topk > kMaxTopk || r->num_groups > moe::kMaxGroups)
+    return MOE_ERR_UNSUPPORTED;
+  if (r->num_experts % r->num_groups != 0 ||
+      r->topk > r->top_groups * (r->num_experts / r->num_groups) ||
+      static_cast<int64_t>(t_cap) * r->topk > INT32_MAX / 2)
+    return MOE_ERR_INVALID_ARG;
+  if (t_cap > 0 && (!logits || !topk_ids || !topk_w)) return MOE_ERR_INVALID_ARG;
+  if (ld > INT64_MAX / 8 / (t_cap > 0 ? t_cap : 1)) return MOE_ERR_INVALID_ARG;
+  if (t_cap == 0) return MOE_OK;
+  moe::RouteArgs a;
+  a.logits = logits;
+  a.logit_type = type;
+  a.ld = ld;
+  a.bias = bias;
+  a.num_experts = r->num_experts;
+  a.topk = r->topk;
+  a.score = r->score;
+  a.renormalize = r->renormalize;
+  a.scale = r->scale;
+  a.num_groups = r->num_groups;
+  a.top_groups = r->top_groups;
+  a.group_top = r->group_top;
+  a.t_cap = t_cap;
+  a.t_live_dev = t_live_dev;
+  a.ids = topk_ids;
+  a.weights = topk_w;
+  return from_hip(moe::launch_route(a, as_stream(stream)));
+}
+
+moe_status moe_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                             uint16_t* out, void* stream) {
+  if (rows < 0 || cols < 1 || cols % 32 != 0 || rows > INT64_MAX / 4 / cols) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned(codes, 8) || !aligned(out, 16)) return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_mxfp4_dequant(codes, scales, rows, cols, out, as_stream(stream)));
 }
 
 moe_status moe_align(const int32_t* topk_ids, int32_t t_cap, const int32_t* t_live_dev,
@@ -162,6 +213,7 @@ static moe_status gemm_checked(const moe::GemmArgs& g, void* stream) {
   if (!dim128(g.n) || !dim128(g.k) || !fmt_ok(g.fmt) || g.a_rows < 0 || g.a_row_div < 1 ||
       g.num_experts < 1 || g.row_cap < 0)
     return MOE_ERR_INVALID_ARG;
+  if (g.fmt == MOE_SCALE_MXFP4) return MOE_ERR_UNSUPPORTED;  // 4-bit activations take 4-bit weights
   if (g.num_experts > moe::kMaxExperts || !gemm_shape_ok(g.a_rows, g.n, g.k))
     return MOE_ERR_UNSUPPORTED;
   if (!g.counts || (!g.offsets && g.seg_cap == 0) || !g.w || !g.w_scales) return MOE_ERR_INVALID_ARG;
@@ -243,6 +295,9 @@ static moe_status gemm_w4_checked(const moe::W4Args& g, void* stream) {
     return MOE_ERR_UNSUPPORTED;
   if (!g.counts || (!g.offsets && g.seg_cap == 0) || !g.w || !g.w_scales) return MOE_ERR_INVALID_ARG;
   if (g.row_cap > 0 && (!g.c || !g.a || !g.a_scales || g.a_rows < 1)) return MOE_ERR_INVALID_ARG;
+  if (g.fmt == MOE_SCALE_MXFP4 && !(aligned(g.a, 16) && aligned(g.w, 16) && aligned(g.c, 16) &&
+                                    aligned(g.a_scales, 4) && aligned(g.w_scales, 4)))
+    return MOE_ERR_INVALID_ARG;
   if (g.row_cap == 0) return MOE_OK;
   return from_hip(moe::launch_grouped_gemm_w4(g, as_stream(stream)));
 }
@@ -333,9 +388,11 @@ moe_status moe_workspace_plan(const moe_problem* p, moe_workspace_layout* L) {
       !fmt_ok(p->scale_fmt) || !act_ok(p->act) || !rounding_ok(p->rounding) ||
       (p->weight_fmt != MOE_WEIGHT_E4M3 && p->weight_fmt != MOE_WEIGHT_MXFP4))
     return MOE_ERR_INVALID_ARG;
+  const bool mx = p->scale_fmt == MOE_SCALE_MXFP4;  // 4-bit activations
   if (p->act != MOE_ACT_SWIGLU && !(p->clamp_limit > 0.0f)) return MOE_ERR_INVALID_ARG;
   if (p->num_experts > moe::kMaxExperts) return MOE_ERR_UNSUPPORTED;
   if (p->expert_cap < 0) return MOE_ERR_INVALID_ARG;
+  if (mx && p->weight_fmt != MOE_WEIGHT_MXFP4) return MOE_ERR_UNSUPPORTED;
   const bool batched = p->expert_cap > 0;
   // Rows: any aligned routing's need, or the batched layout's E * cap.
   const int64_t need = batched ? static_cast<int64_t>(p->num_experts) * p->expert_cap
@@ -360,15 +417,15 @@ moe_status moe_workspace_plan(const moe_problem* p, moe_workspace_layout* L) {
   L->expert_offsets = take((E + 1) * 4);
   L->row_to_pair = take(R * 4);
   L->pair_to_row = take(P * 4);
-  L->xq = take(T * H);
+  L->xq = take(code_bytes(p->scale_fmt, T * H));
   L->xs = take((H / 128) * T * sb);
   L->c1 = take(R * 2 * I * 2);
-  L->hq = take(R * I);
+  L->hq = take(code_bytes(p->scale_fmt, R * I));
   L->hs = take((I / 128) * R * sb);
   L->y = take(R * H * 2);
   // The decode path serves the aligned layout; MXFP4 weights take only its
   // one-launch layer, whose stages need H and I multiples of 256.
-  const bool decode = !batched && moe::down_combine_fits(p->t_cap, p->topk, p->inter) &&
+  const bool decode = !batched && !mx && moe::down_combine_fits(p->t_cap, p->topk, p->inter) &&
                       (p->weight_fmt == MOE_WEIGHT_E4M3 ||
                        moe::decode_layer_fits_fmt(p->t_cap, p->topk, p->hidden, p->inter, p->weight_fmt));
   L->act = decode ? take(R * I * 4) : 0;
@@ -505,6 +562,10 @@ static moe_status forward_impl(const moe_problem* p, const moe_workspace_layout&
   if (!t || !workspace) return MOE_ERR_INVALID_ARG;
   if (p->t_cap > 0 && (!t->x || !t->topk_ids || !t->topk_w || !t->w1 || !t->w1_scales ||
                        !t->w2 || !t->w2_scales || !t->out))
+    return MOE_ERR_INVALID_ARG;
+  if (p->t_cap > 0 && p->scale_fmt == MOE_SCALE_MXFP4 &&
+      !(aligned(t->x, 16) && aligned(t->w1, 16) && aligned(t->w2, 16) && aligned(t->w1_scales, 4) &&
+        aligned(t->w2_scales, 4) && aligned(t->out, 16) && aligned(workspace, 16)))
     return MOE_ERR_INVALID_ARG;
   if (p->t_cap == 0) return MOE_OK;
 

@@ -12,6 +12,7 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kGroup = 128;  // activation quantization group and weight block edge
+constexpr int kMxBlock = 32;  // columns per E8M0 scale of an MXFP4 tensor
 
 // ---- BF16 -----------------------------------------------------------------
 
@@ -27,7 +28,9 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
 
 // ---- activation scale (vLLM PR #65794, Details: max(amax/448, 1/(448*512))) ----
 
-enum ScaleFmt : int { kFp32 = 0, kFp32Pow2 = 1, kUe8m0 = 2 };
+// kMxfp4: not an FP8 scale but 4-bit activations (mx_device.h), E2M1 codes with
+// an E8M0 byte per 32 columns, both row-major.
+enum ScaleFmt : int { kFp32 = 0, kFp32Pow2 = 1, kUe8m0 = 2, kMxfp4 = 4 };
 
 // Rounding conventions of the quantizers. kDivide: the rule above, scale =
 // max(fl32(amax/448), fl32(1/229376)) and codes from fl32(x / scale).

@@ -486,6 +486,7 @@ static hipError_t launch_w4(const W4Args& g, bool large, hipStream_t stream) {
 }
 
 hipError_t launch_grouped_gemm_w4(const W4Args& g, hipStream_t stream) {
+  if (g.fmt == kMxfp4) return launch_grouped_gemm_a4(g, stream);
   // The tiled kernel only when some expert can hold more than kW4SmallMax rows.
   const bool large = g.max_rows_per_expert > kW4SmallMax;
   const bool u = g.fmt == kUe8m0, m = g.a_row_map != nullptr;

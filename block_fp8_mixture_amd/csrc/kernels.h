@@ -97,7 +97,6 @@ bool launch_tiled_w4(const GemmArgs& g, hipStream_t stream, hipError_t* err);
 // The grouped GEMM with MXFP4 weights: w [num_experts, n, k/2] packed E2M1
 // codes (the even K element in the low nibble), w_scales [num_experts, n,
 // k/32] E8M0 bytes; everything else as GemmArgs.
-constexpr int kMxBlock = 32;  // weights per E8M0 scale along K
 enum WeightFmt : int { kWeightE4m3 = 0, kWeightMxfp4 = 1 };  // the values of moe_weight_fmt
 struct W4Args {
   const uint8_t* a;
@@ -119,6 +118,39 @@ struct W4Args {
   uint16_t* c;
 };
 hipError_t launch_grouped_gemm_w4(const W4Args& g, hipStream_t stream);
+
+// The same product with MXFP4 activations (fmt kMxfp4): a [a_rows, k/2] codes
+// and a_scales [a_rows, k/32] E8M0 bytes. Called by launch_grouped_gemm_w4.
+hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream);
+
+// BF16 values of an MXFP4 tensor of rows x cols.
+hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                                uint16_t* out, hipStream_t stream);
+
+// Top-k routing from router logits (the fields as moe_router's and
+// moe_route's in the C ABI).
+enum Score : int { kSoftmax = 0, kSigmoid = 1 };
+enum LogitType : int { kLogitF32 = 0, kLogitBf16 = 1, kLogitF16 = 2 };
+constexpr int kMaxGroups = 64;
+struct RouteArgs {
+  const void* logits;
+  int logit_type;
+  int64_t ld;              // elements between rows
+  const float* bias;       // [num_experts] or nullptr
+  int num_experts;
+  int topk;
+  int score;
+  int renormalize;
+  float scale;
+  int num_groups;
+  int top_groups;
+  int group_top;
+  int t_cap;
+  const int32_t* t_live_dev;
+  int32_t* ids;            // [t_cap, topk]
+  float* weights;          // [t_cap, topk]
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 
 // FC2 and the top-k combine of a decode-sized layer in one launch: a
 // workgroup owns 16 output columns of every live expert. Limits of its LDS

@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "gemm_device.h"
 #include "kernels.h"
 #include "quant_device.h"
 
@@ -97,6 +98,14 @@ __global__ __launch_bounds__(kSmqThreads) void silu_mul_quant_kernel(
 #pragma unroll
           for (int i = 0; i < 8; ++i) y.v[i] = round_bf16(y.v[i]);
         }
+        if constexpr (FMT == kMxfp4) {  // four 32-column blocks, four lanes each
+          uint32_t byte;
+          const uint32_t codes = mx_quantize8_f32(y.v, &byte);
+          const int64_t at = static_cast<int64_t>(r) * inter + gs[k] * kGroup + l16 * 8;
+          *reinterpret_cast<uint32_t*>(hq + at / 2) = codes;
+          if ((l16 & 3) == 0) static_cast<uint8_t*>(hs)[at / kMxBlock] = static_cast<uint8_t>(byte);
+          continue;
+        }
         float sc;
         const uint2 codes = quantize8<FMT>(y, &sc, rnd);
         *reinterpret_cast<uint2*>(hq + static_cast<int64_t>(r) * inter + gs[k] * kGroup + l16 * 8) = codes;
@@ -110,6 +119,39 @@ __global__ __launch_bounds__(kSmqThreads) void silu_mul_quant_kernel(
     run(std::true_type{});
   } else {
     run(std::false_type{});
+  }
+}
+
+// The BF16 values of an MXFP4 tensor: 16 columns per thread, an 8-byte load of
+// codes and a 32-byte store. Every value of the format with a scale byte up to
+// 251 is a BF16 value (2 significant bits; 0.5 x 2^-127 is a BF16 subnormal);
+// what lies past BF16's largest becomes infinity.
+__global__ __launch_bounds__(kThreads) void mxfp4_dequant_kernel(const uint8_t* __restrict__ codes,
+                                                                 const uint8_t* __restrict__ scales,
+                                                                 int64_t chunks, uint16_t* __restrict__ out) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < chunks; i += stride) {
+    const uint2 c = *reinterpret_cast<const uint2*>(codes + 8 * i);
+    const uint32_t byte = scales[i >> 1];
+    const float s = byte == 255u ? __uint_as_float(0x7FC00000u) : mx_scale_float(byte);
+    uint4 o[2];
+    uint32_t* w = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = ((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xFFu;
+      float v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t n = h ? b >> 4 : b & 15u;
+        // E2M1 magnitudes times two are 0, 1, 2, 3, 4, 6, 8, 12.
+        const float m = static_cast<float>((0xC8643210u >> (4 * (n & 7u))) & 15u);
+        v[h] = __builtin_copysignf(m * 0.5f, n & 8u ? -1.0f : 1.0f) * s;
+      }
+      const uint2 p = pack_bf16x4(v4f{v[0], v[1], 0.0f, 0.0f});
+      w[j] = p.x;
+    }
+    reinterpret_cast<uint4*>(out)[2 * i] = o[0];
+    reinterpret_cast<uint4*>(out)[2 * i + 1] = o[1];
   }
 }
 
@@ -167,6 +209,7 @@ hipError_t launch_act_quant(const uint16_t* x, int t_cap, const int32_t* t_live_
     case kFp32: return act_quant_fmt<kFp32>(x, t_cap, t_live_dev, hidden, xq, xs, rounding, stream);
     case kFp32Pow2:
       return act_quant_fmt<kFp32Pow2>(x, t_cap, t_live_dev, hidden, xq, xs, rounding, stream);
+    case kMxfp4: return act_quant_fmt<kMxfp4>(x, t_cap, t_live_dev, hidden, xq, xs, rounding, stream);
     default: return act_quant_fmt<kUe8m0>(x, t_cap, t_live_dev, hidden, xq, xs, rounding, stream);
   }
 }
@@ -183,10 +226,23 @@ hipError_t launch_silu_mul_quant(const uint16_t* gate_up, int inter, const int32
     case kFp32Pow2:
       return smq_fmt<kFp32Pow2>(gate_up, inter, counts, offsets, num_experts, row_cap, act,
                                 clamp_limit, hq, hs, rnd, seg_cap, stream);
+    case kMxfp4:
+      return smq_fmt<kMxfp4>(gate_up, inter, counts, offsets, num_experts, row_cap, act,
+                             clamp_limit, hq, hs, rnd, seg_cap, stream);
     default:
       return smq_fmt<kUe8m0>(gate_up, inter, counts, offsets, num_experts, row_cap, act,
                              clamp_limit, hq, hs, rnd, seg_cap, stream);
   }
+}
+
+hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                                uint16_t* out, hipStream_t stream) {
+  const int64_t chunks = rows * (cols / 16);
+  const int64_t need = (chunks + kThreads - 1) / kThreads;
+  const int64_t cap = static_cast<int64_t>(device_cu_count()) * 16;
+  hipLaunchKernelGGL(mxfp4_dequant_kernel, dim3(static_cast<unsigned>(need < cap ? need : cap)),
+                     dim3(kThreads), 0, stream, codes, scales, chunks, out);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -8,6 +8,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "mx_device.h"
 
 namespace moe {
 
@@ -47,7 +48,8 @@ __device__ __forceinline__ uint2 quantize8(const Vals8& x, float* scale_out, int
 }
 
 // Quantizes group gid (token gid / (hidden / 128), group gid % (hidden / 128))
-// of x with the 16 lanes l16 = 0..15 that call it. Groups past t_cap exit;
+// of x with the 16 lanes l16 = 0..15 that call it (MXFP4: the four 32-column
+// blocks of the group, four lanes each). Groups past t_cap exit;
 // groups of tokens past the live count are not written.
 template <int FMT>
 __device__ __forceinline__ void act_quant_group(const uint16_t* __restrict__ x, int t_cap,
@@ -63,6 +65,13 @@ __device__ __forceinline__ void act_quant_group(const uint16_t* __restrict__ x, 
   // issued together with the live-count load instead of after it.
   const uint4 raw = *reinterpret_cast<const uint4*>(x + base);
   if (t >= clamp_live(t_live_dev, t_cap)) return;
+  if constexpr (FMT == kMxfp4) {
+    uint32_t byte;
+    const uint32_t codes = mx_quantize8_bf16(raw, &byte);
+    *reinterpret_cast<uint32_t*>(xq + base / 2) = codes;
+    if ((l16 & 3) == 0) static_cast<uint8_t*>(xs)[base / kMxBlock] = static_cast<uint8_t>(byte);
+    return;
+  }
   const Vals8 v = unpack_bf16x8(raw);
   float s;
   const uint2 codes = quantize8<FMT>(v, &s, rnd);

@@ -6,6 +6,7 @@
  * Purpose and SM100-on-B200 sections; TensorRT-LLM PR #21250 "Triton
  * FP8-activation MoE for decode-sized batches on Hopper", description):
  *
+ *   moe_route          router logits -> top-k expert ids and weights
  *   moe_align          top-k routing -> per-expert contiguous rows, prefix-sum endpoints
  *   moe_act_quant      BF16 tokens -> FP8 E4M3 codes + one scale per 1x128 group
  *   moe_grouped_gemm_fp8  FP8 x FP8 grouped GEMM with 128x128 fp32 weight block
@@ -30,6 +31,10 @@
  *   g lives at index g * ld + r, where ld is the row capacity of that buffer.
  *   MOE_SCALE_FP32 and MOE_SCALE_FP32_POW2 store float; MOE_SCALE_UE8M0
  *   stores one uint8_t biased exponent (scale = 2^(byte - 127)).
+ * - MOE_SCALE_MXFP4 selects 4-bit activations instead of FP8 ones: the codes
+ *   are E2M1, two per byte with the even column in the low nibble, [rows,
+ *   cols/2], and the scales E8M0 bytes per 32 columns, row-major [rows,
+ *   cols/32]: the layout of MXFP4 weights (moe_weight_fmt).
  * - The live token count may live on the device (`t_live_dev`, one int32),
  *   so a captured graph can replay with a different count. It is clamped to
  *   [0, t_cap]; NULL means t_cap.
@@ -58,11 +63,24 @@ typedef enum {
 
 /* Activation scale formats (vLLM PR #59128, Purpose: packed UE8M0 on one
  * architecture, plain or power-of-two-rounded fp32 on the other; vLLM PR
- * #65794, Overview). Power-of-two rounding rounds up. */
+ * #65794, Overview). Power-of-two rounding rounds up.
+ *
+ * MOE_SCALE_MXFP4 is the format of 4-bit activations (OCP Microscaling v1.0,
+ * MXFP4). A block of 32 consecutive columns with largest magnitude amax has
+ * the scale byte max(floor(log2(amax)) - 2 + 127, 0), and its values x become
+ * the E2M1 magnitude (0, 0.5, 1, 1.5, 2, 3, 4, 6) nearest to |x| / 2^(byte -
+ * 127), ties to the even code, saturating at 6, with x's sign (zeros too). A
+ * block that holds an infinity or a NaN gets byte 255 (the format's NaN) and
+ * zero codes, so that every product with it is NaN. The scale is a power of
+ * two and the division exact: both roundings below give the same codes, and
+ * MOE_ROUND_RECIPROCAL only rounds the SwiGLU output to BF16 first. Taken by
+ * moe_act_quant, moe_silu_mul_quant(_masked), moe_grouped_gemm_mxfp4 and,
+ * with MXFP4 weights, moe_forward; the FP8-weight GEMMs return UNSUPPORTED. */
 typedef enum {
   MOE_SCALE_FP32 = 0,
   MOE_SCALE_FP32_POW2 = 1,
-  MOE_SCALE_UE8M0 = 2
+  MOE_SCALE_UE8M0 = 2,
+  MOE_SCALE_MXFP4 = 4
 } moe_scale_fmt;
 
 /* Rounding conventions of the FP8 quantizers.
@@ -113,6 +131,58 @@ typedef enum {
   MOE_ACT_SWIGLU_CLAMP = 1,
   MOE_ACT_SWIGLU_CLAMP_AFTER_SILU = 2
 } moe_act;
+
+/* Scores of the router (moe_route). */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* exp(l_e - max) / sum over all experts */
+  MOE_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-l_e)) */
+} moe_score;
+
+typedef enum {
+  MOE_LOGIT_FP32 = 0,
+  MOE_LOGIT_BF16 = 1,
+  MOE_LOGIT_FP16 = 2
+} moe_logit_type;
+
+typedef struct {
+  int32_t num_experts;  /* 1 .. 1024 */
+  int32_t topk;         /* 1 .. 64, at most the experts that top_groups groups hold */
+  moe_score score;
+  int32_t renormalize;  /* nonzero: the picked weights are divided by their sum */
+  float scale;          /* multiplies the weights, finite */
+  int32_t num_groups;   /* expert groups, 1 .. 64, dividing num_experts (1: none) */
+  int32_t top_groups;   /* groups whose experts may be picked, 1 .. num_groups */
+  int32_t group_top;    /* 1 or 2: a group's value is its best expert's selection
+                           value or the sum of its best two (of one, if one can be picked) */
+} moe_router;
+
+/* Top-k routing from router logits: what moe_align and moe_forward take as
+ * topk_ids and topk_w. Per live token, with l the logits and s the scores:
+ *   - experts are ordered by their selection value, larger first, ties to the
+ *     lower index: l_e without a bias, s_e + bias_e with one (in a group's
+ *     value with group_top = 2 and no bias: s_e);
+ *   - with num_groups > 1 (num_experts / num_groups consecutive experts
+ *     each), only experts of the top_groups groups of largest value are
+ *     candidates, ties to the lower group;
+ *   - topk_ids[t] are the topk best candidates in that order, topk_w[t] their
+ *     scores (without the bias), divided by their sum if renormalize (zeros
+ *     if it is zero), times scale.
+ * An expert whose logit is -infinity or NaN, or whose selection value is, is
+ * never picked; a NaN logit counts as -infinity in the softmax, and a logit of
+ * +infinity as the largest finite float. Places that no expert fills hold id
+ * -1, which moe_align drops, and weight 0. Scores, the order with a bias and
+ * the weights are evaluated in double, the weights rounded once.
+ *
+ *   logits    device [t_cap, num_experts] of `type`, rows `ld` elements apart
+ *   bias      device float [num_experts] or NULL
+ *   topk_ids  device int32 [t_cap, topk]; rows t >= t_live untouched
+ *   topk_w    device float [t_cap, topk]; rows t >= t_live untouched
+ * Errors: INVALID_ARG (sizes, null pointers, unknown enum values, ld <
+ * num_experts), UNSUPPORTED (num_experts above 1024, topk or num_groups above
+ * 64). */
+moe_status moe_route(const moe_router* r, const void* logits, moe_logit_type type, int64_t ld,
+                     const float* bias, int32_t t_cap, const int32_t* t_live_dev, int32_t* topk_ids,
+                     float* topk_w, void* stream);
 
 /* Smallest row capacity that holds any routing of t_cap tokens with top-k:
  * with P = t_cap * topk pairs and n = min(num_experts, P) experts in use,
@@ -184,11 +254,25 @@ moe_status moe_align_batched(const int32_t* topk_ids, int32_t t_cap, const int32
  *   xq    device uint8 [t_cap, hidden]; rows t >= t_live untouched
  *   xs    device scales [hidden/128][t_cap] (float or uint8, per `fmt`)
  *   rounding  the quantizer's convention (moe_rounding)
+ * MOE_SCALE_MXFP4: xq uint8 [t_cap, hidden/2], xs uint8 [t_cap, hidden/32].
+ * It also quantizes weights: BF16 [rows, K] to an MXFP4 expert's codes and
+ * scale bytes.
  * Errors: INVALID_ARG (hidden not a positive multiple of 128, null pointers,
  * unknown fmt or rounding). */
 moe_status moe_act_quant(const uint16_t* x, int32_t t_cap, const int32_t* t_live_dev,
                          int32_t hidden, moe_scale_fmt fmt, moe_rounding rounding, uint8_t* xq,
                          void* xs, void* stream);
+
+/* The BF16 values of an MXFP4 tensor (activations or weights): out[r, c] =
+ * e2m1(code of column c of row r) * 2^(scales[r, c/32] - 127), NaN under scale
+ * byte 255. Exact up to scale byte 251; beyond BF16's range, infinity.
+ *   codes   device uint8 [rows, cols/2], 8-byte aligned
+ *   scales  device uint8 [rows, cols/32]
+ *   out     device BF16 [rows, cols], 16-byte aligned
+ * Errors: INVALID_ARG (rows < 0, cols not a positive multiple of 32, null or
+ * misaligned pointers). */
+moe_status moe_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                             uint16_t* out, void* stream);
 
 /* Grouped FP8 x FP8 GEMM with per-block scales, over the live rows of every
  * expert segment only (vLLM PR #59128, Purpose and SM90-on-H200: both grouped
@@ -235,15 +319,20 @@ moe_status moe_grouped_gemm_fp8_masked(const uint8_t* a, const void* a_scales, m
                                        int32_t expert_cap, int32_t n, int32_t k, uint16_t* c,
                                        int32_t* tiles_visited, void* stream);
 
-/* Grouped GEMM with FP8 E4M3 activations and MXFP4 weights (vLLM PR #59128,
- * description: FP4 weights on the same prefix-sum expert endpoints; the
- * format is MOE_WEIGHT_MXFP4's). For every expert e and live row r:
+/* Grouped GEMM with FP8 E4M3 or MXFP4 activations and MXFP4 weights (vLLM PR
+ * #59128, description: FP4 weights on the same prefix-sum expert endpoints;
+ * the format is MOE_WEIGHT_MXFP4's). For every expert e and live row r:
  *   C[r, n] = bf16( sum_kb sa[kb, ar] * sum_{j<128} A[ar, kb*128+j] * w(e, n, kb*128+j) )
  *   w(e, n, k) = e2m1(code of column k of row n) * 2^(w_scales[e, n, k/32] - 127)
  * with ar as in moe_grouped_gemm_fp8, accumulated in fp32 (the weight scales
  * applied inside the matrix cores, the activation scale once per 128-wide
  * block; with UE8M0 activation scales the matrix cores apply both) and
  * rounded to nearest even BF16.
+ *
+ * With fmt MOE_SCALE_MXFP4 A is an MXFP4 tensor (a [a_rows, k/2], a_scales
+ * [a_rows, k/32]), and the matrix cores apply both operands' scales:
+ *   C[r, n] = bf16( sum_j a(ar, j) * w(e, n, j) ), accumulated in fp32.
+ * a, w and c are then 16-byte aligned and the scales 4-byte aligned.
  *
  *   a, a_scales, fmt, a_rows, a_row_map, a_row_div   as moe_grouped_gemm_fp8
  *   w          device uint8 [num_experts, n, k/2] packed E2M1 codes
@@ -290,6 +379,7 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a, const void* a_scales, moe_sc
  *   clamp_limit  used by the clamp variants; must be > 0 there
  *   rounding  moe_rounding; MOE_ROUND_RECIPROCAL rounds SiLU(gate)*up to BF16
  *             before quantizing it
+ * MOE_SCALE_MXFP4: hq uint8 [row_cap, inter/2], hs uint8 [row_cap, inter/32].
  * Errors: INVALID_ARG (also when row_cap * inter / 128 exceeds 2^31 - 1). */
 moe_status moe_silu_mul_quant(const uint16_t* gate_up, int32_t inter,
                               const int32_t* expert_counts, const int32_t* expert_offsets,
@@ -369,11 +459,11 @@ typedef struct {
   size_t expert_offsets; /* int32 [E+1] */
   size_t row_to_pair;    /* int32 [row_cap] */
   size_t pair_to_row;    /* int32 [t_cap*topk] */
-  size_t xq;             /* uint8 [t_cap, H] */
-  size_t xs;             /* scales [H/128][t_cap] */
+  size_t xq;             /* uint8 [t_cap, H] (MXFP4: [t_cap, H/2]) */
+  size_t xs;             /* scales [H/128][t_cap] (MXFP4: bytes [t_cap, H/32]) */
   size_t c1;             /* BF16 [row_cap, 2I] */
-  size_t hq;             /* uint8 [row_cap, I] */
-  size_t hs;             /* scales [I/128][row_cap] */
+  size_t hq;             /* uint8 [row_cap, I] (MXFP4: [row_cap, I/2]) */
+  size_t hs;             /* scales [I/128][row_cap] (MXFP4: bytes [row_cap, I/32]) */
   size_t y;              /* BF16 [row_cap, H] */
   size_t act;            /* fp32 [row_cap, I] SiLU(gate)*up before quantization; laid out
                             only on the decode path (t_cap*topk <= 64 and the quantized
@@ -437,6 +527,10 @@ size_t moe_workspace_bytes(const moe_problem* p);
  * FC1 of moe_fc1_decode, then FC2 with the top-k combine. The workspace then
  * holds the same alignment, codes and scales, bit for bit, and FC1/FC2 rows
  * within the GEMM tolerance.
+ * With scale_fmt MOE_SCALE_MXFP4 (weight_fmt must be MOE_WEIGHT_MXFP4, else
+ * UNSUPPORTED) both activation quantizations are MXFP4 and both GEMMs
+ * moe_grouped_gemm_mxfp4's with MXFP4 activations; x, w1, w2, out and the
+ * workspace are then 16-byte aligned and the weight scales 4-byte aligned.
  * `workspace` is device memory of at least moe_workspace_bytes(p) bytes, laid
  * out as moe_workspace_plan describes; its prior contents do not matter.
  * Errors: INVALID_ARG, CAPACITY (workspace or row_cap too small), HIP. */

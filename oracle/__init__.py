@@ -38,6 +38,7 @@ from .align import align, align_batched
 from .moe import (ACTS, MX_BLOCK, WEIGHT_FMTS, combine, forward, gemm_rows_mxfp4,
                   grouped_gemm, mxfp4_dequant, silu_mul_quant, swiglu, token_forward,
                   unquantized_reference)
+from .mx4 import gemm_rows_mx4, mxfp4_quantize, route, token_forward_mx4
 
 __all__ = [
     "E4M3_MAX", "bf16_bits_to_f64", "bf16_from_f64", "e2m1_decode", "e4m3_decode",
@@ -46,4 +47,5 @@ __all__ = [
     "reciprocal_multiplier",
     "scales_to_f64", "align", "align_batched", "ACTS", "combine", "forward", "grouped_gemm",
     "silu_mul_quant", "swiglu", "token_forward", "unquantized_reference",
+    "gemm_rows_mx4", "mxfp4_quantize", "route", "token_forward_mx4",
 ]
