@@ -280,6 +280,9 @@ GEMMS = [
     ([0, 0, 0], 128, 128, 16),
     ([600, 1, 300], 640, 512, 16),
     ([3] * 40, 128, 2048, 1),
+    ([65, 0, 2], 128, 128, 16),
+    ([256, 257, 129], 896, 1536, 1),
+    ([128, 300], 384, 2176, 16),
 ]
 
 
