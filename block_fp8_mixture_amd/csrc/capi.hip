@@ -623,6 +623,7 @@ static moe_status forward_impl(const moe_problem* p, const moe_workspace_layout&
     w.seg_cap = 0;  // the batched layout's offsets are e * cap, written by the alignment
     w.num_experts = p->num_experts;
     w.row_cap = R;
+    w.max_rows = pairs < R ? pairs : R;
     w.max_rows_per_expert = pairs < R ? pairs : R;
     if (p->expert_cap > 0 && p->expert_cap < w.max_rows_per_expert) w.max_rows_per_expert = p->expert_cap;
     if (e == hipSuccess) {

@@ -11,6 +11,7 @@
 // instruction's 128, g = l / 16, in 16 bytes, the even value in the low
 // nibble, with that block's byte as its scale; the result's lane l holds
 // token l % 16 and weight rows 4 (l / 16) + v.
+#include <cmath>
 #include <type_traits>
 
 #include "device_common.h"
@@ -25,7 +26,6 @@ constexpr int kA4Waves = kA4Threads / 64;
 constexpr int kA4TileM = 64;  // token rows of a wave task, four 16-row tiles
 constexpr int kA4Tiles = kA4TileM / 16;
 constexpr int kA4TileN = 32;  // weight rows of a wave task, two 16-row tiles
-constexpr int kA4Small = 64;  // experts with more rows go to the tiled kernel
 
 __device__ __forceinline__ int a4_seg_start(const W4Args& p, int e) {
   return p.seg_cap > 0 ? e * p.seg_cap : p.offsets[e];
@@ -36,20 +36,17 @@ __device__ __forceinline__ int a4_rows(const W4Args& p, int e) {
   return segment_rows(s0, s1, p.counts[e], p.row_cap);
 }
 
-// Exclusive prefix over the experts of ceil(rows / M), into s_pref[0..E], for
-// the experts of more than kA4Small rows or (not LARGE) at most `most`; all
+// Exclusive prefix over the experts of units(e), into s_pref[0..E]; all
 // threads of the workgroup call it.
-template <int M, bool LARGE>
-__device__ void a4_prefix(const W4Args& p, int* s_pref, int* s_wsum, int most = INT32_MAX) {
+template <typename Units>
+__device__ void a4_prefix(int E, Units units, int* s_pref, int* s_wsum) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int E = p.num_experts;
   constexpr int kPer = (kMaxExperts + kA4Threads - 1) / kA4Threads;
   int tiles[kPer], run = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = tid * kPer + i;
-    const int rows = e < E ? a4_rows(p, e) : 0;
-    tiles[i] = (LARGE ? rows > kA4Small : rows <= most) ? (rows + M - 1) / M : 0;
+    tiles[i] = e < E ? units(e) : 0;
     run += tiles[i];
   }
   int incl = run;
@@ -98,7 +95,6 @@ __device__ __forceinline__ v4f mfma_a4(uint4 w, uint32_t ws, uint4 x, uint32_t x
 // operands go from global memory straight into the MFMA registers. The S
 // waves of a K split add their partial sums in LDS in wave order, so the
 // result does not depend on which finishes first.
-template <bool SMALL_ONLY>
 __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
   __shared__ int s_pref[kMaxExperts + 1];
   __shared__ int s_wsum[kA4Waves];
@@ -106,7 +102,7 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r16 = lane & 15, g = lane >> 4;
   const int E = p.num_experts, N = p.n, K = p.k, KB = K / kGroup;
-  a4_prefix<kA4TileM, false>(p, s_pref, s_wsum, SMALL_ONLY ? kA4Small : INT32_MAX);
+  a4_prefix(E, [&](int e) { return (a4_rows(p, e) + kA4TileM - 1) / kA4TileM; }, s_pref, s_wsum);
   const int nt = N / kA4TileN;
   const int tasks = s_pref[E] * nt;
   if (tasks == 0) return;
@@ -211,34 +207,50 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
 // Four waves, one per SIMD, as 2 (tokens) x 2 (weights): each owns a TM/2 x
 // TN/2 piece, 32 x 32 MFMA tiles whose accumulators stay in registers for the
 // whole K (both scales are applied in the matrix cores, so nothing rescales
-// them). A stage is 128 K values of the tile's rows, 64 bytes each, fetched by
-// direct-to-LDS loads three stages ahead into a ring of four; 16-byte chunk c
-// of row r sits at slot c ^ ((r >> 2) & 3), so the 16 lanes one ds_read_b128
-// cycle serves (16 rows, the same chunk) hit distinct banks.
+// them).
 //
-// Stage s runs as two halves of one 64-wide K step each: half 0 issues the
-// loads of stage s + 3 and reads half 1's fragments while its MFMAs run; then
-// a wait for this wave's loads of stage s + 1 and the stage's only barrier;
-// half 1 reads the next stage's first fragments under its own MFMAs. The
-// slot that stage s + 3 goes to held stage s - 1, whose last reads returned
-// before the barrier of stage s - 1.
+// A stage is 256 K values of the tile's rows: 128 bytes of each, one whole
+// cache line per request (with half lines the same bytes took 1.2 times as
+// long: the L2 answers requests, not bytes). Direct-to-LDS loads bring it into
+// one of two buffers per operand; 16-byte chunk c of row r sits at slot c ^
+// ((r >> 1) & 7), so the 16 lanes one ds_read_b128 cycle serves (16 rows, the
+// same chunk) hit distinct banks. A stage runs as four quarters q of one
+// 64-wide K step each, NI x MI MFMAs, under which the next fragments are read:
+//   q = 0: the stage's remaining token fragments (held in registers from here
+//          on) and the weights' of q = 1; barrier: the token buffer is free
+//   q = 1: loads of the tokens of stage s + 2
+//   q = 2: wait for this wave's loads of stage s + 1; barrier: they are there,
+//          and the weight buffer is free
+//   q = 3: the first fragments of stage s + 1; loads of the weights of s + 2
+// (and in each the weights' fragments of the next quarter).
 //
-// Scales: with K a multiple of 512 (WIDE) a row's 16 bytes of four stages are
-// fetched at once into s_sc and held in registers for those stages; otherwise
-// each stage brings its rows' 4 bytes.
+// The grid is persistent and the stream of stages goes on across tiles: the
+// last two stages of a tile issue the next tile's first two, which land while
+// its output is stored. Row sources of a tile are looked up two tiles ahead,
+// during the output. A tile's stages are rounded up to an even number; K values past
+// the end multiply zero codes.
+//
+// Scales: with K a multiple of 1024 (G = 4) a row's bytes of four stages are
+// fetched at once, as two 16-byte loads of one line, with K a multiple of 512
+// (G = 2) those of two stages, and held in registers two stages at a time;
+// otherwise (G = 1) each stage brings its rows' bytes by two 4-byte loads.
+//
+// Row tiles of an expert run fastest, so that neighbours share a weight slab.
 constexpr int kA4TThreads = 256;
+constexpr int kA4TileCols = 256;
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-__device__ __forceinline__ v16f mfma_a4_32(uint4 w, uint4 x, v16f acc, uint32_t ws, uint32_t xs, std::false_type) {
+// One 64-wide K step: the first of its 128-wide block takes byte 0 of the
+// scale words, the second byte 2.
+template <bool SECOND>
+__device__ __forceinline__ v16f mfma_a4_32(uint4 w, uint4 x, v16f acc, uint32_t ws, uint32_t xs) {
   const v8i a = {static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w), 0, 0, 0, 0};
   const v8i b = {static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z), static_cast<int>(x.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, 0, static_cast<int>(ws), 0, static_cast<int>(xs));
-}
-__device__ __forceinline__ v16f mfma_a4_32(uint4 w, uint4 x, v16f acc, uint32_t ws, uint32_t xs, std::true_type) {
-  const v8i a = {static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z), static_cast<int>(w.w), 0, 0, 0, 0};
-  const v8i b = {static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z), static_cast<int>(x.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, 2, static_cast<int>(ws), 2, static_cast<int>(xs));
+  if constexpr (SECOND)
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, 2, static_cast<int>(ws), 2, static_cast<int>(xs));
+  else
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, 4, 0, static_cast<int>(ws), 0, static_cast<int>(xs));
 }
 
 // Direct-to-LDS loads: lane l's bytes land at dst + l * 16 (4).
@@ -249,283 +261,427 @@ __device__ __forceinline__ void load_lds4(const uint8_t* src, void* dst) {
   __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 4, 0, 0);
 }
 
-template <int TM, int TN, bool WIDE>
+constexpr int lp_or_one(int v) { return v > 0 ? v : 1; }
+
+struct A4Tile {
+  int e, n0, row0, rows;  // rows = 0: no tile
+};
+
+template <int TM, int TN, int G>
 __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p) {
   constexpr int MI = TM / 64, NI = TN / 64;   // 32-row MFMA tiles of a wave: tokens, weights
-  constexpr int ROWS = TM + TN;               // weight rows first
-  constexpr int NL = ROWS / 64;               // code loads per wave and stage
-  constexpr int NLW = TN / 64;                //   of them weights
-  constexpr int SL = ROWS / 256;              // scale loads per wave (a group of stages, or a stage)
-  constexpr int kStage = ROWS * 64;
-  static_assert(ROWS % 256 == 0 || ROWS % 128 == 0, "");
-  __shared__ __attribute__((aligned(1024))) uint8_t s_st0[kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_st1[kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_st2[kStage];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_st3[kStage];
-  __shared__ __attribute__((aligned(1024))) uint32_t s_sc0[WIDE ? ROWS * 4 : ROWS];
-  __shared__ __attribute__((aligned(1024))) uint32_t s_sc1[WIDE ? 1 : ROWS];
-  __shared__ __attribute__((aligned(1024))) uint32_t s_sc2[WIDE ? 1 : ROWS];
-  __shared__ __attribute__((aligned(1024))) uint32_t s_sc3[WIDE ? 1 : ROWS];
-  __shared__ int s_pref[kMaxExperts + 1];
+  constexpr int M = MI * NI;
+  constexpr bool WIDE = G > 1;
+  constexpr int U = G == 4 ? 4 : 2;           // stages per loop iteration
+  constexpr int WL = TN / 32, XL = TM / 32;   // code loads per wave and stage
+  constexpr int kScRows = TN + 256;           // rows of scales (weight rows first; all lanes load)
+  static_assert(TN + TM <= kScRows, "");
+  static_assert(TM <= kA4TThreads, "one row source per thread");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_w0[TN * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_w1[TN * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_x0[TM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_x1[TM * 128];
+  // The rows' 16 bytes of two stages (G = 4: and of the next two); G = 1: 4 and
+  // 4 bytes of a stage, per buffer.
+  __shared__ __attribute__((aligned(1024))) uint32_t s_sc0[kScRows * (WIDE ? 2 * G : 2)];
+  __shared__ __attribute__((aligned(1024))) uint32_t s_sc1[WIDE ? 1 : kScRows * 2];
+  __shared__ int s_pref[kMaxExperts + 1];  // exclusive prefix of the row tiles over the experts
+  __shared__ int s_row0[kMaxExperts];      // an expert's first row
+  __shared__ int s_rows[kMaxExperts];      //   and its rows
   __shared__ int s_wsum[kA4Waves];
-  __shared__ int s_src[TM];
+  __shared__ int s_src[3][TM];             // source rows of tile i at [i % 3]
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int r32 = lane & 31, h = lane >> 5;
-  const int E = p.num_experts, N = p.n, K = p.k, KB = K / kGroup;
+  const int E = p.num_experts, N = p.n, K = p.k;
+  const int P = (K + 255) / 256;  // stages with data
+  const int P2 = (P + 1) & ~1;
   const int ntn = (N + TN - 1) / TN;
-  a4_prefix<TM, true>(p, s_pref, s_wsum);
+  for (int e = tid; e < E; e += kA4TThreads) {
+    s_rows[e] = a4_rows(p, e);
+    s_row0[e] = a4_seg_start(p, e);
+  }
+  __syncthreads();
+  a4_prefix(E, [&](int e) { return (s_rows[e] + TM - 1) / TM; }, s_pref, s_wsum);
   const int total = s_pref[E] * ntn;
 
-  for (int t0 = blockIdx.x; t0 < total; t0 += gridDim.x) {
-    const int tile = t0;
-    // Row tiles of an expert fastest: neighbouring tiles share a weight slab.
-    int e, mt, n0;
-    {
-      int lo = 0, hi = E - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_pref[mid] * ntn <= tile) lo = mid; else hi = mid - 1;
-      }
-      e = lo;
-      const int local = tile - s_pref[e] * ntn;
-      const int mtiles = s_pref[e + 1] - s_pref[e];
-      n0 = (local / mtiles) * TN;
-      mt = local % mtiles;
+  auto locate = [&](int tile) {
+    A4Tile t{0, 0, 0, 0};
+    if (tile >= total) return t;
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pref[mid] * ntn <= tile) lo = mid; else hi = mid - 1;
     }
-    const int rows_here = min(TM, a4_rows(p, e) - mt * TM);
-    const int row0 = a4_seg_start(p, e) + mt * TM;
-    __syncthreads();  // the previous tile is done with s_src and the stages
-    for (int i = tid; i < TM; i += kA4TThreads) {
-      int src = -1;
-      if (i < rows_here) {
-        const int r = row0 + i;
-        src = p.a_row_map ? p.a_row_map[r] / p.a_row_div : r;
-        if (static_cast<unsigned>(src) >= static_cast<unsigned>(p.a_rows)) src = -1;
-      }
-      s_src[i] = src;
-    }
-    __syncthreads();
+    const int local = tile - s_pref[lo] * ntn, mtiles = s_pref[lo + 1] - s_pref[lo];
+    const int m0 = (local % mtiles) * TM;
+    t.e = __builtin_amdgcn_readfirstlane(lo);
+    t.n0 = __builtin_amdgcn_readfirstlane((local / mtiles) * TN);
+    t.row0 = __builtin_amdgcn_readfirstlane(s_row0[lo] + m0);
+    t.rows = __builtin_amdgcn_readfirstlane(min(TM, s_rows[lo] - m0));
+    return t;
+  };
+  // Source row of row `tid` of a tile, -1 if it has none.
+  auto row_source = [&](const A4Tile& t) {
+    if (tid >= t.rows) return -1;
+    const int r = t.row0 + tid;
+    const int src = p.a_row_map ? p.a_row_map[r] / p.a_row_div : r;
+    return static_cast<unsigned>(src) < static_cast<unsigned>(p.a_rows) ? src : -1;
+  };
 
-    // Load q of a stage (wave w's i-th: q = 4 i + w) fills rows 16 q .. 16 q +
-    // 15; lane l lands in row 16 q + l / 4, slot l % 4. Rows without a source
-    // and weight rows past N load a valid row, never used.
-    const uint8_t* src[NL];
-    const int chunk = (lane & 3) ^ (lane >> 4);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int row = 16 * (4 * i + wave) + (lane >> 2);
-      if (i < NLW) {
-        const int n = min(n0 + row, N - 1);
-        src[i] = p.w + (static_cast<int64_t>(e) * N + n) * (K / 2) + chunk * 16;
-      } else {
-        const int a = max(s_src[row - TN], 0);
-        src[i] = p.a + static_cast<int64_t>(a) * (K / 2) + chunk * 16;
-      }
-    }
-    // Scale load i of wave w: rows 64 (4 i + w) .. + 63, a row per lane.
-    const uint8_t* ssrc[SL];
-#pragma unroll
-    for (int i = 0; i < SL; ++i) {
-      const int row = 64 * (4 * i + wave) + lane;
-      if (row < TN) {
-        const int n = min(n0 + row, N - 1);
-        ssrc[i] = p.w_scales + (static_cast<int64_t>(e) * N + n) * (K / kMxBlock);
-      } else {
-        const int a = max(s_src[min(row, ROWS - 1) - TN], 0);
-        ssrc[i] = static_cast<const uint8_t*>(p.a_scales) + static_cast<int64_t>(a) * (K / kMxBlock);
-      }
-    }
-    auto issue = [&](int s, uint8_t* st, uint32_t* sc) {
-      const int kb = min(s, KB - 1);
-#pragma unroll
-      for (int i = 0; i < NL; ++i)
-        load_lds16(src[i] + kb * 64, st + (4 * i + wave) * 1024);
-      if constexpr (!WIDE) {
-#pragma unroll
-        for (int i = 0; i < SL; ++i)
-          load_lds4(ssrc[i] + kb * 4, sc + (4 * i + wave) * 64);
-      }
-    };
-    auto issue_scales = [&](int q) {  // WIDE: the four stages 4q .. 4q + 3
-      const int kb = min(4 * q, KB - 4);
-#pragma unroll
-      for (int i = 0; i < SL; ++i)
-        load_lds16(ssrc[i] + kb * 4, s_sc0 + (4 * i + wave) * 256);
-    };
-    constexpr int PER = NL + (WIDE ? 0 : SL);  // loads per wave and stage
+  // Workgroups go round-robin over the 8 XCDs: neighbouring tiles, which share
+  // operand rows, go to workgroups of one XCD and so to one L2.
+  const int grid = static_cast<int>(gridDim.x);
+  int tile = grid % 8 == 0 ? (blockIdx.x & 7) * (grid / 8) + (blockIdx.x >> 3) : blockIdx.x;
+  if (tile >= total) return;
+  A4Tile cur = locate(tile), nxt = locate(tile + grid);
+  if (tid < TM) {
+    s_src[0][tid] = row_source(cur);
+    s_src[1][tid] = row_source(nxt);
+  }
+  __syncthreads();
 
-    v16f acc[NI][MI];
+  // Load q of an operand's stage (wave w's i-th: q = 4 i + w) fills rows 8 q
+  // .. 8 q + 7; lane l lands in row 8 q + l / 8, slot l % 8. Scale load i of
+  // wave w fills rows 64 (4 i + w) .. + 63, a row per lane. Rows without a
+  // source and weight rows past N load a valid row, never used. Addresses are
+  // a uniform base and a 32-bit offset per lane (an operand's bytes, or one
+  // expert's, are below 2^32).
+  static_assert(TN == kA4TThreads, "scale load 0 is the weights'");
+  const uint32_t pitch = K / 2, spitch = K / kMxBlock;
+  const int chunk = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
+  const uint32_t wlane = (8 * wave + (lane >> 3)) * pitch + chunk * 16;
+  // Sources of the current tile [0] and the next [1]; the loads choose by
+  // uniform selects (a branch would let MFMAs be moved past it, out of their
+  // quarter). After a workgroup's last tile they load rows that exist, unused.
+  struct Sources {
+    const uint8_t* w;   // the first weight row
+    const uint8_t* ws;  //   and its scale bytes
+    int blocks;         // 32-row blocks of weights below N
+    uint32_t wsoff, xsoff;
+    uint32_t xoff[XL];
+  } src[2];
+  auto set_sources = [&](Sources& o, const A4Tile& t, const int* rows) {
+    const int64_t row = static_cast<int64_t>(t.e) * N + t.n0;
+    o.w = p.w + row * pitch;
+    o.ws = p.w_scales + row * spitch;
+    o.blocks = min(TN, N - t.n0) / 32;
+    o.wsoff = static_cast<uint32_t>(min(64 * wave + lane, N - t.n0 - 1)) * spitch;
+    o.xsoff = static_cast<uint32_t>(max(rows[min(64 * wave + lane, TM - 1)], 0)) * spitch;
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      o.xoff[i] = static_cast<uint32_t>(max(rows[8 * (4 * i + wave) + (lane >> 3)], 0)) * pitch + chunk * 16;
+  };
+  // Byte offset of stage s of the current tile, or for s >= P2 of stage s - P2
+  // of the next. With K an odd multiple of 128 the last stage's second half
+  // lies past the row: its lanes load the first half again.
+  auto stage_index = [&](int s) { return min(s < P2 ? s : s - P2, P - 1); };
+  auto past_end = [&](int kb) -> uint32_t {
+    if constexpr (WIDE) return 0u;
+    return kb * 256 + 128 >= K && chunk >= 4 ? 64u : 0u;
+  };
+  auto issue_tokens = [&](int s, uint8_t* buf) {
+    const int kb = stage_index(s);
+    const bool n = s >= P2;
+    const uint8_t* base = p.a + kb * 128;
+    const uint32_t back = past_end(kb);
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      load_lds16(base + ((n ? src[1].xoff[i] : src[0].xoff[i]) - back), buf + (4 * i + wave) * 1024);
+  };
+  auto issue_weights = [&](int s, uint8_t* buf) {
+    const int kb = stage_index(s);
+    const bool n = s >= P2;
+    const uint8_t* base = (n ? src[1].w : src[0].w) + kb * 128;
+    const int blocks = n ? src[1].blocks : src[0].blocks;
+    const uint32_t back = past_end(kb);
+#pragma unroll
+    for (int i = 0; i < WL; ++i)
+      load_lds16(base + static_cast<int64_t>(i < blocks ? i : 0) * 32 * pitch + (wlane - back), buf + (4 * i + wave) * 1024);
+  };
+  // The scales of stage s (G = 1), s and s + 1 (G = 2), s .. s + 3 (G = 4).
+  auto issue_scales = [&](int s, uint32_t* sc) {
+    const int kb = stage_index(s);
+    const bool n = s >= P2;
+    const uint8_t* wb = n ? src[1].ws : src[0].ws;
+    const uint8_t* xb = static_cast<const uint8_t*>(p.a_scales);
+    const uint32_t wo = n ? src[1].wsoff : src[0].wsoff, xo = n ? src[1].xsoff : src[0].xsoff;
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < G / 2; ++i) {
+        load_lds16(wb + (kb * 8 + 16 * i) + wo, sc + kScRows * 4 * i + wave * 256);
+        load_lds16(xb + (kb * 8 + 16 * i) + xo, sc + kScRows * 4 * i + TN * 4 + wave * 256);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int b = min(2 * kb + i, K / kGroup - 1) * 4;
+        load_lds4(wb + b + wo, sc + kScRows * i + wave * 64);
+        load_lds4(xb + b + xo, sc + kScRows * i + TN + wave * 64);
+      }
+    }
+  };
+  constexpr int SCL = WIDE ? G : 4;  // its loads
+
+  v16f acc[NI][MI];
+  uint4 fw[2][NI];                // weight fragments of this quarter and the next
+  uint4 fx[4][MI];                // token fragments of the stage's quarters
+  uint4 scw[NI], scx[MI];         // scale bytes of two stages (not WIDE: of one, in x and y)
+  uint32_t cw[NI], cx[MI];        // this quarter's, the lane's half in bytes 0 and 2
+  int wrow = wn * (TN / 2) + r32, xrow = wm * (TM / 2) + r32;
+  const int swz = (r32 >> 1) & 7;
+  auto read_weights = [&](const uint8_t* buf, auto q_t) {
+    constexpr int q = decltype(q_t)::value;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      fw[q & 1][i] = *reinterpret_cast<const uint4*>(buf + (wrow + 32 * i) * 128 + (((2 * q + h) ^ swz) << 4));
+  };
+  auto read_tokens = [&](const uint8_t* buf, auto q_t) {
+    constexpr int q = decltype(q_t)::value;
+#pragma unroll
+    for (int j = 0; j < MI; ++j)
+      fx[q][j] = *reinterpret_cast<const uint4*>(buf + (xrow + 32 * j) * 128 + (((2 * q + h) ^ swz) << 4));
+  };
+  auto read_pair_scales = [&](const uint32_t* sc) {  // WIDE
+#pragma unroll
+    for (int i = 0; i < NI; ++i) scw[i] = *reinterpret_cast<const uint4*>(sc + (wrow + 32 * i) * 4);
+#pragma unroll
+    for (int j = 0; j < MI; ++j) scx[j] = *reinterpret_cast<const uint4*>(sc + (TN + xrow + 32 * j) * 4);
+  };
+  auto read_stage_scales = [&](const uint32_t* sc) {  // not WIDE
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      scw[i].x = sc[wrow + 32 * i];
+      scw[i].y = sc[kScRows + wrow + 32 * i];
+    }
+#pragma unroll
+    for (int j = 0; j < MI; ++j) {
+      scx[j].x = sc[TN + xrow + 32 * j];
+      scx[j].y = sc[kScRows + TN + xrow + 32 * j];
+    }
+  };
+  // The words of K block d (128 wide) of the held stages.
+  auto block_scales = [&](auto d_t) {
+    constexpr int d = decltype(d_t)::value;
+    auto pick = [](uint4 v) { return d == 0 ? v.x : (d == 1 ? v.y : (d == 2 ? v.z : v.w)); };
+#pragma unroll
+    for (int i = 0; i < NI; ++i) cw[i] = pick(scw[i]) >> (8 * h);
+#pragma unroll
+    for (int j = 0; j < MI; ++j) cx[j] = pick(scx[j]) >> (8 * h);
+  };
+  auto products = [&](auto q_t) {
+    constexpr int q = decltype(q_t)::value;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < MI; ++j)
+        acc[i][j] = mfma_a4_32<(q & 1) == 1>(fw[q & 1][i], fx[q][j], acc[i][j], cw[i], cx[j]);
+  };
+  // K values past the end: zero codes.
+  auto mask_tokens = [&](int s, auto q_t) {
+    if constexpr (!WIDE) {
+      constexpr int q = decltype(q_t)::value;
+      const uint32_t m = s * 256 + q * 64 < K ? ~0u : 0u;
+#pragma unroll
+      for (int j = 0; j < MI; ++j) fx[q][j] = uint4{fx[q][j].x & m, fx[q][j].y & m, fx[q][j].z & m, fx[q][j].w & m};
+    }
+  };
+  // Spreads LDS reads and then loads over a quarter's MFMAs.
+  auto spread = [&](auto reads_t, auto loads_t) {
+    constexpr int reads = decltype(reads_t)::value, loads = decltype(loads_t)::value;
+    constexpr int rp = (reads + M - 1) / M;  // reads per MFMA
+    constexpr int lp = (loads + M - 1) / M;
+    constexpr int l0 = M - (loads + lp - 1) / lp_or_one(lp);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                     // MFMA
+      if (i * rp < reads) __builtin_amdgcn_sched_group_barrier(0x100, rp, 0);                // LDS reads
+      if (loads > 0 && i >= l0) __builtin_amdgcn_sched_group_barrier(0x020, lp, 0);          // loads
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const std::integral_constant<int, 0> c0;
+  const std::integral_constant<int, 1> c1;
+  const std::integral_constant<int, 2> c2;
+  const std::integral_constant<int, 3> c3;
+  int buf = 0;  // s_src slot of the current tile
+
+  // Stage s; V = s % U; its buffers w and x, and the next stage's.
+  auto stage = [&](int s, auto v_t, uint8_t* w, uint8_t* x, const uint8_t* w_next, const uint8_t* x_next,
+                   uint32_t* sc, const uint32_t* sc_next) {
+    constexpr int V = decltype(v_t)::value;
+    // q = 0
+    read_tokens(x, c1);
+    read_tokens(x, c2);
+    read_tokens(x, c3);
+    read_weights(w, c1);
+    products(c0);
+    spread(std::integral_constant<int, 3 * MI + NI>{}, c0);
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    // q = 1
+    mask_tokens(s, c1);
+    mask_tokens(s, c2);
+    mask_tokens(s, c3);
+    issue_tokens(s + 2, x);
+    read_weights(w, c2);
+    products(c1);
+    spread(std::integral_constant<int, NI>{}, std::integral_constant<int, XL>{});
+    // q = 2
+    block_scales(std::integral_constant<int, WIDE ? 2 * (V & 1) + 1 : 1>{});
+    read_weights(w, c3);
+    products(c2);
+    spread(std::integral_constant<int, NI>{}, c0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(XL));  // all but the tokens of stage s + 2
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    // q = 3. The scales of the next group or pair go where this one's last
+    // were read two barriers ago at least.
+    constexpr bool SCALES = !WIDE || V == U - 2;
+    constexpr bool PAIR = WIDE && (V & 1) == 1;
+    if constexpr (SCALES) issue_scales(s + 2, sc);
+    issue_weights(s + 2, w);
+    read_tokens(x_next, c0);
+    read_weights(w_next, c0);
+    if constexpr (PAIR) read_pair_scales(s_sc0 + (V == U - 1 ? 0 : kScRows * 4));
+    products(c3);
+    spread(std::integral_constant<int, (PAIR ? 2 : 1) * (MI + NI)>{},
+           std::integral_constant<int, WL + (SCALES ? SCL : 0)>{});
+    if constexpr (!WIDE) read_stage_scales(sc_next);
+    block_scales(std::integral_constant<int, WIDE && (V & 1) == 0 ? 2 : 0>{});
+    mask_tokens(s + 1 < P2 ? s + 1 : 0, c0);
+  };
+  set_sources(src[0], cur, s_src[0]);
+  set_sources(src[1], nxt, s_src[1]);
+  issue_scales(0, s_sc0);
+  if constexpr (!WIDE) issue_scales(1, s_sc1);
+  issue_tokens(0, s_x0);
+  issue_weights(0, s_w0);
+  issue_tokens(1, s_x1);
+  issue_weights(1, s_w1);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(XL + WL));
+  lds_barrier();
+  if constexpr (WIDE) read_pair_scales(s_sc0);
+  else read_stage_scales(s_sc0);
+  read_tokens(s_x0, c0);
+  read_weights(s_w0, c0);
+  block_scales(c0);
+
+  while (true) {
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < MI; ++j) acc[i][j] = v16f{};
-    uint4 fw[2][NI], fx[2][MI];
-    uint4 scw[NI], scx[MI];         // WIDE: the rows' bytes of four stages
-    uint32_t cw[NI], cx[MI];        // this stage's, the lane's half in bytes 0 and 2
-    const int wrow = wn * (TN / 2) + r32, xrow = TN + wm * (TM / 2) + r32;
-    const int swz = (r32 >> 2) & 3;
-    auto frags = [&](const uint8_t* st, auto kk_t) {
-      constexpr int kk = decltype(kk_t)::value;
-      const int off = ((2 * kk + h) ^ swz) << 4;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) fw[kk][i] = *reinterpret_cast<const uint4*>(st + (wrow + 32 * i) * 64 + off);
-#pragma unroll
-      for (int j = 0; j < MI; ++j) fx[kk][j] = *reinterpret_cast<const uint4*>(st + (xrow + 32 * j) * 64 + off);
-    };
-    auto read_group_scales = [&]() {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) scw[i] = *reinterpret_cast<const uint4*>(s_sc0 + (wrow + 32 * i) * 4);
-#pragma unroll
-      for (int j = 0; j < MI; ++j) scx[j] = *reinterpret_cast<const uint4*>(s_sc0 + (xrow + 32 * j) * 4);
-    };
-    auto stage_scales = [&](const uint32_t* sc, auto u_t) {
-      constexpr int u = decltype(u_t)::value;
-      auto pick = [](uint4 v) { return u == 0 ? v.x : (u == 1 ? v.y : (u == 2 ? v.z : v.w)); };
-#pragma unroll
-      for (int i = 0; i < NI; ++i) cw[i] = (WIDE ? pick(scw[i]) : sc[wrow + 32 * i]) >> (8 * h);
-#pragma unroll
-      for (int j = 0; j < MI; ++j) cx[j] = (WIDE ? pick(scx[j]) : sc[xrow + 32 * j]) >> (8 * h);
-    };
-    auto products = [&](auto kk_t) {
-      constexpr int kk = decltype(kk_t)::value;
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < MI; ++j)
-          acc[i][j] = mfma_a4_32(fw[kk][i], fx[kk][j], acc[i][j], cw[i], cx[j], std::bool_constant<kk == 1>{});
-    };
-    const std::integral_constant<int, 0> k0;
-    const std::integral_constant<int, 1> k1;
-    // Past the last stage (K no multiple of 512) the tokens' codes are zeros.
-    auto mask_tokens = [&](int s, auto kk_t) {
-      if constexpr (!WIDE) {
-        const uint32_t m = s < KB ? ~0u : 0u;
-#pragma unroll
-        for (int j = 0; j < MI; ++j) {
-          uint4& x = fx[decltype(kk_t)::value][j];
-          x = uint4{x.x & m, x.y & m, x.z & m, x.w & m};
-        }
+    for (int s = 0; s < P2; s += U) {
+      // Keeps the LDS addresses of every buffer out of registers of their own.
+      asm volatile("" : "+v"(wrow), "+v"(xrow));
+      stage(s, c0, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
+      stage(s + 1, c1, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
+      if constexpr (U == 4) {
+        stage(s + 2, c2, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
+        stage(s + 3, c3, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
       }
-    };
-    // One stage: u = s % 4; cur and next its and the next stage's buffers,
-    // fill the one stage s + 3 goes to. Within a half the reads of the next
-    // one (and the direct-to-LDS loads) are spread between its MFMAs.
-    auto stage = [&](int s, auto u_t, const uint8_t* cur, const uint8_t* next, uint8_t* fill,
-                     const uint32_t* sc_next, uint32_t* sc_fill) {
-      constexpr int u = decltype(u_t)::value;
-      constexpr int M = MI * NI;
-      issue(s + 3, fill, sc_fill);
-      if constexpr (WIDE && u == 1) issue_scales(s / 4 + 1);
-      frags(cur, k1);
-      products(k0);
-#pragma unroll
-      for (int i = 0; i < M; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // MFMA
-        if (i < MI + NI) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
-        if (i >= M - NL) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      // The loads issued after those of stage s + 1: stages s + 2 and s + 3,
-      // and the group's scales if issued with either.
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * PER + (WIDE && (u == 1 || u == 2) ? SL : 0)));
-      lds_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      mask_tokens(s, k1);
-      if constexpr (WIDE && u == 3) read_group_scales();
-      frags(next, k0);
-      products(k1);
-#pragma unroll
-      for (int i = 0; i < M; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (i < (WIDE && u == 3 ? 2 : 1) * (MI + NI)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      stage_scales(sc_next, std::integral_constant<int, (u + 1) & 3>{});
-      mask_tokens(s + 1, k0);
-    };
-    if constexpr (WIDE) issue_scales(0);
-    issue(0, s_st0, s_sc0);
-    issue(1, s_st1, s_sc1);
-    issue(2, s_st2, s_sc2);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * PER));
-    lds_barrier();
-    if constexpr (WIDE) read_group_scales();
-    frags(s_st0, k0);
-    stage_scales(s_sc0, k0);
-    const std::integral_constant<int, 2> k2;
-    const std::integral_constant<int, 3> k3;
-    for (int s = 0; s < KB; s += 4) {
-      stage(s, k0, s_st0, s_st1, s_st3, s_sc1, s_sc3);
-      stage(s + 1, k1, s_st1, s_st2, s_st0, s_sc2, s_sc0);
-      stage(s + 2, k2, s_st2, s_st3, s_st1, s_sc3, s_sc1);
-      stage(s + 3, k3, s_st3, s_st0, s_st2, s_sc0, s_sc2);
     }
-    __builtin_amdgcn_s_waitcnt(0);  // trailing loads have landed before a stage is reused
-    __syncthreads();
 
-    // Output: each wave turns its piece through a stage buffer of its own
-    // (rows of TN/2 BF16, 16-byte chunk c of token row r at slot c ^ (r % 16))
-    // and stores whole rows of the piece.
-    {
-      uint8_t* buf = wave == 0 ? s_st0 : (wave == 1 ? s_st1 : (wave == 2 ? s_st2 : s_st3));
-      constexpr int kRowB = TN;  // TN/2 values x 2 bytes
-      constexpr int kChunks = kRowB / 16;
+    // Output, and the row sources of the tile after the next. A lane holds
+    // weight rows 8 v + 4 h .. + 3 (v = 0..3) of its token; the half waves swap
+    // so that it has 8 consecutive ones of v = 2 u + h, and a row gets 32
+    // contiguous bytes per store.
+    const A4Tile after = locate(tile + 2 * grid);
+    const int after_src = row_source(after);
+    const int* from = s_src[buf];
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+    for (int j = 0; j < MI; ++j) {
+      const int row = wm * (TM / 2) + 32 * j + r32;
+      const bool live = row < cur.rows;
+      const uint32_t keep = from[row] < 0 ? 0u : ~0u;
+      uint16_t* crow = p.c + static_cast<int64_t>(cur.row0 + row) * N + cur.n0 + wn * (TN / 2) + 8 * h;
 #pragma unroll
-        for (int j = 0; j < MI; ++j) {
-          const int r = 32 * j + r32;
+      for (int i = 0; i < NI; ++i) {
+        const v16f& a = acc[i][j];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const v4f q = {acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
-            const int c = 4 * i + v;
-            *reinterpret_cast<uint2*>(buf + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4) + 8 * h) = pack_bf16x4(q);
-          }
-        }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      constexpr int kLanesRow = kChunks, kRowsPass = 64 / kLanesRow;
-      const int c = lane % kLanesRow;
-      const int n = n0 + wn * (TN / 2) + 8 * c;
-#pragma unroll 4
-      for (int q = 0; q < TM / 2 / kRowsPass; ++q) {
-        const int r = q * kRowsPass + lane / kLanesRow;
-        const int row = wm * (TM / 2) + r;
-        uint4 v = *reinterpret_cast<const uint4*>(buf + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4));
-        if (row < rows_here && n < N) {
-          if (s_src[row] < 0) v = uint4{0, 0, 0, 0};
-          *reinterpret_cast<uint4*>(p.c + static_cast<int64_t>(row0 + row) * N + n) = v;
+        for (int u = 0; u < 2; ++u) {
+          const uint2 e = pack_bf16x4(v4f{a[8 * u], a[8 * u + 1], a[8 * u + 2], a[8 * u + 3]});
+          const uint2 o = pack_bf16x4(v4f{a[8 * u + 4], a[8 * u + 5], a[8 * u + 6], a[8 * u + 7]});
+          const auto lo = __builtin_amdgcn_permlane32_swap(e.x, o.x, false, false);
+          const auto hi = __builtin_amdgcn_permlane32_swap(e.y, o.y, false, false);
+          const uint4 q = {lo[0] & keep, hi[0] & keep, lo[1] & keep, hi[1] & keep};
+          if (live && cur.n0 + wn * (TN / 2) + 32 * i < N) *reinterpret_cast<uint4*>(crow + 32 * i + 16 * u) = q;
         }
       }
     }
+    if (tid < TM) s_src[buf == 0 ? 2 : buf - 1][tid] = after_src;
+    tile += grid;
+    if (tile >= total) break;
+    lds_barrier();  // the sources are written
+    cur = nxt;
+    nxt = after;
+    src[0] = src[1];
+    set_sources(src[1], nxt, s_src[buf == 0 ? 2 : buf - 1]);
+    buf = buf == 2 ? 0 : buf + 1;
   }
+  __builtin_amdgcn_s_waitcnt(0);  // no load may land after the workgroup's end
 }
 
-template <int TM, int TN>
+template <int TM>
 hipError_t launch_a4_tiled(const W4Args& g, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(device_cu_count()));
-  if (g.k % 512 == 0)
-    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, TN, true>), grid, dim3(kA4TThreads), 0, stream, g);
+  if (g.k % 1024 == 0)
+    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, kA4TileCols, 4>), grid, dim3(kA4TThreads), 0, stream, g);
+  else if (g.k % 512 == 0)
+    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, kA4TileCols, 2>), grid, dim3(kA4TThreads), 0, stream, g);
   else
-    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, TN, false>), grid, dim3(kA4TThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, kA4TileCols, 1>), grid, dim3(kA4TThreads), 0, stream, g);
   return hipGetLastError();
+}
+
+// Row tiles of TM rows that an expert of `mean` rows takes, as expected of
+// routing that spreads rows at random (a Poisson count, near enough normal).
+double expected_tiles(double mean, int tm) {
+  const double sd = sqrt(mean);
+  double n = 0.0;
+  for (double at = 0.0; at < mean + 5.0 * sd; at += tm)
+    n += at == 0.0 ? 1.0 : 0.5 * erfc((at - mean) / (sd * 1.4142135623730951));
+  return n;
 }
 
 }  // namespace
 
 hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
-  const bool large = g.max_rows_per_expert > kA4Small;
-  const dim3 grid(static_cast<unsigned>(4 * device_cu_count()));
-  if (!large) {
-    hipLaunchKernelGGL(gemm_a4_kernel<false>, grid, dim3(kA4Threads), 0, stream, g);
+  const int cus = device_cu_count();
+  const int rows = g.max_rows > 0 ? g.max_rows : g.row_cap;
+  const int live = rows < g.num_experts ? rows : g.num_experts;  // experts with rows, at most
+  const int64_t cols = (g.n + kA4TileCols - 1) / kA4TileCols;
+  // Too few 256-row weight slabs for the CUs: K is split instead.
+  if (live * cols < cus) {
+    hipLaunchKernelGGL(gemm_a4_kernel, dim3(static_cast<unsigned>(4 * cus)), dim3(kA4Threads), 0, stream, g);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(gemm_a4_kernel<true>, grid, dim3(kA4Threads), 0, stream, g);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_a4_tiled<256, 256>(g, stream);
+  // The tile height with the least expected time: tiles of an expert times a
+  // tile's time, 0.6, 0.7, 0.8 and 1 for 64, 128, 192 and 256 rows (32
+  // experts, N 4096, K 7168: 57, 62 and 76 us a round of 128-, 192- and
+  // 256-row tiles; N 7168, K 2048: 18, 23 and 30 us).
+  double mean = static_cast<double>(rows) / live;
+  if (mean > g.max_rows_per_expert) mean = g.max_rows_per_expert;
+  constexpr int kHeights[4] = {64, 128, 192, 256};
+  constexpr double kCost[4] = {0.6, 0.7, 0.8, 1.0};
+  int best = 0;
+  double least = 1e300;
+  for (int i = 0; i < 4; ++i) {
+    const double t = expected_tiles(mean, kHeights[i]) * kCost[i];
+    if (t < least) {
+      least = t;
+      best = i;
+    }
+  }
+  switch (best) {
+    case 0: return launch_a4_tiled<64>(g, stream);
+    case 1: return launch_a4_tiled<128>(g, stream);
+    case 2: return launch_a4_tiled<192>(g, stream);
+    default: return launch_a4_tiled<256>(g, stream);
+  }
 }
 
 }  // namespace moe

@@ -116,6 +116,7 @@ struct W4Args {
   int n;
   int k;
   uint16_t* c;
+  int max_rows = 0;         // host bound on the live rows of all experts (0: row_cap); as above
 };
 hipError_t launch_grouped_gemm_w4(const W4Args& g, hipStream_t stream);
 
