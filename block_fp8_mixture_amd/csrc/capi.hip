@@ -588,6 +588,31 @@ static moe_status forward_impl(const moe_problem* p, const moe_workspace_layout&
   const int pairs = static_cast<int>(pairs64);
 
   hipError_t e = hipSuccess;
+  if (p->scale_fmt == MOE_SCALE_MXFP4 && p->expert_cap == 0 && pairs64 <= moe::kL4MaxPairs) {
+    // A few tokens: the whole layer in two launches.
+    moe::LayerA4Args a;
+    a.ids = t->topk_ids;
+    a.topk_w = t->topk_w;
+    a.t_live_dev = t->t_live_dev;
+    a.t_cap = p->t_cap;
+    a.topk = p->topk;
+    a.num_experts = p->num_experts;
+    a.expert_start = p->expert_start;
+    a.x = t->x;
+    a.hidden = p->hidden;
+    a.inter = p->inter;
+    a.w1 = t->w1;
+    a.w1_scales = static_cast<const uint8_t*>(t->w1_scales);
+    a.w2 = t->w2;
+    a.w2_scales = static_cast<const uint8_t*>(t->w2_scales);
+    a.act = p->act;
+    a.act_limit = p->clamp_limit;
+    a.rounding = p->rounding;
+    a.hq = hq;
+    a.hs = static_cast<uint8_t*>(hs);
+    a.out = t->out;
+    return from_hip(moe::launch_layer_a4(a, s));
+  }
   if (decode && moe::decode_layer_fits_fmt(p->t_cap, p->topk, p->hidden, p->inter, p->weight_fmt) &&
       moe::decode_layer_grid(moe::decode_layer_wide(p->t_cap, p->hidden)) > 0) {
     // The whole layer in one launch.

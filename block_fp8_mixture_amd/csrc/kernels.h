@@ -124,6 +124,34 @@ hipError_t launch_grouped_gemm_w4(const W4Args& g, hipStream_t stream);
 // and a_scales [a_rows, k/32] E8M0 bytes. Called by launch_grouped_gemm_w4.
 hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream);
 
+// The whole layer with MXFP4 activations and weights for at most kL4MaxPairs
+// routed pairs, in two launches. hq [pairs, I/2] and hs [pairs, I/32] hold the
+// quantized FC2 input between them, a row per pair.
+constexpr int kL4MaxPairs = 64;
+struct LayerA4Args {
+  const int32_t* ids;         // [t_cap, topk]
+  const float* topk_w;        // [t_cap, topk]
+  const int32_t* t_live_dev;  // nullable: t_cap
+  int t_cap;
+  int topk;
+  int num_experts;
+  int expert_start;
+  const uint16_t* x;          // [t_cap, H] BF16
+  int hidden;
+  int inter;
+  const uint8_t* w1;          // [E, 2I, H/2], gate rows first
+  const uint8_t* w1_scales;   // [E, 2I, H/32]
+  const uint8_t* w2;          // [E, H, I/2]
+  const uint8_t* w2_scales;   // [E, H, I/32]
+  int act;
+  float act_limit;
+  int rounding;
+  uint8_t* hq;
+  uint8_t* hs;
+  uint16_t* out;              // [t_cap, H]
+};
+hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream);
+
 // BF16 values of an MXFP4 tensor of rows x cols.
 hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                 uint16_t* out, hipStream_t stream);

@@ -1,0 +1,360 @@
+// The expert layer with MXFP4 activations and weights for a few tokens (at
+// most kL4MaxPairs routed pairs), in two launches:
+//   1. per (expert in use, 32 columns of the FC2 input): the tokens' MXFP4
+//      quantization, FC1's 32 gate and 32 up rows, SiLU(gate) * up and its
+//      MXFP4 quantization (one block of 32 columns per token);
+//   2. per 16 output columns: FC2 for every pair and the top-k sum.
+// Nothing passes between the two but the quantized FC2 input, in the caller's
+// workspace, so calls may overlap on different streams.
+//
+// Both read each weight of the experts in use once and are bound by that:
+// the weights go from global memory straight into the operands of
+// v_mfma_scale_f32_16x16x128_f8f6f4, every load of a wave's K share issued
+// before the first is used, and the waves of a workgroup split K.
+//
+// K order. An operand lane (row l % 16, group g = l / 16) holds 32 consecutive
+// K values of an instruction's 128, any 32 as long as both operands agree. Of
+// 256 values two instructions j = 0, 1 give lane group g the blocks 2 g + j:
+// the first load then touches all of a row's 128-byte line, so the memory is
+// asked for whole lines (with blocks g and 4 + g, for two halves of each).
+//
+// Routing. A pair's workgroups compare its expert with those of all pairs (one
+// id per lane, one ballot): the lowest pair of an expert works for all of its
+// tokens, the others' workgroups leave. No table is built.
+#include "device_common.h"
+#include "gemm_device.h"
+#include "kernels.h"
+#include "mx_device.h"
+#include "quant_device.h"
+
+namespace moe {
+namespace {
+
+constexpr int kL1Threads = 512;
+constexpr int kL1Waves = kL1Threads / 64;
+constexpr int kL2Threads = 1024;
+constexpr int kL2Waves = kL2Threads / 64;
+
+// One 128-wide instruction; J: which byte of the scale words.
+template <int J>
+__device__ __forceinline__ v4f mfma_l4(uint4 w, uint32_t ws, uint4 x, uint32_t xs, v4f acc) {
+  const v8i a = {static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z),
+                 static_cast<int>(w.w), 0, 0, 0, 0};
+  const v8i b = {static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z),
+                 static_cast<int>(x.w), 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, J, static_cast<int>(ws), J,
+                                                          static_cast<int>(xs));
+}
+
+// A lane's part of 256 K values of a row: the codes of its blocks 2 g and
+// 2 g + 1 and their scale bytes (bytes 0 and 1). Of a row's last 128 values
+// (`half`) the lane has block g alone: the second load repeats it, and the
+// tokens' second codes are zeros. No branch, so that loads stay together.
+struct L4Frag {
+  uint4 c[2];
+  uint32_t s;
+};
+struct L4Lane {
+  uint32_t c0, c1, s;        // byte offsets of a chunk's two loads and of its scales
+  uint32_t shift, scale_mask;
+  uint32_t second;           // mask of the second codes
+};
+__device__ __forceinline__ L4Lane l4_lane(int g, bool half) {
+  L4Lane l;
+  l.c0 = half ? 16 * g : 32 * g;
+  l.c1 = half ? 16 * g : 32 * g + 16;
+  l.s = half ? g & 2 : 2 * g;
+  l.shift = half ? 8 * (g & 1) : 0;
+  l.scale_mask = half ? 0xFFu : 0xFFFFu;
+  l.second = half ? 0u : ~0u;
+  return l;
+}
+// `codes` and `scales` are uniform, `row` and `srow` the lane's row in them.
+__device__ __forceinline__ void l4_load(L4Frag& f, const uint8_t* codes, uint32_t row, const uint8_t* scales,
+                                        uint32_t srow, int chunk, const L4Lane& l) {
+  const uint8_t* c = codes + chunk * 128;
+  f.c[0] = *reinterpret_cast<const uint4*>(c + (row + l.c0));
+  f.c[1] = *reinterpret_cast<const uint4*>(c + (row + l.c1));
+  f.s = *reinterpret_cast<const uint16_t*>(scales + chunk * 8 + (srow + l.s));
+}
+__device__ __forceinline__ uint32_t l4_scales(const L4Frag& f, const L4Lane& l) {
+  return (f.s >> l.shift) & l.scale_mask;
+}
+
+// Chunks of 256 K values that share `s` of `shares` takes.
+__device__ __forceinline__ int l4_split(int chunks, int s, int shares) { return chunks * s / shares; }
+
+// The r-th set bit of m (64 if there are fewer).
+__device__ __forceinline__ int nth_bit(uint64_t m, int r) {
+  for (int i = 0; i < r && m; ++i) m &= m - 1;
+  return m ? __builtin_ctzll(m) : 64;
+}
+
+// LDS of the tokens of a pass: codes and scale bytes, rows padded so that 16
+// rows' chunks fall on distinct banks.
+__host__ __device__ constexpr int l4_code_stride(int hidden) { return hidden / 2 + 16; }
+__host__ __device__ constexpr int l4_scale_stride(int hidden) { return hidden / kMxBlock + 4; }
+
+__global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];  // a pass's tokens
+  __shared__ __attribute__((aligned(16))) v4f s_part[kL1Waves][4][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int PQ = a.t_cap * a.topk;
+  const int pair = blockIdx.y;
+  // Which expert, and for which pairs.
+  const int t_live = clamp_live(a.t_live_dev, a.t_cap);
+  const int id = lane < PQ ? a.ids[lane] - a.expert_start : -1;
+  const int e = __builtin_amdgcn_readlane(id, pair);
+  const uint64_t mine = __ballot(lane < t_live * a.topk && id == e);
+  if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.num_experts) || mine == 0 ||
+      __builtin_ctzll(mine) != pair)
+    return;
+  const int n_tok = __popcll(mine);
+
+  const int H = a.hidden, I = a.inter;
+  const int col0 = blockIdx.x * 32;
+  const int chunks = (H + 255) / 256;
+  const int ch0 = l4_split(chunks, wave, kL1Waves), ch1 = l4_split(chunks, wave + 1, kL1Waves);
+  // Row tiles: gate rows col0 .. +15, +16 .. +31, then the up rows.
+  const int64_t row0 = static_cast<int64_t>(e) * 2 * I + col0;
+  const uint8_t* wb[4];
+  const uint8_t* sb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + (i >> 1) * I + (i & 1) * 16;
+    wb[i] = a.w1 + row * (H / 2);
+    sb[i] = a.w1_scales + row * (H / kMxBlock);
+  }
+  uint32_t wrow = r16 * (H / 2), srow = r16 * (H / kMxBlock);
+  const int XS = l4_code_stride(H), XB = l4_scale_stride(H);
+  const int width = min(a.t_cap, 16);  // tokens of a pass, at most
+  uint8_t* s_x = s_dyn;
+  uint8_t* s_xs = s_dyn + width * XS;
+
+  for (int t0 = 0; t0 < n_tok; t0 += 16) {
+    const int nt = min(16, n_tok - t0);
+    // Opaque to the compiler, which otherwise keeps every address and index of
+    // this (mostly single) pass in registers of its own and spills.
+    int gl = g, tl = tid;
+    asm volatile("" : "+v"(gl), "+v"(tl), "+v"(wrow), "+v"(srow));
+    // The first two chunks' weights go out before anything waits. Chunks past
+    // the share load its last one, unused.
+    L4Frag w[2][4];
+    auto load = [&](int ch, L4Frag (&f)[4]) {
+      const int c = min(ch, max(ch1 - 1, 0));
+      const L4Lane l = l4_lane(gl, c * 256 + 128 >= H);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l4_load(f[i], wb[i], wrow, sb[i], srow, c, l);
+    };
+    // The pass's tokens to LDS, 8 values per item. The first items' loads go
+    // out ahead of the weights (loads return in order).
+    const int per = H / 8, items = nt * per;
+    auto load_item = [&](int i) {
+      const int k = i / per;
+      const int q = nth_bit(mine, t0 + k);
+      return *reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(q / a.topk) * H + (i - k * per) * 8);
+    };
+    auto store_item = [&](int i, uint4 raw) {
+      const int k = i / per, c = i - k * per;
+      uint32_t byte;
+      const uint32_t codes = mx_quantize8_bf16(raw, &byte);
+      if (i >= items) return;  // whole quads: items is a multiple of 16
+      *reinterpret_cast<uint32_t*>(s_x + k * XS + c * 4) = codes;
+      if ((c & 3) == 0) s_xs[k * XB + (c >> 2)] = static_cast<uint8_t>(byte);
+    };
+    const uint4 raw0 = load_item(min(tl, items - 1)), raw1 = load_item(min(tl + kL1Threads, items - 1));
+    __builtin_amdgcn_sched_barrier(0);
+    load(ch0, w[0]);
+    load(ch0 + 1, w[1]);
+    __builtin_amdgcn_sched_barrier(0);
+    store_item(tl, raw0);
+    store_item(tl + kL1Threads, raw1);
+    for (int i = tl + 2 * kL1Threads; i < items; i += 2 * kL1Threads) {
+      const int i1 = i + kL1Threads;
+      const uint4 r0 = load_item(i), r1 = load_item(min(i1, items - 1));
+      store_item(i, r0);
+      store_item(i1, r1);
+    }
+    lds_barrier();  // (leaves the weights in flight)
+    v4f acc[4] = {};
+    // Columns past the tokens repeat the last.
+    const uint32_t xrow = min(r16, nt - 1) * XS, xsrow = min(r16, nt - 1) * XB;
+    auto products = [&](int ch, const L4Frag (&f)[4]) {
+      const L4Lane l = l4_lane(gl, ch * 256 + 128 >= H);
+      L4Frag x;
+      l4_load(x, s_x, xrow, s_xs, xsrow, ch, l);
+      const uint32_t xs = l4_scales(x, l), m = l.second;
+      const uint4 x1 = {x.c[1].x & m, x.c[1].y & m, x.c[1].z & m, x.c[1].w & m};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = mfma_l4<0>(f[i].c[0], l4_scales(f[i], l), x.c[0], xs, acc[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = mfma_l4<1>(f[i].c[1], l4_scales(f[i], l), x1, xs, acc[i]);
+    };
+    int ch = ch0;
+    for (; ch + 2 < ch1; ch += 2) {
+      products(ch, w[0]);
+      load(ch + 2, w[0]);
+      products(ch + 1, w[1]);
+      load(ch + 3, w[1]);
+    }
+    if (ch < ch1) products(ch, w[0]);
+    if (ch + 1 < ch1) products(ch + 1, w[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_part[wave][i][lane] = acc[i];
+    __syncthreads();
+    // Thread (token, column): 32 lanes hold a token's 32 columns. The shares
+    // add in wave order. Value (column c, token k) of a tile pair lies in tile
+    // c / 16, lane 16 (c % 16 / 4) + k, element c % 4.
+    {
+      const int k = tl >> 5, c = tl & 31;
+      const int src = 16 * ((c & 15) >> 2) + k;
+      float gate = 0.0f, up = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kL1Waves; ++w) {
+        gate += s_part[w][c >> 4][src][c & 3];
+        up += s_part[w][2 + (c >> 4)][src][c & 3];
+      }
+      const uint2 b = pack_bf16x4(v4f{gate, up, 0.0f, 0.0f});  // C1 is BF16
+      const float y = swiglu_any(a.act, bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), a.act_limit, a.rounding);
+      uint32_t amax = __float_as_uint(y) & 0x7FFFFFFFu;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_xor(static_cast<int>(amax), d, 64);
+        amax = o > amax ? o : amax;
+      }
+      const uint32_t byte = mx_scale_byte(amax);
+      // Lane c even packs columns c and c + 1; every fourth pair's first lane
+      // stores four bytes.
+      const float y1 = __shfl_xor(y, 1, 64);
+      uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y, y1, mx_scale_float(byte), 0) & 0xFFu;
+      if (byte == 255u) code = 0;
+      code |= __shfl_xor(static_cast<int>(code), 2, 64) << 8;
+      code |= __shfl_xor(static_cast<int>(code), 4, 64) << 16;
+      if (t0 + k < n_tok) {
+        const int q = nth_bit(mine, t0 + k);
+        const int64_t at = static_cast<int64_t>(q) * I + col0;
+        if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + at / 2 + c / 2) = code;
+        if (c == 0) a.hs[at / kMxBlock] = static_cast<uint8_t>(byte);
+      }
+    }
+    __syncthreads();  // the partials are free for the next 16 tokens
+  }
+}
+
+// A wave task is (expert in use, a share of K); the shares of a pair's row
+// add in order before its BF16 rounding, then out[t] = sum over ascending k of
+// w[t, k] * row, in fp32.
+__global__ __launch_bounds__(kL2Threads, 4) void layer_a4_fc2_kernel(LayerA4Args a) {
+  extern __shared__ __attribute__((aligned(16))) float s_slot[];  // [share][pair][16 columns]
+  __shared__ float s_w[kL4MaxPairs];
+  __shared__ int s_ok[kL4MaxPairs];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int TK = a.topk, PQ = a.t_cap * TK;
+  const int t_live = clamp_live(a.t_live_dev, a.t_cap);
+  const int id = lane < PQ ? a.ids[lane] - a.expert_start : -1;
+  const float tw = lane < PQ ? a.topk_w[lane] : 0.0f;
+  const bool ok = lane < t_live * TK && static_cast<unsigned>(id) < static_cast<unsigned>(a.num_experts);
+  // Pairs with this lane's expert: one ballot per bit of an expert id.
+  uint64_t eq = __ballot(ok);
+  for (int b = 31 - __builtin_clz(a.num_experts | 1); b >= 0; --b) {
+    const bool bit = (id >> b) & 1;
+    const uint64_t m = __ballot(ok && bit);
+    eq &= bit ? m : ~m;
+  }
+  const uint64_t below = (uint64_t{1} << lane) - 1;
+  const uint64_t leaders = __ballot(ok && (eq & below) == 0);
+  const int n_lead = __popcll(leaders);
+  if (wave == 0) {
+    s_w[lane] = tw;
+    s_ok[lane] = ok;
+  }
+  const int H = a.hidden, I = a.inter;
+  const int n0 = blockIdx.x * 16;
+  const int chunks = (I + 255) / 256;
+  int S = 1;
+  while (n_lead * S * 2 <= kL2Waves && S * 2 <= chunks) S *= 2;
+  for (int task = wave; task < n_lead * S; task += kL2Waves) {
+    const int share = task & (S - 1);
+    const int lead = nth_bit(leaders, task / S);
+    const int e = __builtin_amdgcn_readlane(id, lead);
+    const uint64_t mine = static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(eq), lead))) |
+                          static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(eq >> 32), lead))) << 32;
+    const int n_tok = __popcll(mine);
+    const int64_t row = static_cast<int64_t>(e) * H + n0;
+    const uint8_t* wb = a.w2 + row * (I / 2);
+    const uint8_t* sb = a.w2_scales + row * (I / kMxBlock);
+    const uint32_t wrow = r16 * (I / 2), srow = r16 * (I / kMxBlock);
+    const int ch0 = l4_split(chunks, share, S), ch1 = l4_split(chunks, share + 1, S);
+    for (int t0 = 0; t0 < n_tok; t0 += 16) {
+      const int q = nth_bit(mine, t0 + min(r16, n_tok - t0 - 1));
+      const uint32_t xrow = q * (I / 2), xsrow = q * (I / kMxBlock);
+      v4f acc = {};
+      // Two chunks' loads together (past the share: its last one, unused).
+      for (int ch = ch0; ch < ch1; ch += 2) {
+        const int c1 = min(ch + 1, ch1 - 1);
+        const L4Lane l0 = l4_lane(g, ch * 256 + 128 >= I), l1 = l4_lane(g, c1 * 256 + 128 >= I);
+        L4Frag w[2], x[2];
+        l4_load(w[0], wb, wrow, sb, srow, ch, l0);
+        l4_load(w[1], wb, wrow, sb, srow, c1, l1);
+        l4_load(x[0], a.hq, xrow, a.hs, xsrow, ch, l0);
+        l4_load(x[1], a.hq, xrow, a.hs, xsrow, c1, l1);
+        auto products = [&](int u, const L4Lane& l) {
+          const uint32_t ws = l4_scales(w[u], l), xs = l4_scales(x[u], l), m = l.second;
+          const uint4 x1 = {x[u].c[1].x & m, x[u].c[1].y & m, x[u].c[1].z & m, x[u].c[1].w & m};
+          acc = mfma_l4<0>(w[u].c[0], ws, x[u].c[0], xs, acc);
+          acc = mfma_l4<1>(w[u].c[1], ws, x1, xs, acc);
+        };
+        products(0, l0);
+        if (ch + 1 < ch1) products(1, l1);
+      }
+      if (t0 + r16 < n_tok)
+        *reinterpret_cast<v4f*>(s_slot + (share * PQ + q) * 16 + 4 * g) = acc;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < t_live * 8; i += kL2Threads) {
+    const int t = i >> 3, c = (i & 7) * 2;
+    float o0 = 0.0f, o1 = 0.0f;
+    for (int k = 0; k < TK; ++k) {
+      const int q = t * TK + k;
+      if (!s_ok[q]) continue;
+      float y0 = 0.0f, y1 = 0.0f;
+      for (int s = 0; s < S; ++s) {
+        const float2 v = *reinterpret_cast<const float2*>(s_slot + (s * PQ + q) * 16 + c);
+        y0 += v.x;
+        y1 += v.y;
+      }
+      const uint2 b = pack_bf16x4(v4f{y0, y1, 0.0f, 0.0f});
+      o0 = fmaf(s_w[q], bf16_to_f32(b.x & 0xFFFFu), o0);
+      o1 = fmaf(s_w[q], bf16_to_f32(b.x >> 16), o1);
+    }
+    const uint2 b = pack_bf16x4(v4f{o0, o1, 0.0f, 0.0f});
+    *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(t) * H + n0 + c) = b.x;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream) {
+  const int pairs = a.t_cap * a.topk;
+  if (pairs < 1 || pairs > kL4MaxPairs) return hipErrorInvalidValue;
+  const size_t tokens = static_cast<size_t>(a.t_cap < 16 ? a.t_cap : 16) * (l4_code_stride(a.hidden) + l4_scale_stride(a.hidden));
+  hipLaunchKernelGGL(layer_a4_fc1_kernel, dim3(static_cast<unsigned>(a.inter / 32), static_cast<unsigned>(pairs)),
+                     dim3(kL1Threads), tokens, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // At most kL2Waves shares in all of experts in use x shares, plus one per
+  // expert: 16 columns x pairs x shares of them, shares <= 16.
+  const int chunks = (a.inter + 255) / 256;
+  int shares = 1;
+  while (shares * 2 <= kL2Waves && shares * 2 <= chunks) shares *= 2;
+  const size_t lds = static_cast<size_t>(shares) * pairs * 16 * sizeof(float);
+  hipLaunchKernelGGL(layer_a4_fc2_kernel, dim3(static_cast<unsigned>(a.hidden / 16)), dim3(kL2Threads), lds, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe
