@@ -145,11 +145,29 @@ def _check(fn, status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+# The handle of a device's current stream (torch.cuda.current_stream builds a
+# Stream object around it: 3 us per call against 0.1).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(index):
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream(index).cuda_stream
+
+
+def _enqueue(name, device, *args):
+    """Calls library function `name` on the current stream of `device`, where the
+    tensors live (made the current device if it is another)."""
+    fn = getattr(_lib, name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(device.index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device.index))
+    if status != 0:
+        raise MoeError(name, status)
 
 
 def _need(t, name, dtype, device=None, ndim=None):
@@ -166,7 +184,7 @@ def _need(t, name, dtype, device=None, ndim=None):
 
 def _shape(t, name, shape):
     """Raises ValueError unless tensor ``t`` has exactly ``shape``."""
-    if tuple(t.shape) != tuple(int(d) for d in shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -179,12 +197,19 @@ def _min_numel(t, name, n):
 
 def _same_device(*tensors):
     """All given tensors on one GPU (checked after every shape, so shape errors
-    are reported first)."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors live on different devices: {sorted(map(str, devs))}")
-    if any(d.type != "cuda" for d in devs):
+    are reported first). Returns the device."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            devs = {t.device for t in tensors if t is not None}
+            raise ValueError(f"tensors live on different devices: {sorted(map(str, devs))}")
+    if dev is None or dev.type != "cuda":
         raise ValueError("tensors must be GPU tensors")
+    return dev
 
 
 def _fmt(fmt):
@@ -263,12 +288,11 @@ def moe_route(logits, topk, score="softmax", bias=None, renormalize=True, scale=
         weights = torch.empty((t_cap, topk), dtype=torch.float32, device=logits.device)
     _shape(_need(ids, "ids", torch.int32), "ids", (t_cap, topk))
     _shape(_need(weights, "weights", torch.float32), "weights", (t_cap, topk))
-    _same_device(logits, bias, ids, weights)
+    dev = _same_device(logits, bias, ids, weights, t_live)
     router = _Router(num_experts, topk, SCORES[score], int(bool(renormalize)), float(scale),
                      int(num_groups), int(top_groups), int(group_top))
-    st = lib.moe_route(ctypes.byref(router), _ptr(logits), LOGIT_TYPES[logits.dtype], ld, _ptr(bias),
-                       t_cap, _live(t_live), _ptr(ids), _ptr(weights), _stream())
-    _check("moe_route", st)
+    _enqueue("moe_route", dev, ctypes.byref(router), _ptr(logits), LOGIT_TYPES[logits.dtype], ld,
+             _ptr(bias), t_cap, _live(t_live), _ptr(ids), _ptr(weights))
     return ids, weights
 
 
@@ -284,10 +308,9 @@ def moe_mxfp4_dequant(codes, scales, out=None):
     if out is None:
         out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
     ob = _shape(_bf16_view(out, "out"), "out", lead + (cols,))
-    _same_device(codes, scales, ob)
-    st = lib.moe_mxfp4_dequant(_ptr(codes), _ptr(scales), codes.numel() * 2 // cols, cols, _ptr(ob),
-                               _stream())
-    _check("moe_mxfp4_dequant", st)
+    dev = _same_device(codes, scales, ob)
+    _enqueue("moe_mxfp4_dequant", dev, _ptr(codes), _ptr(scales), codes.numel() * 2 // cols, cols,
+             _ptr(ob))
     return out
 
 
@@ -311,11 +334,10 @@ def moe_align(topk_ids, num_experts, align_rows=16, row_cap=None, t_live=None, o
     for k, n in (("counts", num_experts), ("offsets", num_experts + 1),
                  ("row_to_pair", row_cap), ("pair_to_row", t_cap * topk)):
         _min_numel(_need(out[k], k, torch.int32), k, n)
-    _same_device(ids, *out.values())
-    st = lib.moe_align(_ptr(ids), t_cap, _live(t_live), topk, num_experts, expert_start,
-                       align_rows, row_cap, _ptr(out["counts"]), _ptr(out["offsets"]),
-                       _ptr(out["row_to_pair"]), _ptr(out["pair_to_row"]), _stream())
-    _check("moe_align", st)
+    dev = _same_device(ids, *out.values())
+    _enqueue("moe_align", dev, _ptr(ids), t_cap, _live(t_live), topk, num_experts, expert_start,
+             align_rows, row_cap, _ptr(out["counts"]), _ptr(out["offsets"]),
+             _ptr(out["row_to_pair"]), _ptr(out["pair_to_row"]))
     return out
 
 
@@ -336,11 +358,10 @@ def moe_align_batched(topk_ids, num_experts, expert_cap, t_live=None, out=None, 
     for k, n in (("masked_m", num_experts), ("row_to_pair", num_experts * expert_cap),
                  ("pair_to_row", t_cap * topk), ("overflow", 1)):
         _min_numel(_need(out[k], k, torch.int32), k, n)
-    _same_device(ids, *out.values())
-    st = lib.moe_align_batched(_ptr(ids), t_cap, _live(t_live), topk, num_experts, expert_start,
-                               expert_cap, _ptr(out["masked_m"]), _ptr(out["row_to_pair"]),
-                               _ptr(out["pair_to_row"]), _ptr(out["overflow"]), _stream())
-    _check("moe_align_batched", st)
+    dev = _same_device(ids, *out.values())
+    _enqueue("moe_align_batched", dev, _ptr(ids), t_cap, _live(t_live), topk, num_experts,
+             expert_start, expert_cap, _ptr(out["masked_m"]), _ptr(out["row_to_pair"]),
+             _ptr(out["pair_to_row"]), _ptr(out["overflow"]))
     return out
 
 
@@ -358,10 +379,9 @@ def moe_act_quant(x, fmt="fp32", t_live=None, xq=None, xs=None, rounding="divide
         xs = torch.empty(_scale_shape(t_cap, hidden, fmt), dtype=_scale_dtype(fmt), device=xb.device)
     _shape(_need(xq, "xq", torch.uint8), "xq", (t_cap, _code_cols(hidden, fmt)))
     _shape(_need(xs, "xs", _scale_dtype(fmt)), "xs", _scale_shape(t_cap, hidden, fmt))
-    _same_device(xb, xq, xs)
-    st = lib.moe_act_quant(_ptr(xb), t_cap, _live(t_live), hidden, _fmt(fmt), _rounding(rounding),
-                           _ptr(xq), _ptr(xs), _stream())
-    _check("moe_act_quant", st)
+    dev = _same_device(xb, xq, xs, t_live)
+    _enqueue("moe_act_quant", dev, _ptr(xb), t_cap, _live(t_live), hidden, _fmt(fmt),
+             _rounding(rounding), _ptr(xq), _ptr(xs))
     return xq, xs
 
 
@@ -394,12 +414,10 @@ def moe_grouped_gemm_fp8(a, a_scales, fmt, w, w_scales, counts, offsets, row_cap
         raise ValueError("without a row map, a needs row_cap rows")
     if tiles_visited is not None:
         _min_numel(_need(tiles_visited, "tiles_visited", torch.int32), "tiles_visited", 1)
-    _same_device(a, a_scales, w, w_scales, counts, offsets, ob, a_row_map, tiles_visited)
-    st = lib.moe_grouped_gemm_fp8(_ptr(a), _ptr(a_scales), _fmt(fmt), a_rows, _ptr(a_row_map),
-                                  a_row_div, _ptr(w), _ptr(w_scales), _ptr(counts),
-                                  _ptr(offsets), num_experts, row_cap, max_rows_per_expert, n, k,
-                                  _ptr(ob), _ptr(tiles_visited), _stream())
-    _check("moe_grouped_gemm_fp8", st)
+    dev = _same_device(a, a_scales, w, w_scales, counts, offsets, ob, a_row_map, tiles_visited)
+    _enqueue("moe_grouped_gemm_fp8", dev, _ptr(a), _ptr(a_scales), _fmt(fmt), a_rows,
+             _ptr(a_row_map), a_row_div, _ptr(w), _ptr(w_scales), _ptr(counts), _ptr(offsets),
+             num_experts, row_cap, max_rows_per_expert, n, k, _ptr(ob), _ptr(tiles_visited))
     return out
 
 
@@ -440,12 +458,10 @@ def moe_grouped_gemm_mxfp4(a, a_scales, fmt, w, w_scales, counts, offsets=None, 
         _min_numel(_need(a_row_map, "a_row_map", torch.int32), "a_row_map", row_cap)
     elif a_rows < row_cap:
         raise ValueError("without a row map, a needs row_cap rows")
-    _same_device(a, a_scales, w, w_scales, counts, offsets, ob, a_row_map)
-    st = lib.moe_grouped_gemm_mxfp4(_ptr(a), _ptr(a_scales), _fmt(fmt), a_rows, _ptr(a_row_map),
-                                    a_row_div, _ptr(w), _ptr(w_scales), _ptr(counts),
-                                    _ptr(offsets), int(expert_cap), num_experts, row_cap,
-                                    int(max_rows_per_expert), n, k, _ptr(ob), _stream())
-    _check("moe_grouped_gemm_mxfp4", st)
+    dev = _same_device(a, a_scales, w, w_scales, counts, offsets, ob, a_row_map)
+    _enqueue("moe_grouped_gemm_mxfp4", dev, _ptr(a), _ptr(a_scales), _fmt(fmt), a_rows,
+             _ptr(a_row_map), a_row_div, _ptr(w), _ptr(w_scales), _ptr(counts), _ptr(offsets),
+             int(expert_cap), num_experts, row_cap, int(max_rows_per_expert), n, k, _ptr(ob))
     return out
 
 
@@ -477,12 +493,10 @@ def moe_grouped_gemm_fp8_masked(a, a_scales, fmt, w, w_scales, masked_m, expert_
         raise ValueError("without a row map, a needs num_experts * expert_cap rows")
     if tiles_visited is not None:
         _min_numel(_need(tiles_visited, "tiles_visited", torch.int32), "tiles_visited", 1)
-    _same_device(a, a_scales, w, w_scales, masked_m, ob, a_row_map, tiles_visited)
-    st = lib.moe_grouped_gemm_fp8_masked(_ptr(a), _ptr(a_scales), _fmt(fmt), a_rows,
-                                         _ptr(a_row_map), a_row_div, _ptr(w), _ptr(w_scales),
-                                         _ptr(masked_m), num_experts, expert_cap, n, k, _ptr(ob),
-                                         _ptr(tiles_visited), _stream())
-    _check("moe_grouped_gemm_fp8_masked", st)
+    dev = _same_device(a, a_scales, w, w_scales, masked_m, ob, a_row_map, tiles_visited)
+    _enqueue("moe_grouped_gemm_fp8_masked", dev, _ptr(a), _ptr(a_scales), _fmt(fmt), a_rows,
+             _ptr(a_row_map), a_row_div, _ptr(w), _ptr(w_scales), _ptr(masked_m), num_experts,
+             expert_cap, n, k, _ptr(ob), _ptr(tiles_visited))
     return out
 
 
@@ -506,13 +520,12 @@ def moe_silu_mul_quant_masked(gate_up, masked_m, expert_cap, act="swiglu",
         hs = torch.empty(_scale_shape(rows, inter, fmt), dtype=_scale_dtype(fmt), device=gu.device)
     _shape(_need(hq, "hq", torch.uint8), "hq", (rows, _code_cols(inter, fmt)))
     _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", _scale_shape(rows, inter, fmt))
-    _same_device(gu, masked_m, hq, hs)
+    dev = _same_device(gu, masked_m, hq, hs)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
-    st = lib.moe_silu_mul_quant_masked(_ptr(gu), inter, _ptr(masked_m), num_experts, expert_cap,
-                                       ACTS[act], float(clamp_limit), _fmt(fmt),
-                                       _rounding(rounding), _ptr(hq), _ptr(hs), _stream())
-    _check("moe_silu_mul_quant_masked", st)
+    _enqueue("moe_silu_mul_quant_masked", dev, _ptr(gu), inter, _ptr(masked_m), num_experts,
+             expert_cap, ACTS[act], float(clamp_limit), _fmt(fmt), _rounding(rounding), _ptr(hq),
+             _ptr(hs))
     return hq, hs
 
 
@@ -536,13 +549,12 @@ def moe_silu_mul_quant(gate_up, counts, offsets, act="swiglu", clamp_limit=float
         hs = torch.empty(_scale_shape(row_cap, inter, fmt), dtype=_scale_dtype(fmt), device=gu.device)
     _shape(_need(hq, "hq", torch.uint8), "hq", (row_cap, _code_cols(inter, fmt)))
     _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", _scale_shape(row_cap, inter, fmt))
-    _same_device(gu, counts, offsets, hq, hs)
+    dev = _same_device(gu, counts, offsets, hq, hs)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
-    st = lib.moe_silu_mul_quant(_ptr(gu), inter, _ptr(counts), _ptr(offsets), num_experts,
-                                row_cap, ACTS[act], float(clamp_limit), _fmt(fmt),
-                                _rounding(rounding), _ptr(hq), _ptr(hs), _stream())
-    _check("moe_silu_mul_quant", st)
+    _enqueue("moe_silu_mul_quant", dev, _ptr(gu), inter, _ptr(counts), _ptr(offsets), num_experts,
+             row_cap, ACTS[act], float(clamp_limit), _fmt(fmt), _rounding(rounding), _ptr(hq),
+             _ptr(hs))
     return hq, hs
 
 
@@ -559,10 +571,9 @@ def moe_topk_combine(y, pair_to_row, topk_w, t_live=None, out=None):
     if out is None:
         out = torch.empty((t_cap, hidden), dtype=torch.int16, device=yb.device)
     ob = _shape(_bf16_view(out, "out"), "out", (t_cap, hidden))
-    _same_device(yb, pair_to_row, w, ob)
-    st = lib.moe_topk_combine(_ptr(yb), row_cap, _ptr(pair_to_row), _ptr(w), t_cap, _live(t_live),
-                              topk, hidden, _ptr(ob), _stream())
-    _check("moe_topk_combine", st)
+    dev = _same_device(yb, pair_to_row, w, ob)
+    _enqueue("moe_topk_combine", dev, _ptr(yb), row_cap, _ptr(pair_to_row), _ptr(w), t_cap,
+             _live(t_live), topk, hidden, _ptr(ob))
     return out
 
 
@@ -665,12 +676,11 @@ def moe_forward(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="fp32", a
     ob = _shape(_bf16_view(out, "out"), "out", (t_cap, hidden))
     if t_live is not None:
         _shape(_need(t_live, "t_live", torch.int32), "t_live", (1,))
-    _same_device(xb, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, ob, workspace, t_live)
+    dev = _same_device(xb, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, ob, workspace, t_live)
     tens = _Tensors(_ptr(xb), _ptr(topk_ids), _ptr(topk_w), _live(t_live), _ptr(w1),
                     _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(ob))
-    st = lib.moe_forward(ctypes.byref(prob), ctypes.byref(tens), _ptr(workspace),
-                         workspace.numel(), _stream())
-    _check("moe_forward", st)
+    _enqueue("moe_forward", dev, ctypes.byref(prob), ctypes.byref(tens), _ptr(workspace),
+             workspace.numel())
     return out, workspace
 
 
@@ -702,13 +712,12 @@ def moe_forward_noalloc(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="
     ob = _shape(_bf16_view(out, "out"), "out", (t_cap, hidden))
     if t_live is not None:
         _shape(_need(t_live, "t_live", torch.int32), "t_live", (1,))
-    _same_device(xb, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, ob, t_live)
+    dev = _same_device(xb, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, ob, t_live)
     prob = _problem(num_experts, hidden, inter, topk, t_cap, align_rows, row_cap, fmt, act,
                     clamp_limit, rounding, expert_start, expert_cap, weight_fmt)
     tens = _Tensors(_ptr(xb), _ptr(topk_ids), _ptr(topk_w), _live(t_live), _ptr(w1),
                     _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(ob))
-    _check("moe_forward_noalloc", lib.moe_forward_noalloc(ctypes.byref(prob), ctypes.byref(tens),
-                                                          _stream()))
+    _enqueue("moe_forward_noalloc", dev, ctypes.byref(prob), ctypes.byref(tens))
     return out
 
 
@@ -733,12 +742,11 @@ def moe_fc1_decode(x, topk_ids, w1, w1_scales, inter, fmt="fp32", act="swiglu",
     _need(workspace, "workspace", torch.uint8)
     if t_live is not None:
         _shape(_need(t_live, "t_live", torch.int32), "t_live", (1,))
-    _same_device(xb, topk_ids, w1, w1_scales, workspace, t_live)
+    dev = _same_device(xb, topk_ids, w1, w1_scales, workspace, t_live)
     tens = _Tensors(_ptr(xb), _ptr(topk_ids), None, _live(t_live), _ptr(w1), _ptr(w1_scales),
                     None, None, None)
-    st = lib.moe_fc1_decode(ctypes.byref(prob), ctypes.byref(tens), _ptr(workspace),
-                            workspace.numel(), _stream())
-    _check("moe_fc1_decode", st)
+    _enqueue("moe_fc1_decode", dev, ctypes.byref(prob), ctypes.byref(tens), _ptr(workspace),
+             workspace.numel())
     return workspace
 
 

@@ -98,11 +98,13 @@ __host__ __device__ constexpr int l4_scale_stride(int hidden) { return hidden / 
 __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];  // a pass's tokens
   __shared__ __attribute__((aligned(16))) v4f s_part[kL1Waves][4][64];
+  __shared__ int s_pair[16];  // the pass's tokens' pairs
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int PQ = a.t_cap * a.topk;
   const int pair = blockIdx.y;
+  const int lane_token = lane / a.topk;
   // Which expert, and for which pairs.
   const int t_live = clamp_live(a.t_live_dev, a.t_cap);
   const int id = lane < PQ ? a.ids[lane] - a.expert_start : -1;
@@ -118,12 +120,12 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
   const int chunks = (H + 255) / 256;
   const int ch0 = l4_split(chunks, wave, kL1Waves), ch1 = l4_split(chunks, wave + 1, kL1Waves);
   // Row tiles: gate rows col0 .. +15, +16 .. +31, then the up rows.
-  const int64_t row0 = static_cast<int64_t>(e) * 2 * I + col0;
+  const int64_t first = static_cast<int64_t>(e) * 2 * I + col0;
   const uint8_t* wb[4];
   const uint8_t* sb[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t row = row0 + (i >> 1) * I + (i & 1) * 16;
+    const int64_t row = first + (i >> 1) * I + (i & 1) * 16;
     wb[i] = a.w1 + row * (H / 2);
     sb[i] = a.w1_scales + row * (H / kMxBlock);
   }
@@ -148,34 +150,55 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
 #pragma unroll
       for (int i = 0; i < 4; ++i) l4_load(f[i], wb[i], wrow, sb[i], srow, c, l);
     };
-    // The pass's tokens to LDS, 8 values per item. The first items' loads go
-    // out ahead of the weights (loads return in order).
-    const int per = H / 8, items = nt * per;
-    auto load_item = [&](int i) {
-      const int k = i / per;
-      const int q = nth_bit(mine, t0 + k);
-      return *reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(q / a.topk) * H + (i - k * per) * 8);
+    // The pass's tokens to LDS, 8 values per thread and step. The loads of the
+    // first two tokens' first two steps go out ahead of the weights (loads
+    // return in order).
+    const int per = H / 8;
+    uint64_t left = mine;
+    for (int i = 0; i < t0; ++i) left &= left - 1;
+    auto next_pair = [&]() {
+      const int q = __builtin_ctzll(left);
+      left &= left - 1;
+      return q;
     };
-    auto store_item = [&](int i, uint4 raw) {
-      const int k = i / per, c = i - k * per;
+    auto row_of = [&](int q) { return a.x + static_cast<int64_t>(__builtin_amdgcn_readlane(lane_token, q)) * H; };
+    auto load_item = [&](const uint16_t* row, int c) {
+      return *reinterpret_cast<const uint4*>(row + min(c, per - 1) * 8);
+    };
+    auto store_item = [&](int k, int c, uint4 raw) {
       uint32_t byte;
       const uint32_t codes = mx_quantize8_bf16(raw, &byte);
-      if (i >= items) return;  // whole quads: items is a multiple of 16
+      if (c >= per) return;  // whole quads: per is a multiple of 16
       *reinterpret_cast<uint32_t*>(s_x + k * XS + c * 4) = codes;
       if ((c & 3) == 0) s_xs[k * XB + (c >> 2)] = static_cast<uint8_t>(byte);
     };
-    const uint4 raw0 = load_item(min(tl, items - 1)), raw1 = load_item(min(tl + kL1Threads, items - 1));
+    const int q0 = next_pair(), q1 = nt > 1 ? next_pair() : q0;
+    const uint16_t *row0 = row_of(q0), *row1 = row_of(q1);
+    const uint4 raw00 = load_item(row0, tl), raw01 = load_item(row0, tl + kL1Threads);
+    const uint4 raw10 = load_item(row1, tl), raw11 = load_item(row1, tl + kL1Threads);
     __builtin_amdgcn_sched_barrier(0);
     load(ch0, w[0]);
     load(ch0 + 1, w[1]);
     __builtin_amdgcn_sched_barrier(0);
-    store_item(tl, raw0);
-    store_item(tl + kL1Threads, raw1);
-    for (int i = tl + 2 * kL1Threads; i < items; i += 2 * kL1Threads) {
-      const int i1 = i + kL1Threads;
-      const uint4 r0 = load_item(i), r1 = load_item(min(i1, items - 1));
-      store_item(i, r0);
-      store_item(i1, r1);
+    store_item(0, tl, raw00);
+    if (per > kL1Threads) store_item(0, tl + kL1Threads, raw01);
+    if (nt > 1) {
+      store_item(1, tl, raw10);
+      if (per > kL1Threads) store_item(1, tl + kL1Threads, raw11);
+    }
+    if (tl == 0) {
+      s_pair[0] = q0;
+      s_pair[1] = q1;
+    }
+    for (int k = per > 2 * kL1Threads ? 0 : 2; k < nt; ++k) {
+      const int q = k == 0 ? q0 : (k == 1 ? q1 : next_pair());
+      const uint16_t* row = row_of(q);
+      for (int c = k < 2 ? tl + 2 * kL1Threads : tl; c - tl < per; c += 2 * kL1Threads) {
+        const uint4 r0 = load_item(row, c), r1 = load_item(row, c + kL1Threads);
+        store_item(k, c, r0);
+        if (c - tl + kL1Threads < per) store_item(k, c + kL1Threads, r1);
+      }
+      if (tl == 0) s_pair[k] = q;
     }
     lds_barrier();  // (leaves the weights in flight)
     v4f acc[4] = {};
@@ -204,40 +227,40 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
 #pragma unroll
     for (int i = 0; i < 4; ++i) s_part[wave][i][lane] = acc[i];
     __syncthreads();
-    // Thread (token, column): 32 lanes hold a token's 32 columns. The shares
-    // add in wave order. Value (column c, token k) of a tile pair lies in tile
-    // c / 16, lane 16 (c % 16 / 4) + k, element c % 4.
-    {
-      const int k = tl >> 5, c = tl & 31;
+    // The shares add in wave order, a value quartet per thread.
+    if (tl < 256) {
+      v4f sum = s_part[0][tl >> 6][lane];
+#pragma unroll
+      for (int w = 1; w < kL1Waves; ++w) sum += s_part[w][tl >> 6][lane];
+      s_part[0][tl >> 6][lane] = sum;
+    }
+    __syncthreads();
+    // Thread (token, column): 32 lanes hold a token's 32 columns. Value
+    // (column c, token k) of a tile pair lies in tile c / 16, lane 16 (c % 16 /
+    // 4) + k, element c % 4.
+    const int k = tl >> 5, c = tl & 31;
+    if (k < nt) {
       const int src = 16 * ((c & 15) >> 2) + k;
-      float gate = 0.0f, up = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kL1Waves; ++w) {
-        gate += s_part[w][c >> 4][src][c & 3];
-        up += s_part[w][2 + (c >> 4)][src][c & 3];
-      }
-      const uint2 b = pack_bf16x4(v4f{gate, up, 0.0f, 0.0f});  // C1 is BF16
+      const uint2 b = pack_bf16x4(v4f{s_part[0][c >> 4][src][c & 3], s_part[0][2 + (c >> 4)][src][c & 3], 0.0f, 0.0f});  // C1 is BF16
       const float y = swiglu_any(a.act, bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), a.act_limit, a.rounding);
-      uint32_t amax = __float_as_uint(y) & 0x7FFFFFFFu;
+      // The block's largest magnitude, over the 32 lanes that hold it (all or
+      // none of them are here).
+      uint32_t amax = quad_max_u32(__float_as_uint(y) & 0x7FFFFFFFu);
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
+      for (int d = 4; d < 32; d <<= 1) {
         const uint32_t o = __shfl_xor(static_cast<int>(amax), d, 64);
         amax = o > amax ? o : amax;
       }
       const uint32_t byte = mx_scale_byte(amax);
-      // Lane c even packs columns c and c + 1; every fourth pair's first lane
-      // stores four bytes.
+      // Lane c even packs columns c and c + 1; every eighth stores four bytes.
       const float y1 = __shfl_xor(y, 1, 64);
       uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y, y1, mx_scale_float(byte), 0) & 0xFFu;
       if (byte == 255u) code = 0;
       code |= __shfl_xor(static_cast<int>(code), 2, 64) << 8;
       code |= __shfl_xor(static_cast<int>(code), 4, 64) << 16;
-      if (t0 + k < n_tok) {
-        const int q = nth_bit(mine, t0 + k);
-        const int64_t at = static_cast<int64_t>(q) * I + col0;
-        if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + at / 2 + c / 2) = code;
-        if (c == 0) a.hs[at / kMxBlock] = static_cast<uint8_t>(byte);
-      }
+      const int64_t at = static_cast<int64_t>(s_pair[k]) * I + col0;
+      if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + at / 2 + c / 2) = code;
+      if (c == 0) a.hs[at / kMxBlock] = static_cast<uint8_t>(byte);
     }
     __syncthreads();  // the partials are free for the next 16 tokens
   }
@@ -319,18 +342,26 @@ __global__ __launch_bounds__(kL2Threads, 4) void layer_a4_fc2_kernel(LayerA4Args
   for (int i = tid; i < t_live * 8; i += kL2Threads) {
     const int t = i >> 3, c = (i & 7) * 2;
     float o0 = 0.0f, o1 = 0.0f;
-    for (int k = 0; k < TK; ++k) {
-      const int q = t * TK + k;
-      if (!s_ok[q]) continue;
-      float y0 = 0.0f, y1 = 0.0f;
-      for (int s = 0; s < S; ++s) {
-        const float2 v = *reinterpret_cast<const float2*>(s_slot + (s * PQ + q) * 16 + c);
-        y0 += v.x;
-        y1 += v.y;
+    for (int k0 = 0; k0 < TK; k0 += 4) {  // four pairs' reads together
+      float y0[4], y1[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y0[j] = y1[j] = 0.0f;
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int q = t * TK + min(k0 + j, TK - 1);
+          const float2 v = *reinterpret_cast<const float2*>(s_slot + (s * PQ + q) * 16 + c);
+          y0[j] += v.x;
+          y1[j] += v.y;
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = t * TK + min(k0 + j, TK - 1);
+        if (k0 + j >= TK || !s_ok[q]) continue;
+        const uint2 b = pack_bf16x4(v4f{y0[j], y1[j], 0.0f, 0.0f});
+        o0 = fmaf(s_w[q], bf16_to_f32(b.x & 0xFFFFu), o0);
+        o1 = fmaf(s_w[q], bf16_to_f32(b.x >> 16), o1);
       }
-      const uint2 b = pack_bf16x4(v4f{y0, y1, 0.0f, 0.0f});
-      o0 = fmaf(s_w[q], bf16_to_f32(b.x & 0xFFFFu), o0);
-      o1 = fmaf(s_w[q], bf16_to_f32(b.x >> 16), o1);
     }
     const uint2 b = pack_bf16x4(v4f{o0, o1, 0.0f, 0.0f});
     *reinterpret_cast<uint32_t*>(a.out + static_cast<int64_t>(t) * H + n0 + c) = b.x;
