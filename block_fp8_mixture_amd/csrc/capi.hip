@@ -296,7 +296,7 @@ static moe_status gemm_w4_checked(const moe::W4Args& g, void* stream) {
   if (!g.counts || (!g.offsets && g.seg_cap == 0) || !g.w || !g.w_scales) return MOE_ERR_INVALID_ARG;
   if (g.row_cap > 0 && (!g.c || !g.a || !g.a_scales || g.a_rows < 1)) return MOE_ERR_INVALID_ARG;
   if (g.fmt == MOE_SCALE_MXFP4 && !(aligned(g.a, 16) && aligned(g.w, 16) && aligned(g.c, 16) &&
-                                    aligned(g.a_scales, 4) && aligned(g.w_scales, 4)))
+                                    aligned(g.a_scales, 16) && aligned(g.w_scales, 16)))
     return MOE_ERR_INVALID_ARG;
   if (g.row_cap == 0) return MOE_OK;
   return from_hip(moe::launch_grouped_gemm_w4(g, as_stream(stream)));
@@ -564,8 +564,8 @@ static moe_status forward_impl(const moe_problem* p, const moe_workspace_layout&
                        !t->w2 || !t->w2_scales || !t->out))
     return MOE_ERR_INVALID_ARG;
   if (p->t_cap > 0 && p->scale_fmt == MOE_SCALE_MXFP4 &&
-      !(aligned(t->x, 16) && aligned(t->w1, 16) && aligned(t->w2, 16) && aligned(t->w1_scales, 4) &&
-        aligned(t->w2_scales, 4) && aligned(t->out, 16) && aligned(workspace, 16)))
+      !(aligned(t->x, 16) && aligned(t->w1, 16) && aligned(t->w2, 16) && aligned(t->w1_scales, 16) &&
+        aligned(t->w2_scales, 16) && aligned(t->out, 16) && aligned(workspace, 16)))
     return MOE_ERR_INVALID_ARG;
   if (p->t_cap == 0) return MOE_OK;
 

@@ -332,7 +332,7 @@ moe_status moe_grouped_gemm_fp8_masked(const uint8_t* a, const void* a_scales, m
  * With fmt MOE_SCALE_MXFP4 A is an MXFP4 tensor (a [a_rows, k/2], a_scales
  * [a_rows, k/32]), and the matrix cores apply both operands' scales:
  *   C[r, n] = bf16( sum_j a(ar, j) * w(e, n, j) ), accumulated in fp32.
- * a, w and c are then 16-byte aligned and the scales 4-byte aligned.
+ * All of a, a_scales, w, w_scales and c are then 16-byte aligned.
  *
  *   a, a_scales, fmt, a_rows, a_row_map, a_row_div   as moe_grouped_gemm_fp8
  *   w          device uint8 [num_experts, n, k/2] packed E2M1 codes
@@ -529,8 +529,8 @@ size_t moe_workspace_bytes(const moe_problem* p);
  * within the GEMM tolerance.
  * With scale_fmt MOE_SCALE_MXFP4 (weight_fmt must be MOE_WEIGHT_MXFP4, else
  * UNSUPPORTED) both activation quantizations are MXFP4 and both GEMMs
- * moe_grouped_gemm_mxfp4's with MXFP4 activations; x, w1, w2, out and the
- * workspace are then 16-byte aligned and the weight scales 4-byte aligned.
+ * moe_grouped_gemm_mxfp4's with MXFP4 activations; x, w1, w2, their scales,
+ * out and the workspace are then 16-byte aligned.
  * `workspace` is device memory of at least moe_workspace_bytes(p) bytes, laid
  * out as moe_workspace_plan describes; its prior contents do not matter.
  * Errors: INVALID_ARG, CAPACITY (workspace or row_cap too small), HIP. */

@@ -14,6 +14,7 @@ OK, INVALID, UNSUPPORTED, CAPACITY = 0, 1, 2, 3
 NULL = None
 FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: validation fails first
 ODD = ctypes.c_void_p(0x1002)
+EIGHT = ctypes.c_void_p(0x1008)  # every MXFP4 operand is at a multiple of 16
 MX = 4
 
 
@@ -76,7 +77,7 @@ def test_mxfp4_gemm_alignment(lib):
     def call(a=FAKE, asc=FAKE, w=FAKE, ws=FAKE, c=FAKE, n=256, k=256, rc=64):
         return f(a, asc, MX, 64, NULL, 1, w, ws, FAKE, FAKE, 0, 4, rc, 0, n, k, c, NULL)
     for bad in (dict(a=ODD), dict(w=ODD), dict(c=ODD), dict(asc=ODD), dict(ws=ODD), dict(asc=NULL),
-                dict(n=200), dict(k=64)):
+                dict(a=EIGHT), dict(w=EIGHT), dict(c=EIGHT), dict(asc=EIGHT), dict(ws=EIGHT), dict(n=200), dict(k=64)):
         assert call(**bad) == INVALID, bad
     assert call(rc=0) == OK
 
@@ -116,6 +117,15 @@ def test_forward_refuses_misaligned_tensors(lib):
 
 
 # ---- the binding --------------------------------------------------------------
+
+@pytest.mark.parametrize("name", ["x", "w1", "w2", "out", "w1_scales", "w2_scales"])
+def test_forward_refuses_tensors_at_odd_multiples_of_eight(lib, name):
+    p = _problem(t_cap=4)
+    n = lib.moe_workspace_bytes(ctypes.byref(p))
+    names = [f for f, _ in B._Tensors._fields_]
+    t = B._Tensors(*[EIGHT.value if f == name else (None if f == "t_live_dev" else FAKE.value) for f in names])
+    assert lib.moe_forward(ctypes.byref(p), ctypes.byref(t), FAKE, n, NULL) == INVALID
+
 
 def test_route_binding_refusals():
     l = torch.zeros((4, 8))
