@@ -9,6 +9,7 @@
 #include "../../include/moe_fp8.h"
 #include "kernels.h"
 
+static_assert(MOE_MXFP4_FEW_PAIRS == moe::kL4MaxPairs);
 static_assert(MOE_DECODE_MAX_PAIRS == moe::kDcMaxPairs && MOE_DECODE_FC2_ROW_BYTES == moe::kDcTokBytes &&
                   MOE_DECODE_FC2_MAX_SCALES == moe::kDcMaxScales &&
                   MOE_DECODE_LAYER_TOKEN_BYTES == moe::kF1TokBytesWide &&
@@ -588,7 +589,8 @@ static moe_status forward_impl(const moe_problem* p, const moe_workspace_layout&
   const int pairs = static_cast<int>(pairs64);
 
   hipError_t e = hipSuccess;
-  if (p->scale_fmt == MOE_SCALE_MXFP4 && p->expert_cap == 0 && pairs64 <= moe::kL4MaxPairs) {
+  if (p->scale_fmt == MOE_SCALE_MXFP4 && p->expert_cap == 0 &&
+      moe::layer_a4_fits(p->t_cap, p->topk, p->num_experts, p->hidden, p->inter)) {
     // A few tokens: the whole layer in two launches.
     moe::LayerA4Args a;
     a.ids = t->topk_ids;

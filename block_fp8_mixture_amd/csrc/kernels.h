@@ -126,8 +126,15 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream);
 
 // The whole layer with MXFP4 activations and weights for at most kL4MaxPairs
 // routed pairs, in two launches. hq [pairs, I/2] and hs [pairs, I/32] hold the
-// quantized FC2 input between them, a row per pair.
-constexpr int kL4MaxPairs = 64;
+// quantized FC2 input between them, a row per pair. Its two sides, us captured,
+// these launches against the general path's (experts, hidden, inter; pairs):
+//   288, 4096, 512:  8: 15 / 34, 32: 27 / 53, 48: 38 / 71, 64: 50 / 68
+//   32, 7168, 2048:  8: 47 / 77, 32: 118..129 / 142..145, 48: 149 / 153, 64: 167..181 / 157..162
+//   64, 2048, 1024:  6: 16 / 31, 24: 34 / 43, 48: 52 / 50, 64: 61 / 51
+//   16, 4096, 4096:  64: 115..127 / 103..106
+constexpr int kL4MaxPairs = 48;
+static_assert(kL4MaxPairs <= 64);  // a pair per lane
+constexpr size_t kLdsBytes = 160 * 1024;  // of a workgroup
 struct LayerA4Args {
   const int32_t* ids;         // [t_cap, topk]
   const float* topk_w;        // [t_cap, topk]
@@ -149,7 +156,10 @@ struct LayerA4Args {
   uint8_t* hq;
   uint8_t* hs;
   uint16_t* out;              // [t_cap, H]
+  int token_of = 0;           // set by the launcher: pair -> token
 };
+// Whether launch_layer_a4 takes such a layer.
+bool layer_a4_fits(int t_cap, int topk, int num_experts, int hidden, int inter);
 hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream);
 
 // BF16 values of an MXFP4 tensor of rows x cols.

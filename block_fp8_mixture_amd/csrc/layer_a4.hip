@@ -18,6 +18,17 @@
 // the first load then touches all of a row's 128-byte line, so the memory is
 // asked for whole lines (with blocks g and 4 + g, for two halves of each).
 //
+// Measured, captured: 288 experts of 4096 -> 512, top 8: 15.3 us at 1 token
+// (27 MB of weights), 27.2 us at 4 (about 100 MB: 3.7 TB/s over both launches,
+// where a large copy runs at 4.8). Of the first's 15 us about 6 are the bytes;
+// the rest is two launches' ramps, each a chain of ids, weights, quantization,
+// products and a reduction over the waves. 32 experts of 7168 -> 2048: 47 us at
+// 1 token (187 MB, 4.0 TB/s). FC1 is bound by its instructions where the
+// weights are in cache, so its addresses are 32-bit offsets from uniform bases
+// and its tokens are found with scalar operations: with 64-bit addresses, a
+// division per lane and a loop over sets of 16 tokens (which spilled) the same
+// calls took 17.1, 32.8 and 53.1 us.
+//
 // Routing. A pair's workgroups compare its expert with those of all pairs (one
 // id per lane, one ballot): the lowest pair of an expert works for all of its
 // tokens, the others' workgroups leave. No table is built.
@@ -82,7 +93,9 @@ __device__ __forceinline__ uint32_t l4_scales(const L4Frag& f, const L4Lane& l) 
 }
 
 // Chunks of 256 K values that share `s` of `shares` takes.
-__device__ __forceinline__ int l4_split(int chunks, int s, int shares) { return chunks * s / shares; }
+__device__ __forceinline__ int l4_split(int chunks, int s, int shares) {
+  return static_cast<unsigned>(chunks * s) / static_cast<unsigned>(shares);
+}
 
 // The r-th set bit of m (64 if there are fewer).
 __device__ __forceinline__ int nth_bit(uint64_t m, int r) {
@@ -90,21 +103,26 @@ __device__ __forceinline__ int nth_bit(uint64_t m, int r) {
   return m ? __builtin_ctzll(m) : 64;
 }
 
-// LDS of the tokens of a pass: codes and scale bytes, rows padded so that 16
+// LDS of a workgroup's tokens: codes and scale bytes, rows padded so that 16
 // rows' chunks fall on distinct banks.
 __host__ __device__ constexpr int l4_code_stride(int hidden) { return hidden / 2 + 16; }
 __host__ __device__ constexpr int l4_scale_stride(int hidden) { return hidden / kMxBlock + 4; }
 
+size_t l4_token_bytes(int hidden, int t_cap) {
+  return static_cast<size_t>(t_cap < 16 ? t_cap : 16) * (l4_code_stride(hidden) + l4_scale_stride(hidden));
+}
+// What FC1 has beside them: the shares' partial sums and the tokens' pairs.
+constexpr size_t kL1Lds = kL1Waves * 4 * 64 * sizeof(v4f) + 16 * sizeof(uint64_t);
+
 __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];  // a pass's tokens
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];  // the tokens
   __shared__ __attribute__((aligned(16))) v4f s_part[kL1Waves][4][64];
-  __shared__ int s_pair[16];  // the pass's tokens' pairs
+  __shared__ uint64_t s_pairs[16];  // the tokens' pairs with the expert
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int PQ = a.t_cap * a.topk;
   const int pair = blockIdx.y;
-  const int lane_token = lane / a.topk;
   // Which expert, and for which pairs.
   const int t_live = clamp_live(a.t_live_dev, a.t_cap);
   const int id = lane < PQ ? a.ids[lane] - a.expert_start : -1;
@@ -113,9 +131,29 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
   if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.num_experts) || mine == 0 ||
       __builtin_ctzll(mine) != pair)
     return;
-  const int n_tok = __popcll(mine);
+  // Their tokens: a token may have the expert more than once, and its row is
+  // computed once. Sixteen tokens per workgroup (a loop here costs spilled
+  // registers).
+  const uint64_t token_bits = ~uint64_t{0} >> (64 - a.topk);
+  uint64_t left = mine;
+  auto next_token = [&](int* t) {
+    *t = static_cast<int>(static_cast<unsigned>(__builtin_ctzll(left)) * a.token_of >> 16);
+    const uint64_t of = left & token_bits << (*t * a.topk);
+    left ^= of;
+    return of;  // its pairs with this expert
+  };
+  int t;
+  for (unsigned i = 0; i < 16 * blockIdx.z && left; ++i) next_token(&t);
+  if (left == 0) return;
+  const uint64_t pass = left;
+  int nt = 0;
+  while (left && nt < 16) {
+    next_token(&t);
+    ++nt;
+  }
+  left = pass;
 
-  const int H = a.hidden, I = a.inter;
+  const unsigned H = a.hidden, I = a.inter;
   const int col0 = blockIdx.x * 32;
   const int chunks = (H + 255) / 256;
   const int ch0 = l4_split(chunks, wave, kL1Waves), ch1 = l4_split(chunks, wave + 1, kL1Waves);
@@ -129,140 +167,131 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
     wb[i] = a.w1 + row * (H / 2);
     sb[i] = a.w1_scales + row * (H / kMxBlock);
   }
-  uint32_t wrow = r16 * (H / 2), srow = r16 * (H / kMxBlock);
+  const uint32_t wrow = r16 * (H / 2), srow = r16 * (H / kMxBlock);
   const int XS = l4_code_stride(H), XB = l4_scale_stride(H);
-  const int width = min(a.t_cap, 16);  // tokens of a pass, at most
+  const int width = min(a.t_cap, 16);  // tokens of a workgroup, at most
   uint8_t* s_x = s_dyn;
   uint8_t* s_xs = s_dyn + width * XS;
 
-  for (int t0 = 0; t0 < n_tok; t0 += 16) {
-    const int nt = min(16, n_tok - t0);
-    // Opaque to the compiler, which otherwise keeps every address and index of
-    // this (mostly single) pass in registers of its own and spills.
-    int gl = g, tl = tid;
-    asm volatile("" : "+v"(gl), "+v"(tl), "+v"(wrow), "+v"(srow));
-    // The first two chunks' weights go out before anything waits. Chunks past
-    // the share load its last one, unused.
-    L4Frag w[2][4];
-    auto load = [&](int ch, L4Frag (&f)[4]) {
-      const int c = min(ch, max(ch1 - 1, 0));
-      const L4Lane l = l4_lane(gl, c * 256 + 128 >= H);
+  // The first two chunks' weights go out before anything waits. Chunks past
+  // the share load its last one, unused.
+  L4Frag w[2][4];
+  auto load = [&](int ch, L4Frag (&f)[4]) {
+    const int c = min(ch, max(ch1 - 1, 0));
+    const L4Lane l = l4_lane(g, c * 256 + 128 >= H);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l4_load(f[i], wb[i], wrow, sb[i], srow, c, l);
-    };
-    // The pass's tokens to LDS, 8 values per thread and step. The loads of the
-    // first two tokens' first two steps go out ahead of the weights (loads
-    // return in order).
-    const int per = H / 8;
-    uint64_t left = mine;
-    for (int i = 0; i < t0; ++i) left &= left - 1;
-    auto next_pair = [&]() {
-      const int q = __builtin_ctzll(left);
-      left &= left - 1;
-      return q;
-    };
-    auto row_of = [&](int q) { return a.x + static_cast<int64_t>(__builtin_amdgcn_readlane(lane_token, q)) * H; };
-    auto load_item = [&](const uint16_t* row, int c) {
-      return *reinterpret_cast<const uint4*>(row + min(c, per - 1) * 8);
-    };
-    auto store_item = [&](int k, int c, uint4 raw) {
-      uint32_t byte;
-      const uint32_t codes = mx_quantize8_bf16(raw, &byte);
-      if (c >= per) return;  // whole quads: per is a multiple of 16
-      *reinterpret_cast<uint32_t*>(s_x + k * XS + c * 4) = codes;
-      if ((c & 3) == 0) s_xs[k * XB + (c >> 2)] = static_cast<uint8_t>(byte);
-    };
-    const int q0 = next_pair(), q1 = nt > 1 ? next_pair() : q0;
-    const uint16_t *row0 = row_of(q0), *row1 = row_of(q1);
-    const uint4 raw00 = load_item(row0, tl), raw01 = load_item(row0, tl + kL1Threads);
-    const uint4 raw10 = load_item(row1, tl), raw11 = load_item(row1, tl + kL1Threads);
-    __builtin_amdgcn_sched_barrier(0);
-    load(ch0, w[0]);
-    load(ch0 + 1, w[1]);
-    __builtin_amdgcn_sched_barrier(0);
-    store_item(0, tl, raw00);
-    if (per > kL1Threads) store_item(0, tl + kL1Threads, raw01);
-    if (nt > 1) {
-      store_item(1, tl, raw10);
-      if (per > kL1Threads) store_item(1, tl + kL1Threads, raw11);
+    for (int i = 0; i < 4; ++i) l4_load(f[i], wb[i], wrow, sb[i], srow, c, l);
+  };
+  // The tokens to LDS, 8 values per thread and step. The loads of the
+  // first two tokens' first two steps go out ahead of the weights (loads
+  // return in order).
+  const int per = H / 8;
+  auto row_of = [&](int t) { return a.x + static_cast<int64_t>(t) * H; };
+  auto load_item = [&](const uint16_t* row, int c) {
+    return *reinterpret_cast<const uint4*>(row + min(c, per - 1) * 8);
+  };
+  auto store_item = [&](int k, int c, uint4 raw) {
+    uint32_t byte;
+    const uint32_t codes = mx_quantize8_bf16(raw, &byte);
+    if (c >= per) return;  // whole quads: per is a multiple of 16
+    *reinterpret_cast<uint32_t*>(s_x + k * XS + c * 4) = codes;
+    if ((c & 3) == 0) s_xs[k * XB + (c >> 2)] = static_cast<uint8_t>(byte);
+  };
+  int tok0;
+  const uint64_t of0 = next_token(&tok0);
+  int tok1 = tok0;
+  const uint64_t of1 = nt > 1 ? next_token(&tok1) : 0;
+  const uint16_t *row0 = row_of(tok0), *row1 = row_of(tok1);
+  const uint4 raw00 = load_item(row0, tid), raw01 = load_item(row0, tid + kL1Threads);
+  const uint4 raw10 = load_item(row1, tid), raw11 = load_item(row1, tid + kL1Threads);
+  __builtin_amdgcn_sched_barrier(0);
+  load(ch0, w[0]);
+  load(ch0 + 1, w[1]);
+  __builtin_amdgcn_sched_barrier(0);
+  store_item(0, tid, raw00);
+  if (per > kL1Threads) store_item(0, tid + kL1Threads, raw01);
+  if (nt > 1) {
+    store_item(1, tid, raw10);
+    if (per > kL1Threads) store_item(1, tid + kL1Threads, raw11);
+  }
+  if (tid == 0) {
+    s_pairs[0] = of0;
+    s_pairs[1] = of1;
+  }
+  for (int k = per > 2 * kL1Threads ? 0 : 2; k < nt; ++k) {
+    uint64_t of = 0;
+    if (k >= 2) of = next_token(&t);
+    const uint16_t* row = row_of(k == 0 ? tok0 : (k == 1 ? tok1 : t));
+    for (int c = k < 2 ? tid + 2 * kL1Threads : tid; c - tid < per; c += 2 * kL1Threads) {
+      const uint4 r0 = load_item(row, c), r1 = load_item(row, c + kL1Threads);
+      store_item(k, c, r0);
+      if (c - tid + kL1Threads < per) store_item(k, c + kL1Threads, r1);
     }
-    if (tl == 0) {
-      s_pair[0] = q0;
-      s_pair[1] = q1;
+    if (tid == 0 && k >= 2) s_pairs[k] = of;
+  }
+  lds_barrier();  // (leaves the weights in flight)
+  v4f acc[4] = {};
+  // Columns past the tokens repeat the last.
+  const uint32_t xrow = min(r16, nt - 1) * XS, xsrow = min(r16, nt - 1) * XB;
+  auto products = [&](int ch, const L4Frag (&f)[4]) {
+    const L4Lane l = l4_lane(g, ch * 256 + 128 >= H);
+    L4Frag x;
+    l4_load(x, s_x, xrow, s_xs, xsrow, ch, l);
+    const uint32_t xs = l4_scales(x, l), m = l.second;
+    const uint4 x1 = {x.c[1].x & m, x.c[1].y & m, x.c[1].z & m, x.c[1].w & m};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = mfma_l4<0>(f[i].c[0], l4_scales(f[i], l), x.c[0], xs, acc[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = mfma_l4<1>(f[i].c[1], l4_scales(f[i], l), x1, xs, acc[i]);
+  };
+  int ch = ch0;
+  for (; ch + 2 < ch1; ch += 2) {
+    products(ch, w[0]);
+    load(ch + 2, w[0]);
+    products(ch + 1, w[1]);
+    load(ch + 3, w[1]);
+  }
+  if (ch < ch1) products(ch, w[0]);
+  if (ch + 1 < ch1) products(ch + 1, w[1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s_part[wave][i][lane] = acc[i];
+  __syncthreads();
+  // The shares add in wave order, a value quartet per thread.
+  if (tid < 256) {
+    v4f sum = s_part[0][tid >> 6][lane];
+#pragma unroll
+    for (int w = 1; w < kL1Waves; ++w) sum += s_part[w][tid >> 6][lane];
+    s_part[0][tid >> 6][lane] = sum;
+  }
+  __syncthreads();
+  // Thread (token, column): 32 lanes hold a token's 32 columns. Value
+  // (column c, token k) of a tile pair lies in tile c / 16, lane 16 (c % 16 /
+  // 4) + k, element c % 4.
+  const int k = tid >> 5, c = tid & 31;
+  if (k < nt) {
+    const int src = 16 * ((c & 15) >> 2) + k;
+    const uint2 b = pack_bf16x4(v4f{s_part[0][c >> 4][src][c & 3], s_part[0][2 + (c >> 4)][src][c & 3], 0.0f, 0.0f});  // C1 is BF16
+    const float y = swiglu_any(a.act, bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), a.act_limit, a.rounding);
+    // The block's largest magnitude, over the 32 lanes that hold it (all or
+    // none of them are here).
+    uint32_t amax = quad_max_u32(__float_as_uint(y) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_xor(static_cast<int>(amax), d, 64);
+      amax = o > amax ? o : amax;
     }
-    for (int k = per > 2 * kL1Threads ? 0 : 2; k < nt; ++k) {
-      const int q = k == 0 ? q0 : (k == 1 ? q1 : next_pair());
-      const uint16_t* row = row_of(q);
-      for (int c = k < 2 ? tl + 2 * kL1Threads : tl; c - tl < per; c += 2 * kL1Threads) {
-        const uint4 r0 = load_item(row, c), r1 = load_item(row, c + kL1Threads);
-        store_item(k, c, r0);
-        if (c - tl + kL1Threads < per) store_item(k, c + kL1Threads, r1);
-      }
-      if (tl == 0) s_pair[k] = q;
-    }
-    lds_barrier();  // (leaves the weights in flight)
-    v4f acc[4] = {};
-    // Columns past the tokens repeat the last.
-    const uint32_t xrow = min(r16, nt - 1) * XS, xsrow = min(r16, nt - 1) * XB;
-    auto products = [&](int ch, const L4Frag (&f)[4]) {
-      const L4Lane l = l4_lane(gl, ch * 256 + 128 >= H);
-      L4Frag x;
-      l4_load(x, s_x, xrow, s_xs, xsrow, ch, l);
-      const uint32_t xs = l4_scales(x, l), m = l.second;
-      const uint4 x1 = {x.c[1].x & m, x.c[1].y & m, x.c[1].z & m, x.c[1].w & m};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = mfma_l4<0>(f[i].c[0], l4_scales(f[i], l), x.c[0], xs, acc[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = mfma_l4<1>(f[i].c[1], l4_scales(f[i], l), x1, xs, acc[i]);
-    };
-    int ch = ch0;
-    for (; ch + 2 < ch1; ch += 2) {
-      products(ch, w[0]);
-      load(ch + 2, w[0]);
-      products(ch + 1, w[1]);
-      load(ch + 3, w[1]);
-    }
-    if (ch < ch1) products(ch, w[0]);
-    if (ch + 1 < ch1) products(ch + 1, w[1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[wave][i][lane] = acc[i];
-    __syncthreads();
-    // The shares add in wave order, a value quartet per thread.
-    if (tl < 256) {
-      v4f sum = s_part[0][tl >> 6][lane];
-#pragma unroll
-      for (int w = 1; w < kL1Waves; ++w) sum += s_part[w][tl >> 6][lane];
-      s_part[0][tl >> 6][lane] = sum;
-    }
-    __syncthreads();
-    // Thread (token, column): 32 lanes hold a token's 32 columns. Value
-    // (column c, token k) of a tile pair lies in tile c / 16, lane 16 (c % 16 /
-    // 4) + k, element c % 4.
-    const int k = tl >> 5, c = tl & 31;
-    if (k < nt) {
-      const int src = 16 * ((c & 15) >> 2) + k;
-      const uint2 b = pack_bf16x4(v4f{s_part[0][c >> 4][src][c & 3], s_part[0][2 + (c >> 4)][src][c & 3], 0.0f, 0.0f});  // C1 is BF16
-      const float y = swiglu_any(a.act, bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), a.act_limit, a.rounding);
-      // The block's largest magnitude, over the 32 lanes that hold it (all or
-      // none of them are here).
-      uint32_t amax = quad_max_u32(__float_as_uint(y) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        const uint32_t o = __shfl_xor(static_cast<int>(amax), d, 64);
-        amax = o > amax ? o : amax;
-      }
-      const uint32_t byte = mx_scale_byte(amax);
-      // Lane c even packs columns c and c + 1; every eighth stores four bytes.
-      const float y1 = __shfl_xor(y, 1, 64);
-      uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y, y1, mx_scale_float(byte), 0) & 0xFFu;
-      if (byte == 255u) code = 0;
-      code |= __shfl_xor(static_cast<int>(code), 2, 64) << 8;
-      code |= __shfl_xor(static_cast<int>(code), 4, 64) << 16;
-      const int64_t at = static_cast<int64_t>(s_pair[k]) * I + col0;
+    const uint32_t byte = mx_scale_byte(amax);
+    // Lane c even packs columns c and c + 1; every eighth stores four bytes.
+    const float y1 = __shfl_xor(y, 1, 64);
+    uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y, y1, mx_scale_float(byte), 0) & 0xFFu;
+    if (byte == 255u) code = 0;
+    code |= __shfl_xor(static_cast<int>(code), 2, 64) << 8;
+    code |= __shfl_xor(static_cast<int>(code), 4, 64) << 16;
+    for (uint64_t to = s_pairs[k]; to; to &= to - 1) {
+      const int64_t at = static_cast<int64_t>(__builtin_ctzll(to)) * I + col0;
       if ((c & 7) == 0) *reinterpret_cast<uint32_t*>(a.hq + at / 2 + c / 2) = code;
       if (c == 0) a.hs[at / kMxBlock] = static_cast<uint8_t>(byte);
     }
-    __syncthreads();  // the partials are free for the next 16 tokens
   }
 }
 
@@ -271,8 +300,8 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
 // w[t, k] * row, in fp32.
 __global__ __launch_bounds__(kL2Threads, 4) void layer_a4_fc2_kernel(LayerA4Args a) {
   extern __shared__ __attribute__((aligned(16))) float s_slot[];  // [share][pair][16 columns]
-  __shared__ float s_w[kL4MaxPairs];
-  __shared__ int s_ok[kL4MaxPairs];
+  __shared__ float s_w[64];
+  __shared__ int s_ok[64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
@@ -370,12 +399,20 @@ __global__ __launch_bounds__(kL2Threads, 4) void layer_a4_fc2_kernel(LayerA4Args
 
 }  // namespace
 
+bool layer_a4_fits(int t_cap, int topk, int num_experts, int hidden, int inter) {
+  const int64_t pairs = static_cast<int64_t>(t_cap) * topk;
+  return pairs >= 1 && pairs <= kL4MaxPairs && l4_token_bytes(hidden, t_cap) + kL1Lds <= kLdsBytes;
+}
+
 hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream) {
   const int pairs = a.t_cap * a.topk;
-  if (pairs < 1 || pairs > kL4MaxPairs) return hipErrorInvalidValue;
-  const size_t tokens = static_cast<size_t>(a.t_cap < 16 ? a.t_cap : 16) * (l4_code_stride(a.hidden) + l4_scale_stride(a.hidden));
-  hipLaunchKernelGGL(layer_a4_fc1_kernel, dim3(static_cast<unsigned>(a.inter / 32), static_cast<unsigned>(pairs)),
-                     dim3(kL1Threads), tokens, stream, a);
+  if (!layer_a4_fits(a.t_cap, a.topk, a.num_experts, a.hidden, a.inter)) return hipErrorInvalidValue;
+  LayerA4Args p = a;
+  p.token_of = 65536 / a.topk + 1;  // q * token_of >> 16 is q / topk for q < 64, topk <= 64
+  hipLaunchKernelGGL(layer_a4_fc1_kernel,
+                     dim3(static_cast<unsigned>(a.inter / 32), static_cast<unsigned>(pairs),
+                          static_cast<unsigned>((a.t_cap + 15) / 16)),
+                     dim3(kL1Threads), l4_token_bytes(a.hidden, a.t_cap), stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // At most kL2Waves shares in all of experts in use x shares, plus one per

@@ -503,6 +503,8 @@ size_t moe_workspace_bytes(const moe_problem* p);
 #define MOE_DECODE_LAYER_TOKEN_BYTES 61440
 #define MOE_DECODE_LAYER_MAX_SCALES 512
 
+#define MOE_MXFP4_FEW_PAIRS 48
+
 /* The whole expert layer: align -> act_quant -> FC1 -> silu_mul_quant -> FC2
  * -> topk_combine, enqueued on one stream with no host synchronization
  * (vLLM PR #59128, SM100 on B200: the full-expert benchmark scope; the layer
@@ -530,7 +532,11 @@ size_t moe_workspace_bytes(const moe_problem* p);
  * With scale_fmt MOE_SCALE_MXFP4 (weight_fmt must be MOE_WEIGHT_MXFP4, else
  * UNSUPPORTED) both activation quantizations are MXFP4 and both GEMMs
  * moe_grouped_gemm_mxfp4's with MXFP4 activations; x, w1, w2, their scales,
- * out and the workspace are then 16-byte aligned.
+ * out and the workspace are then 16-byte aligned. In the contiguous layout up
+ * to MOE_MXFP4_FEW_PAIRS routed pairs (t_cap * topk; fewer tokens where
+ * hidden is past 15360) go through two launches that keep no state
+ * between calls and build no alignment: of the workspace they write `hq` and
+ * `hs` alone, a row per routed pair.
  * `workspace` is device memory of at least moe_workspace_bytes(p) bytes, laid
  * out as moe_workspace_plan describes; its prior contents do not matter.
  * Errors: INVALID_ARG, CAPACITY (workspace or row_cap too small), HIP. */

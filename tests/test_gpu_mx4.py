@@ -469,6 +469,41 @@ def test_layer_batched_layout_and_odd_row_alignment(li):
     _check_layer(got, ref, live, k)
 
 
+@pytest.mark.parametrize("t,k,e", [(1, 8, 3), (2, 5, 2), (5, 12, 4), (16, 4, 3), (1, 64, 7), (13, 5, 3)])
+def test_layer_of_tokens_that_have_an_expert_more_than_once(t, k, e):
+    say(f"mx4 layer of {t} tokens, {k} choices among {e} experts with repetition")
+    x, ids, w, w1, w2 = _exact_layer(60 + t, t, max(e, k), 384, 256, k)
+    g = _rng(61, t, k)
+    ids = g.integers(0, e, (t, k)).astype(np.int32)
+    ids[0] = ids[0, 0]
+    w1, w2 = (w1[0][:e], w1[1][:e]), (w2[0][:e], w2[1][:e])
+    out = torch.full((t, 384), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_forward(*[up(v) for v in (x, ids, w, *w1, *w2)], "mxfp4", weight_fmt="mxfp4", out=out)
+    ref = oracle.token_forward_mx4(x, ids, w, w1, w2, e, t)
+    _check_layer(down(out), ref, t, k)
+
+
+@pytest.mark.parametrize("t,k,h,i", [(48, 1, 128, 128), (49, 1, 128, 128), (16, 3, 7168, 128), (17, 2, 7168, 128),
+                                     (16, 1, 16384, 128), (1, 2, 32768, 128), (2, 1, 32640, 256),
+                                     (4, 2, 128, 8192)])
+def test_layer_at_the_limits_of_the_few_token_path(t, k, h, i):
+    """48 and 49 pairs; hidden sizes whose tokens do and do not fit the LDS.
+    The sums of _exact_layer are exact to K = 7168 and its FC2 sums short; past
+    that about one block of 32 in 16 is kept, the rest is zeros."""
+    say(f"mx4 layer {t} tokens, top {k}, {h} -> {i}")
+    e = 5
+    x, ids, w, w1, w2 = _exact_layer(70 + t, t, e, h, i, k)
+    g = _rng(71, t, h)
+    if h > 7168:
+        x = x * np.repeat(g.random((t, h // 32)) < 1 / 16, 32, axis=1).astype(x.dtype)
+    if i > 7168:
+        w2[0][:] *= np.repeat(g.random((e, h, i // 32)) < 1 / 16, 16, axis=2).astype(np.uint8)
+    out = torch.full((t, h), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_forward(*[up(v) for v in (x, ids, w, *w1, *w2)], "mxfp4", weight_fmt="mxfp4", out=out)
+    ref = oracle.token_forward_mx4(x, ids, w, w1, w2, e, t)
+    _check_layer(down(out), ref, t, k)
+
+
 @pytest.mark.parametrize("t,e,k", [(3, 12, 4), (100, 12, 4)])
 def test_router_and_layer_captured_and_replayed(t, e, k):
     """Routing and the layer as a user runs them, captured once on a side
