@@ -188,6 +188,8 @@ struct RouteArgs {
   const int32_t* t_live_dev;
   int32_t* ids;            // [t_cap, topk]
   float* weights;          // [t_cap, topk]
+  int group_shift = 0;        // set by the launcher
+  int group_of = 0;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 

@@ -91,6 +91,42 @@ def test_route_matches_oracle(ci, biased, dtype):
     _check_route(l, ref, k, bias, **kw)
 
 
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("tokens", [1, 3, 4, 17])
+@pytest.mark.parametrize("experts,topk,kw", [
+    (2, 1, {}), (16, 16, dict(score="sigmoid")), (17, 17, {}), (32, 2, dict(renormalize=False)),
+    (48, 16, dict(num_groups=16, top_groups=9, group_top=2)), (64, 16, dict(num_groups=4, top_groups=1)),
+    (60, 4, dict(num_groups=3, top_groups=2, group_top=2)), (34, 2, dict(num_groups=17, top_groups=3)),
+    (62, 7, dict(num_groups=31, top_groups=8, group_top=2, score="sigmoid"))])
+def test_route_of_few_experts(experts, topk, kw, tokens, biased):
+    g = _rng(15, experts, topk, tokens)
+    l, ref_l = _as(g.standard_normal((tokens, experts)) * 3, torch.float32)
+    bias = np.float32(g.standard_normal(experts) * 0.3) if biased else None
+    _check_route(l, ref_l, topk, bias=bias, **kw)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("capacity,experts,topk,kw", [
+    (8192, 65, 8, {}), (8191, 65, 8, {}), (8192, 128, 16, dict(score="sigmoid", num_groups=16, top_groups=5)),
+    (8192, 128, 17, {}), (9000, 256, 8, dict(num_groups=8, top_groups=4, group_top=2, score="sigmoid")),
+    (8192, 256, 6, dict(renormalize=False)), (8192, 255, 4, dict(num_groups=17, top_groups=2, group_top=2)),
+    (8192, 257, 3, {})])
+def test_route_of_many_tokens(capacity, experts, topk, kw, biased):
+    """Sizes around those at which fewer lanes take a token; the live count
+    ends inside a wave and the rest of the rows stay as they were."""
+    g = _rng(16, capacity, experts, topk)
+    live = 41
+    l, ref_l = _as(g.standard_normal((capacity, experts)) * 3, torch.bfloat16)
+    bias = np.float32(g.standard_normal(experts) * 0.3) if biased else None
+    ids = torch.full((capacity, topk), POISON_I32, dtype=torch.int32, device=dev())
+    w = torch.full((capacity, topk), 7.0, device=dev())
+    moe.moe_route(l, topk, bias=None if bias is None else up(bias), t_live=_i32([live]), ids=ids, weights=w, **kw)
+    ri, rw = oracle.route(ref_l[:live], topk, bias=bias, **kw)
+    assert np.array_equal(down(ids)[:live], ri)
+    assert np.all(np.abs(down(w)[:live] - rw) <= 2.0 ** -23 * np.abs(rw) + 2.0 ** -149)
+    assert np.all(down(ids)[live:] == POISON_I32) and np.all(down(w)[live:] == 7.0)
+
+
 @pytest.mark.parametrize("kw", [{}, dict(score="sigmoid"), dict(num_groups=4, top_groups=2, group_top=2),
                                 dict(num_groups=4, top_groups=2, renormalize=False)])
 @pytest.mark.parametrize("biased", [False, True])
@@ -112,6 +148,27 @@ def test_route_masks_ties_and_extremes(biased, kw):
         bias = np.zeros(16, np.float32)
         bias[[2, 5, 7, 11]] = [-inf, nan, inf, 0.25]
     say(f"route extremes {kw} bias={biased}")
+    _check_route(up(l), l.astype(np.float64), 6, bias, **kw)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(score="sigmoid"), dict(num_groups=4, top_groups=2, group_top=2),
+                                dict(num_groups=20, top_groups=6, renormalize=False)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_masks_and_ties_of_a_wave_per_token(biased, kw):
+    inf, nan, e = np.inf, np.nan, 160
+    g, i = _rng(17), np.arange(e)
+    rows = [np.full(e, -inf), np.full(e, nan), np.zeros(e), np.where(i == 159, 1.0, -inf),
+            np.where(i % 64 == 7, 3.0, -1.0), np.where(i < 130, -inf, 0.5), np.where(i % 3 == 0, nan, 2.0)]
+    for _ in range(6):
+        r = g.integers(-2, 3, e).astype(np.float64)  # many ties
+        r[g.integers(0, e, 70)] = -inf
+        rows.append(r)
+    l = np.stack(rows).astype(np.float32)
+    bias = None
+    if biased:
+        bias = np.zeros(e, np.float32)
+        bias[[2, 65, 70, 131]] = [-inf, nan, inf, 0.25]
+    say(f"route of a wave per token, extremes {kw} bias={biased}")
     _check_route(up(l), l.astype(np.float64), 6, bias, **kw)
 
 
