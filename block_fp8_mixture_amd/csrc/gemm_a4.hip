@@ -491,7 +491,9 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   // Spreads LDS reads and then loads over a quarter's MFMAs.
   auto spread = [&](auto reads_t, auto loads_t) {
     constexpr int reads = decltype(reads_t)::value, loads = decltype(loads_t)::value;
-    constexpr int rp = (reads + M - 1) / M;  // reads per MFMA
+    // Twice the even rate, so that the last have arrived when the quarter ends
+    // (evenly spread: 0.7 to 1.5 % more for 32768 rows of 7168 -> 4096).
+    constexpr int rp = 2 * ((reads + M - 1) / M);  // reads per MFMA
     constexpr int lp = (loads + M - 1) / M;
     constexpr int l0 = M - (loads + lp - 1) / lp_or_one(lp);
 #pragma unroll
