@@ -328,7 +328,7 @@ __global__ __launch_bounds__(kL2Threads, 4) void layer_a4_fc2_kernel(LayerA4Args
   const int n0 = blockIdx.x * 16;
   const int chunks = (I + 255) / 256;
   int S = 1;
-  while (n_lead * S * 2 <= kL2Waves && S * 2 <= chunks) S *= 2;
+  while (max(n_lead, 1) * S * 2 <= kL2Waves && S * 2 <= chunks) S *= 2;
   for (int task = wave; task < n_lead * S; task += kL2Waves) {
     const int share = task & (S - 1);
     const int lead = nth_bit(leaders, task / S);
@@ -415,8 +415,8 @@ hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream) {
                      dim3(kL1Threads), l4_token_bytes(a.hidden, a.t_cap), stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // At most kL2Waves shares in all of experts in use x shares, plus one per
-  // expert: 16 columns x pairs x shares of them, shares <= 16.
+  // The kernel's shares at their most, with one expert in use: 16 columns of
+  // them per pair.
   const int chunks = (a.inter + 255) / 256;
   int shares = 1;
   while (shares * 2 <= kL2Waves && shares * 2 <= chunks) shares *= 2;

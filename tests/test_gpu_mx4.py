@@ -541,7 +541,8 @@ def test_layer_of_tokens_that_have_an_expert_more_than_once(t, k, e):
 
 
 @pytest.mark.parametrize("t,k,h,i", [(48, 1, 128, 128), (49, 1, 128, 128), (16, 3, 7168, 128), (17, 2, 7168, 128),
-                                     (16, 1, 16384, 128), (1, 2, 32768, 128), (2, 1, 32640, 256),
+                                     (16, 1, 15360, 128), (16, 1, 16384, 128), (1, 2, 32768, 128),
+                                     (8, 1, 30720, 128), (2, 1, 32640, 256),
                                      (4, 2, 128, 8192)])
 def test_layer_at_the_limits_of_the_few_token_path(t, k, h, i):
     """48 and 49 pairs; hidden sizes whose tokens do and do not fit the LDS.
@@ -559,6 +560,23 @@ def test_layer_at_the_limits_of_the_few_token_path(t, k, h, i):
     moe.moe_forward(*[up(v) for v in (x, ids, w, *w1, *w2)], "mxfp4", weight_fmt="mxfp4", out=out)
     ref = oracle.token_forward_mx4(x, ids, w, w1, w2, e, t)
     _check_layer(down(out), ref, t, k)
+
+
+@pytest.mark.parametrize("t,i", [(2, 128), (5, 4096), (3, 16384), (60, 512)])
+def test_layer_of_tokens_without_an_expert_here(t, i):
+    """No id is this rank's: zeros, whatever the weights hold."""
+    g = _rng(72, t, i)
+    x = _bf16(g.standard_normal((t, 256)))
+    ids = g.choice(np.array([-1, -2 ** 31, 3, 7, 2 ** 31 - 1], np.int32), (t, 6))
+    w = g.random((t, 6)).astype(np.float32)
+    w[0, 0] = np.nan
+    codes = [torch.zeros(s, dtype=torch.uint8, device=dev()) for s in ((3, 2 * i, 128), (3, 256, i // 2))]
+    scales = [torch.full(s, 255, dtype=torch.uint8, device=dev()) for s in ((3, 2 * i, 8), (3, 256, i // 32))]
+    out = torch.full((t, 256), POISON_BF16, dtype=torch.int16, device=dev())
+    say(f"mx4 layer without experts, {t} tokens, inter {i}")
+    moe.moe_forward(up(x), up(ids), up(w), codes[0], scales[0], codes[1], scales[1], "mxfp4", weight_fmt="mxfp4",
+                    out=out)
+    assert not down(out).any()
 
 
 @pytest.mark.parametrize("t,e,k", [(3, 12, 4), (100, 12, 4)])
