@@ -25,8 +25,8 @@ DECODE_LIMITS = {"max_pairs": 64, "fc2_row_bytes": 24576, "fc2_max_scales": 256,
 
 
 def decode_layer_applies(t_cap, topk, hidden, inter, weight_fmt="e4m3"):
-    """Whether moe_forward runs this problem (aligned layout) as its one-launch
-    decode layer; with MXFP4 weights H and I must also be multiples of 256."""
+    """Whether moe_forward runs this problem (aligned layout, FP8 activations) as
+    its one-launch decode layer; with MXFP4 weights H and I must also be multiples of 256."""
     d, p = DECODE_LIMITS, t_cap * topk
     if _weight_fmt(weight_fmt) == 1 and (hidden % 256 or inter % 256):
         return False

@@ -642,6 +642,7 @@ hipError_t launch_a4_tiled(const W4Args& g, hipStream_t stream) {
 // Row tiles of TM rows that an expert of `mean` rows takes, as expected of
 // routing that spreads rows at random (a Poisson count, near enough normal).
 double expected_tiles(double mean, int tm) {
+  if (mean > 16.0 * tm) return mean / tm + 0.5;  // whole tiles and half of one
   const double sd = sqrt(mean);
   double n = 0.0;
   for (double at = 0.0; at < mean + 5.0 * sd; at += tm)
