@@ -270,7 +270,6 @@ struct A4Tile {
 template <int TM, int TN, int G>
 __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p) {
   constexpr int MI = TM / 64, NI = TN / 64;   // 32-row MFMA tiles of a wave: tokens, weights
-  constexpr int M = MI * NI;
   constexpr bool WIDE = G > 1;
   constexpr int U = G == 4 ? 4 : 2;           // stages per loop iteration
   constexpr int WL = TN / 32, XL = TM / 32;   // code loads per wave and stage
@@ -382,13 +381,13 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     if constexpr (WIDE) return 0u;
     return kb * 256 + 128 >= K && chunk >= 4 ? 64u : 0u;
   };
-  auto issue_tokens = [&](int s, uint8_t* buf) {
+  auto issue_tokens = [&](int s, uint8_t* buf, auto n_t) {  // the tile's first 32 n_t rows
     const int kb = stage_index(s);
     const bool n = s >= P2;
     const uint8_t* base = p.a + kb * 128;
     const uint32_t back = past_end(kb);
 #pragma unroll
-    for (int i = 0; i < XL; ++i)
+    for (int i = 0; i < decltype(n_t)::value; ++i)
       load_lds16(base + ((n ? src[1].xoff[i] : src[0].xoff[i]) - back), buf + (4 * i + wave) * 1024);
   };
   auto issue_weights = [&](int s, uint8_t* buf) {
@@ -430,7 +429,7 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   uint4 fx[4][MI];                // token fragments of the stage's quarters
   uint4 scw[NI], scx[MI];         // scale bytes of two stages (not WIDE: of one, in x and y)
   uint32_t cw[NI], cx[MI];        // this quarter's, the lane's half in bytes 0 and 2
-  int wrow = wn * (TN / 2) + r32, xrow = wm * (TM / 2) + r32;
+  int wrow = wn * (TN / 2) + r32, xrow = 32 * wm + r32;  // of the first MFMA tiles
   const int swz = (r32 >> 1) & 7;
   auto read_weights = [&](const uint8_t* buf, auto q_t) {
     constexpr int q = decltype(q_t)::value;
@@ -438,17 +437,17 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     for (int i = 0; i < NI; ++i)
       fw[q & 1][i] = *reinterpret_cast<const uint4*>(buf + (wrow + 32 * i) * 128 + (((2 * q + h) ^ swz) << 4));
   };
-  auto read_tokens = [&](const uint8_t* buf, auto q_t) {
+  auto read_tokens = [&](const uint8_t* buf, auto q_t, auto mj_t) {
     constexpr int q = decltype(q_t)::value;
 #pragma unroll
-    for (int j = 0; j < MI; ++j)
-      fx[q][j] = *reinterpret_cast<const uint4*>(buf + (xrow + 32 * j) * 128 + (((2 * q + h) ^ swz) << 4));
+    for (int j = 0; j < decltype(mj_t)::value; ++j)
+      fx[q][j] = *reinterpret_cast<const uint4*>(buf + (xrow + 64 * j) * 128 + (((2 * q + h) ^ swz) << 4));
   };
   auto read_pair_scales = [&](const uint32_t* sc) {  // WIDE
 #pragma unroll
     for (int i = 0; i < NI; ++i) scw[i] = *reinterpret_cast<const uint4*>(sc + (wrow + 32 * i) * 4);
 #pragma unroll
-    for (int j = 0; j < MI; ++j) scx[j] = *reinterpret_cast<const uint4*>(sc + (TN + xrow + 32 * j) * 4);
+    for (int j = 0; j < MI; ++j) scx[j] = *reinterpret_cast<const uint4*>(sc + (TN + xrow + 64 * j) * 4);
   };
   auto read_stage_scales = [&](const uint32_t* sc) {  // not WIDE
 #pragma unroll
@@ -458,8 +457,8 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     }
 #pragma unroll
     for (int j = 0; j < MI; ++j) {
-      scx[j].x = sc[TN + xrow + 32 * j];
-      scx[j].y = sc[kScRows + TN + xrow + 32 * j];
+      scx[j].x = sc[TN + xrow + 64 * j];
+      scx[j].y = sc[kScRows + TN + xrow + 64 * j];
     }
   };
   // The words of K block d (128 wide) of the held stages.
@@ -471,12 +470,12 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
 #pragma unroll
     for (int j = 0; j < MI; ++j) cx[j] = pick(scx[j]) >> (8 * h);
   };
-  auto products = [&](auto q_t) {
+  auto products = [&](auto q_t, auto mj_t) {
     constexpr int q = decltype(q_t)::value;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < MI; ++j)
+      for (int j = 0; j < decltype(mj_t)::value; ++j)
         acc[i][j] = mfma_a4_32<(q & 1) == 1>(fw[q & 1][i], fx[q][j], acc[i][j], cw[i], cx[j]);
   };
   // K values past the end: zero codes.
@@ -489,7 +488,8 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     }
   };
   // Spreads LDS reads and then loads over a quarter's MFMAs.
-  auto spread = [&](auto reads_t, auto loads_t) {
+  auto spread = [&](auto mj_t, auto reads_t, auto loads_t) {
+    constexpr int M = NI * decltype(mj_t)::value;
     constexpr int reads = decltype(reads_t)::value, loads = decltype(loads_t)::value;
     // Twice the even rate, so that the last have arrived when the quarter ends
     // (evenly spread: 0.7 to 1.5 % more for 32768 rows of 7168 -> 4096).
@@ -508,35 +508,39 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   const std::integral_constant<int, 1> c1;
   const std::integral_constant<int, 2> c2;
   const std::integral_constant<int, 3> c3;
+  const std::integral_constant<int, MI> all;
+  const std::integral_constant<int, XL> xl;
+  const std::integral_constant<int, 2> xl_short;
   int buf = 0;  // s_src slot of the current tile
 
-  // Stage s; V = s % U; its buffers w and x, and the next stage's.
-  auto stage = [&](int s, auto v_t, uint8_t* w, uint8_t* x, const uint8_t* w_next, const uint8_t* x_next,
+  // Stage s; V = s % U; mj: MFMA tiles of tokens that hold rows; xn: loads of
+  // tokens for stage s + 2; its buffers w and x, and the next stage's.
+  auto stage = [&](int s, auto v_t, auto mj, auto xn, uint8_t* w, uint8_t* x, const uint8_t* w_next, const uint8_t* x_next,
                    uint32_t* sc, const uint32_t* sc_next) {
-    constexpr int V = decltype(v_t)::value;
+    constexpr int V = decltype(v_t)::value, MJ = decltype(mj)::value, XN = decltype(xn)::value;
     // q = 0
-    read_tokens(x, c1);
-    read_tokens(x, c2);
-    read_tokens(x, c3);
+    read_tokens(x, c1, mj);
+    read_tokens(x, c2, mj);
+    read_tokens(x, c3, mj);
     read_weights(w, c1);
-    products(c0);
-    spread(std::integral_constant<int, 3 * MI + NI>{}, c0);
+    products(c0, mj);
+    spread(mj, std::integral_constant<int, 3 * MJ + NI>{}, c0);
     lds_barrier();
     __builtin_amdgcn_sched_barrier(0);
     // q = 1
     mask_tokens(s, c1);
     mask_tokens(s, c2);
     mask_tokens(s, c3);
-    issue_tokens(s + 2, x);
+    issue_tokens(s + 2, x, xn);
     read_weights(w, c2);
-    products(c1);
-    spread(std::integral_constant<int, NI>{}, std::integral_constant<int, XL>{});
+    products(c1, mj);
+    spread(mj, std::integral_constant<int, NI>{}, xn);
     // q = 2
     block_scales(std::integral_constant<int, WIDE ? 2 * (V & 1) + 1 : 1>{});
     read_weights(w, c3);
-    products(c2);
-    spread(std::integral_constant<int, NI>{}, c0);
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(XL));  // all but the tokens of stage s + 2
+    products(c2, mj);
+    spread(mj, std::integral_constant<int, NI>{}, c0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(XN));  // all but the tokens of stage s + 2
     lds_barrier();
     __builtin_amdgcn_sched_barrier(0);
     // q = 3. The scales of the next group or pair go where this one's last
@@ -545,11 +549,11 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     constexpr bool PAIR = WIDE && (V & 1) == 1;
     if constexpr (SCALES) issue_scales(s + 2, sc);
     issue_weights(s + 2, w);
-    read_tokens(x_next, c0);
+    read_tokens(x_next, c0, all);
     read_weights(w_next, c0);
     if constexpr (PAIR) read_pair_scales(s_sc0 + (V == U - 1 ? 0 : kScRows * 4));
-    products(c3);
-    spread(std::integral_constant<int, (PAIR ? 2 : 1) * (MI + NI)>{},
+    products(c3, mj);
+    spread(mj, std::integral_constant<int, (PAIR ? 2 : 1) * (MI + NI)>{},
            std::integral_constant<int, WL + (SCALES ? SCL : 0)>{});
     if constexpr (!WIDE) read_stage_scales(sc_next);
     block_scales(std::integral_constant<int, WIDE && (V & 1) == 0 ? 2 : 0>{});
@@ -559,15 +563,15 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   set_sources(src[1], nxt, s_src[1]);
   issue_scales(0, s_sc0);
   if constexpr (!WIDE) issue_scales(1, s_sc1);
-  issue_tokens(0, s_x0);
+  issue_tokens(0, s_x0, xl);
   issue_weights(0, s_w0);
-  issue_tokens(1, s_x1);
+  issue_tokens(1, s_x1, xl);
   issue_weights(1, s_w1);
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(XL + WL));
   lds_barrier();
   if constexpr (WIDE) read_pair_scales(s_sc0);
   else read_stage_scales(s_sc0);
-  read_tokens(s_x0, c0);
+  read_tokens(s_x0, c0, all);
   read_weights(s_w0, c0);
   block_scales(c0);
 
@@ -576,15 +580,26 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < MI; ++j) acc[i][j] = v16f{};
-    for (int s = 0; s < P2; s += U) {
+    // U stages; the last two of them load xn2 rows' worth of tokens.
+    auto stages = [&](int s, auto mj, auto xn, auto xn2) {
       // Keeps the LDS addresses of every buffer out of registers of their own.
       asm volatile("" : "+v"(wrow), "+v"(xrow));
-      stage(s, c0, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
-      stage(s + 1, c1, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
       if constexpr (U == 4) {
-        stage(s + 2, c2, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
-        stage(s + 3, c3, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
+        stage(s, c0, mj, xn, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
+        stage(s + 1, c1, mj, xn, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
+        stage(s + 2, c2, mj, xn2, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
+        stage(s + 3, c3, mj, xn2, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
+      } else {
+        stage(s, c0, mj, xn2, s_w0, s_x0, s_w1, s_x1, s_sc0, s_sc1);
+        stage(s + 1, c1, mj, xn2, s_w1, s_x1, s_w0, s_x0, s_sc1, s_sc0);
       }
+    };
+    if (MI > 1 && cur.rows <= 64) {
+      int s = 0;
+      for (; s + U < P2; s += U) stages(s, c1, xl_short, xl_short);
+      stages(s, c1, xl_short, xl);
+    } else {
+      for (int s = 0; s < P2; s += U) stages(s, all, xl, xl);
     }
 
     // Output, and the row sources of the tile after the next. A lane holds
@@ -596,7 +611,8 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     const int* from = s_src[buf];
 #pragma unroll
     for (int j = 0; j < MI; ++j) {
-      const int row = wm * (TM / 2) + 32 * j + r32;
+      if (64 * j >= cur.rows) break;
+      const int row = 64 * j + 32 * wm + r32;
       const bool live = row < cur.rows;
       const uint32_t keep = from[row] < 0 ? 0u : ~0u;
       uint16_t* crow = p.c + static_cast<int64_t>(cur.row0 + row) * N + cur.n0 + wn * (TN / 2) + 8 * h;
