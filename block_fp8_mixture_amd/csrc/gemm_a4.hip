@@ -235,6 +235,10 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
 // (G = 2) those of two stages, and held in registers two stages at a time;
 // otherwise (G = 1) each stage brings its rows' bytes by two 4-byte loads.
 //
+// A tile of at most 64 rows (an expert's last, as a rule) takes stages that load
+// those rows and multiply the first MFMA tile of each wave alone: 0.4 of a
+// whole tile's time (32768 rows over 32 experts, K 7168, N 4096: 543 -> 529 us).
+//
 // Row tiles of an expert run fastest, so that neighbours share a weight slab.
 constexpr int kA4TThreads = 256;
 constexpr int kA4TileCols = 256;
@@ -331,11 +335,16 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   };
 
   // Workgroups go round-robin over the 8 XCDs: neighbouring tiles, which share
-  // operand rows, go to workgroups of one XCD and so to one L2.
-  const int grid = static_cast<int>(gridDim.x);
-  int tile = grid % 8 == 0 ? (blockIdx.x & 7) * (grid / 8) + (blockIdx.x >> 3) : blockIdx.x;
-  if (tile >= total) return;
-  A4Tile cur = locate(tile), nxt = locate(tile + grid);
+  // operand rows, go to workgroups of one XCD and so to one L2. Within the XCD
+  // they move on by one workgroup per round, so that a workgroup does not meet
+  // the same (full or short) row tile of every expert.
+  const unsigned grid = gridDim.x, xcds = grid % 8 == 0 ? 8 : 1, per_xcd = grid / xcds;
+  auto tile_of = [&](unsigned round) {
+    return static_cast<int>(round * grid + (blockIdx.x % xcds) * per_xcd + (blockIdx.x / xcds + round) % per_xcd);
+  };
+  unsigned round = 0;
+  if (tile_of(0) >= total) return;
+  A4Tile cur = locate(tile_of(0)), nxt = locate(tile_of(1));
   if (tid < TM) {
     s_src[0][tid] = row_source(cur);
     s_src[1][tid] = row_source(nxt);
@@ -606,7 +615,7 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     // weight rows 8 v + 4 h .. + 3 (v = 0..3) of its token; the half waves swap
     // so that it has 8 consecutive ones of v = 2 u + h, and a row gets 32
     // contiguous bytes per store.
-    const A4Tile after = locate(tile + 2 * grid);
+    const A4Tile after = locate(tile_of(round + 2));
     const int after_src = row_source(after);
     const int* from = s_src[buf];
 #pragma unroll
@@ -631,8 +640,7 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
       }
     }
     if (tid < TM) s_src[buf == 0 ? 2 : buf - 1][tid] = after_src;
-    tile += grid;
-    if (tile >= total) break;
+    if (tile_of(++round) >= total) break;
     lds_barrier();  // the sources are written
     cur = nxt;
     nxt = after;
@@ -655,15 +663,21 @@ hipError_t launch_a4_tiled(const W4Args& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Row tiles of TM rows that an expert of `mean` rows takes, as expected of
-// routing that spreads rows at random (a Poisson count, near enough normal).
-double expected_tiles(double mean, int tm) {
-  if (mean > 16.0 * tm) return mean / tm + 0.5;  // whole tiles and half of one
-  const double sd = sqrt(mean);
-  double n = 0.0;
-  for (double at = 0.0; at < mean + 5.0 * sd; at += tm)
-    n += at == 0.0 ? 1.0 : 0.5 * erfc((at - mean) / (sd * 1.4142135623730951));
-  return n;
+// Expected time of an expert's row tiles of tm rows, a whole tile's time being
+// `full` and one of at most 64 rows' kA4ShortCost, when routing spreads rows at
+// random (a Poisson count of that mean, near enough normal).
+constexpr double kA4ShortCost = 0.4;
+double expected_cost(double mean, int tm, double full) {
+  const double step = tm > 64 ? kA4ShortCost : full;  // of the first rows, then of more than 64
+  if (mean > 16.0 * tm) return (mean / tm - 0.5) * full + step + (full - step) * (1.0 - 64.0 / tm);
+  const double sd = sqrt(mean) * 1.4142135623730951;
+  auto more = [&](double rows) { return rows == 0.0 ? 1.0 : 0.5 * erfc((rows - mean) / sd); };
+  double t = 0.0;
+  for (double at = 0.0; at < mean + 4.0 * sd; at += tm) {
+    t += step * more(at);
+    if (tm > 64) t += (full - step) * more(at + 64.0);
+  }
+  return t;
 }
 
 }  // namespace
@@ -678,18 +692,21 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
     hipLaunchKernelGGL(gemm_a4_kernel, dim3(static_cast<unsigned>(4 * cus)), dim3(kA4Threads), 0, stream, g);
     return hipGetLastError();
   }
-  // The tile height with the least expected time: tiles of an expert times a
-  // tile's time, 0.6, 0.7, 0.8 and 1 for 64, 128, 192 and 256 rows (32
-  // experts, N 4096, K 7168: 57, 62 and 76 us a round of 128-, 192- and
-  // 256-row tiles; N 7168, K 2048: 18, 23 and 30 us).
+  // The tile height with the least expected time; whole tiles of 64, 128, 192
+  // and 256 rows take 0.39, 0.7, 0.8 and 1. Measured, us: a layer of 64 and 512
+  // tokens over 128 experts of 2048 -> 768, top 8, at 64 / 128: 88/90, 104/106;
+  // 32 experts of 80 rows, K 7168, N 4096: 163/113; of 150, 300, 520 and 1040
+  // rows at 128 / 192 / 256: 172/125/135, 242/201/207, 379/303/318 and
+  // 672/572/550; K 2048, N 7168: 90/78/83, 139/118/121, 225/188/186 and
+  // 404/350/333.
   double mean = static_cast<double>(rows) / live;
   if (mean > g.max_rows_per_expert) mean = g.max_rows_per_expert;
   constexpr int kHeights[4] = {64, 128, 192, 256};
-  constexpr double kCost[4] = {0.6, 0.7, 0.8, 1.0};
+  constexpr double kCost[4] = {0.39, 0.7, 0.8, 1.0};
   int best = 0;
   double least = 1e300;
   for (int i = 0; i < 4; ++i) {
-    const double t = expected_tiles(mean, kHeights[i]) * kCost[i];
+    const double t = expected_cost(mean, kHeights[i], kCost[i]);
     if (t < least) {
       least = t;
       best = i;

@@ -396,6 +396,64 @@ def test_product_matches_oracle(ci, gather):
         _check_gemm(out, counts, offsets, a, asc, w, ws, row_map, k)
 
 
+# Eight experts and 32 column tiles: enough for the product through LDS. The
+# mean rows per expert set the height of its row tiles, 64, 128, 192 or 256; in
+# each set some end in a whole tile, some in one of at most 64 rows.
+TILED = [
+    [64, 1, 0, 65, 33, 17, 100, 40],
+    [128, 129, 1, 64, 65, 192, 0, 61],
+    [192, 193, 256, 257, 1, 0, 150, 151],
+    [256, 257, 320, 321, 1, 0, 512, 400],
+]
+
+
+@pytest.mark.parametrize("k", [128, 640, 512, 1536, 1024, 2048])
+@pytest.mark.parametrize("ci", range(len(TILED)))
+def test_product_through_lds_matches_oracle(ci, k):
+    gather, n = bool((ci + k // 128) & 1), 8064 if ci & 1 else 8192
+    say(f"mx4 gemm through LDS {TILED[ci]} n={n} k={k} gather={gather}")
+    counts, offsets, row_cap, a, asc, w, ws, row_map = _gemm(TILED[ci], n, k, 1, gather, 100 + ci)
+    out = torch.full((row_cap, n), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_grouped_gemm_mxfp4(up(a), up(asc), "mxfp4", up(w), up(ws), up(counts), up(offsets), row_cap,
+                               a_row_map=None if row_map is None else up(row_map), a_row_div=4 if gather else 1,
+                               out=out)
+    _check_gemm(out, counts, offsets, a, asc, w, ws, row_map, k)
+
+
+@pytest.mark.parametrize("ci", [1, 3])
+def test_product_through_lds_masked_layout(ci):
+    counts, offsets, row_cap, a, asc, w, ws, _ = _gemm(TILED[ci], 8192, 768, 1, False, 110 + ci, masked=True)
+    out = torch.full((row_cap, 8192), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_grouped_gemm_mxfp4(up(a), up(asc), "mxfp4", up(w), up(ws), up(counts), None, row_cap,
+                               expert_cap=row_cap // len(counts), out=out)
+    _check_gemm(out, counts, offsets, a, asc, w, ws, None, 768)
+
+
+@pytest.mark.parametrize("k", [640, 1024])
+def test_product_through_lds_of_nan_scales_and_sourceless_rows(k):
+    counts, offsets, row_cap, a, asc, w, ws, row_map = _gemm(TILED[3], 8192, k, 1, True, 120)
+    asc[7, 3] = 255
+    ws[1, 5, 2] = 255
+    for r, v in ((1, -4), (offsets[1] + 2, 4 * len(a)), (offsets[1] + 3, 4 * 7), (offsets[4], -2 ** 31),
+                 (offsets[2] - 1, 2 ** 31 - 1)):
+        row_map[r] = v
+    out = torch.full((row_cap, 8192), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_grouped_gemm_mxfp4(up(a), up(asc), "mxfp4", up(w), up(ws), up(counts), up(offsets), row_cap,
+                               a_row_map=up(row_map), a_row_div=4, out=out)
+    got = oracle.bf16_bits_to_f64(down(out))
+    for e, c in enumerate(counts):
+        for r in range(offsets[e], offsets[e] + c):
+            src = row_map[r] // 4 if row_map[r] >= 0 else -1
+            nan = np.isnan(got[r])
+            if not 0 <= src < len(a):
+                assert not got[r].any(), (e, r)
+                continue
+            want = np.full(8192, src == 7)
+            if e == 1:
+                want[5] = True
+            assert np.array_equal(nan, want), (e, r, src)
+
+
 @pytest.mark.parametrize("ci", [1, 3, 5])
 def test_product_masked_layout(ci):
     counts, n, k, align = GEMMS[ci]
