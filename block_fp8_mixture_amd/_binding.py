@@ -151,6 +151,7 @@ def _ptr(t):
 # The handle of a device's current stream (torch.cuda.current_stream builds a
 # Stream object around it: 3 us per call against 0.1).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # without its checks
 
 
 def _stream(index):
@@ -161,7 +162,7 @@ def _enqueue(name, device, *args):
     """Calls library function `name` on the current stream of `device`, where the
     tensors live (made the current device if it is another)."""
     fn = getattr(_lib, name)
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         status = fn(*args, _stream(device.index))
     else:
         with torch.cuda.device(device):
@@ -187,6 +188,13 @@ def _shape(t, name, shape):
     if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
+
+
+def _exact(t, name, dtype, shape):
+    """_need and _shape (a tuple), at once where they hold."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
+    return _shape(_need(t, name, dtype), name, shape)
 
 
 def _min_numel(t, name, n):
@@ -248,10 +256,9 @@ def _live(t_live):
     return _ptr(t_live)
 
 
-def _bf16_view(t, name):
-    if t.dtype == torch.bfloat16:
-        t = t.view(torch.int16)
-    return _need(t, name, torch.int16)
+def _bf16(t, name):
+    """BF16 values or their bits (int16); only the address is used."""
+    return _need(t, name, torch.bfloat16 if t.dtype == torch.bfloat16 else torch.int16)
 
 
 def moe_min_row_cap(t_cap, topk, num_experts, align_rows):
@@ -281,13 +288,13 @@ def moe_route(logits, topk, score="softmax", bias=None, renormalize=True, scale=
     if score not in SCORES:
         raise ValueError(f"score must be one of {list(SCORES)}")
     if bias is not None:
-        _shape(_need(bias, "bias", torch.float32), "bias", (num_experts,))
+        _exact(bias, "bias", torch.float32, (num_experts,))
     if ids is None:
         ids = torch.empty((t_cap, topk), dtype=torch.int32, device=logits.device)
     if weights is None:
         weights = torch.empty((t_cap, topk), dtype=torch.float32, device=logits.device)
-    _shape(_need(ids, "ids", torch.int32), "ids", (t_cap, topk))
-    _shape(_need(weights, "weights", torch.float32), "weights", (t_cap, topk))
+    _exact(ids, "ids", torch.int32, (t_cap, topk))
+    _exact(weights, "weights", torch.float32, (t_cap, topk))
     dev = _same_device(logits, bias, ids, weights, t_live)
     router = _Router(num_experts, topk, SCORES[score], int(bool(renormalize)), float(scale),
                      int(num_groups), int(top_groups), int(group_top))
@@ -300,14 +307,14 @@ def moe_mxfp4_dequant(codes, scales, out=None):
     """BF16 values of an MXFP4 tensor: codes uint8 [..., cols/2], scales uint8
     [..., cols/32]. Returns BF16 [..., cols] (or ``out``)."""
     lib = load_library()
-    _need(codes, "codes", torch.uint8)
-    if codes.dim() < 1 or codes.shape[-1] < 16 or codes.shape[-1] % 16:
+    shape = tuple(_need(codes, "codes", torch.uint8).shape)
+    if not shape or shape[-1] < 16 or shape[-1] % 16:
         raise ValueError("codes must be [..., cols / 2] with cols a multiple of 32")
-    lead, cols = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
-    _shape(_need(scales, "scales", torch.uint8), "scales", lead + (cols // 32,))
+    lead, cols = shape[:-1], 2 * shape[-1]
+    _exact(scales, "scales", torch.uint8, lead + (cols // 32,))
     if out is None:
         out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
-    ob = _shape(_bf16_view(out, "out"), "out", lead + (cols,))
+    ob = _shape(_bf16(out, "out"), "out", lead + (cols,))
     dev = _same_device(codes, scales, ob)
     _enqueue("moe_mxfp4_dequant", dev, _ptr(codes), _ptr(scales), codes.numel() * 2 // cols, cols,
              _ptr(ob))
@@ -369,7 +376,7 @@ def moe_act_quant(x, fmt="fp32", t_live=None, xq=None, xs=None, rounding="divide
     """Per-token 1x128 quantization. Returns (xq uint8 [t_cap, H], xs [H/128, t_cap]);
     with ``fmt="mxfp4"`` (xq uint8 [t_cap, H/2], xs uint8 [t_cap, H/32])."""
     lib = load_library()
-    xb = _bf16_view(x, "x")
+    xb = _bf16(x, "x")
     if xb.dim() != 2:
         raise ValueError("x must be [t_cap, hidden]")
     t_cap, hidden = xb.shape
@@ -377,8 +384,8 @@ def moe_act_quant(x, fmt="fp32", t_live=None, xq=None, xs=None, rounding="divide
         xq = torch.empty((t_cap, _code_cols(hidden, fmt)), dtype=torch.uint8, device=xb.device)
     if xs is None:
         xs = torch.empty(_scale_shape(t_cap, hidden, fmt), dtype=_scale_dtype(fmt), device=xb.device)
-    _shape(_need(xq, "xq", torch.uint8), "xq", (t_cap, _code_cols(hidden, fmt)))
-    _shape(_need(xs, "xs", _scale_dtype(fmt)), "xs", _scale_shape(t_cap, hidden, fmt))
+    _exact(xq, "xq", torch.uint8, (t_cap, _code_cols(hidden, fmt)))
+    _exact(xs, "xs", _scale_dtype(fmt), _scale_shape(t_cap, hidden, fmt))
     dev = _same_device(xb, xq, xs, t_live)
     _enqueue("moe_act_quant", dev, _ptr(xb), t_cap, _live(t_live), hidden, _fmt(fmt),
              _rounding(rounding), _ptr(xq), _ptr(xs))
@@ -401,11 +408,11 @@ def moe_grouped_gemm_fp8(a, a_scales, fmt, w, w_scales, counts, offsets, row_cap
         raise ValueError("a and w disagree on K")
     _shape(a_scales, "a_scales", (k // 128, a_rows))
     _shape(w_scales, "w_scales", (num_experts, n // 128, k // 128))
-    _shape(_need(counts, "counts", torch.int32), "counts", (num_experts,))
-    _shape(_need(offsets, "offsets", torch.int32), "offsets", (num_experts + 1,))
+    _exact(counts, "counts", torch.int32, (num_experts,))
+    _exact(offsets, "offsets", torch.int32, (num_experts + 1,))
     if out is None:
         out = torch.empty((max(row_cap, 1), n), dtype=torch.int16, device=a.device)
-    ob = _bf16_view(out, "out")
+    ob = _bf16(out, "out")
     if ob.dim() != 2 or ob.shape[1] != n or ob.shape[0] < row_cap:
         raise ValueError(f"out must be [>= {row_cap}, {n}], got {tuple(ob.shape)}")
     if a_row_map is not None:
@@ -441,17 +448,17 @@ def moe_grouped_gemm_mxfp4(a, a_scales, fmt, w, w_scales, counts, offsets=None, 
         raise ValueError("a and w disagree on K")
     _shape(a_scales, "a_scales", _scale_shape(a_rows, k, fmt))
     _shape(w_scales, "w_scales", (num_experts, n, k // 32))
-    _shape(_need(counts, "counts", torch.int32), "counts", (num_experts,))
+    _exact(counts, "counts", torch.int32, (num_experts,))
     if expert_cap > 0:
         row_cap = num_experts * expert_cap if row_cap is None else row_cap
         offsets = None
     else:
         if offsets is None or row_cap is None:
             raise ValueError("the aligned layout needs offsets and row_cap")
-        _shape(_need(offsets, "offsets", torch.int32), "offsets", (num_experts + 1,))
+        _exact(offsets, "offsets", torch.int32, (num_experts + 1,))
     if out is None:
         out = torch.empty((max(row_cap, 1), n), dtype=torch.int16, device=a.device)
-    ob = _bf16_view(out, "out")
+    ob = _bf16(out, "out")
     if ob.dim() != 2 or ob.shape[1] != n or ob.shape[0] < row_cap:
         raise ValueError(f"out must be [>= {row_cap}, {n}], got {tuple(ob.shape)}")
     if a_row_map is not None:
@@ -481,10 +488,10 @@ def moe_grouped_gemm_fp8_masked(a, a_scales, fmt, w, w_scales, masked_m, expert_
         raise ValueError("a and w disagree on K")
     _shape(a_scales, "a_scales", (k // 128, a_rows))
     _shape(w_scales, "w_scales", (num_experts, n // 128, k // 128))
-    _shape(_need(masked_m, "masked_m", torch.int32), "masked_m", (num_experts,))
+    _exact(masked_m, "masked_m", torch.int32, (num_experts,))
     if out is None:
         out = torch.empty((max(rows, 1), n), dtype=torch.int16, device=a.device)
-    ob = _bf16_view(out, "out")
+    ob = _bf16(out, "out")
     if ob.dim() != 2 or ob.shape[1] != n or ob.shape[0] < rows:
         raise ValueError(f"out must be [>= {rows}, {n}], got {tuple(ob.shape)}")
     if a_row_map is not None:
@@ -507,7 +514,7 @@ def moe_silu_mul_quant_masked(gate_up, masked_m, expert_cap, act="swiglu",
     Returns (hq uint8 [E*cap, I], hs [I/128, E*cap]); with ``fmt="mxfp4"`` (hq
     [E*cap, I/2], hs uint8 [E*cap, I/32])."""
     lib = load_library()
-    gu = _bf16_view(gate_up, "gate_up")
+    gu = _bf16(gate_up, "gate_up")
     _need(masked_m, "masked_m", torch.int32, ndim=1)
     num_experts = masked_m.shape[0]
     rows = num_experts * expert_cap
@@ -518,8 +525,8 @@ def moe_silu_mul_quant_masked(gate_up, masked_m, expert_cap, act="swiglu",
         hq = torch.empty((rows, _code_cols(inter, fmt)), dtype=torch.uint8, device=gu.device)
     if hs is None:
         hs = torch.empty(_scale_shape(rows, inter, fmt), dtype=_scale_dtype(fmt), device=gu.device)
-    _shape(_need(hq, "hq", torch.uint8), "hq", (rows, _code_cols(inter, fmt)))
-    _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", _scale_shape(rows, inter, fmt))
+    _exact(hq, "hq", torch.uint8, (rows, _code_cols(inter, fmt)))
+    _exact(hs, "hs", _scale_dtype(fmt), _scale_shape(rows, inter, fmt))
     dev = _same_device(gu, masked_m, hq, hs)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
@@ -535,20 +542,20 @@ def moe_silu_mul_quant(gate_up, counts, offsets, act="swiglu", clamp_limit=float
     Returns (hq uint8 [row_cap, I], hs [I/128, row_cap]); with ``fmt="mxfp4"``
     (hq [row_cap, I/2], hs uint8 [row_cap, I/32])."""
     lib = load_library()
-    gu = _bf16_view(gate_up, "gate_up")
+    gu = _bf16(gate_up, "gate_up")
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gate_up must be [row_cap, 2 * inter]")
     row_cap, two_i = gu.shape
     inter = two_i // 2
     _need(counts, "counts", torch.int32, ndim=1)
     num_experts = counts.shape[0]
-    _shape(_need(offsets, "offsets", torch.int32), "offsets", (num_experts + 1,))
+    _exact(offsets, "offsets", torch.int32, (num_experts + 1,))
     if hq is None:
         hq = torch.empty((row_cap, _code_cols(inter, fmt)), dtype=torch.uint8, device=gu.device)
     if hs is None:
         hs = torch.empty(_scale_shape(row_cap, inter, fmt), dtype=_scale_dtype(fmt), device=gu.device)
-    _shape(_need(hq, "hq", torch.uint8), "hq", (row_cap, _code_cols(inter, fmt)))
-    _shape(_need(hs, "hs", _scale_dtype(fmt)), "hs", _scale_shape(row_cap, inter, fmt))
+    _exact(hq, "hq", torch.uint8, (row_cap, _code_cols(inter, fmt)))
+    _exact(hs, "hs", _scale_dtype(fmt), _scale_shape(row_cap, inter, fmt))
     dev = _same_device(gu, counts, offsets, hq, hs)
     if act not in ACTS:
         raise ValueError(f"act must be one of {list(ACTS)}")
@@ -561,7 +568,7 @@ def moe_silu_mul_quant(gate_up, counts, offsets, act="swiglu", clamp_limit=float
 def moe_topk_combine(y, pair_to_row, topk_w, t_live=None, out=None):
     """Top-k weighted sum of expert rows. Returns BF16 bits (int16) [t_cap, H]."""
     lib = load_library()
-    yb = _bf16_view(y, "y")
+    yb = _bf16(y, "y")
     if yb.dim() != 2:
         raise ValueError("y must be [row_cap, hidden]")
     row_cap, hidden = yb.shape
@@ -570,7 +577,7 @@ def moe_topk_combine(y, pair_to_row, topk_w, t_live=None, out=None):
     _min_numel(_need(pair_to_row, "pair_to_row", torch.int32), "pair_to_row", t_cap * topk)
     if out is None:
         out = torch.empty((t_cap, hidden), dtype=torch.int16, device=yb.device)
-    ob = _shape(_bf16_view(out, "out"), "out", (t_cap, hidden))
+    ob = _shape(_bf16(out, "out"), "out", (t_cap, hidden))
     dev = _same_device(yb, pair_to_row, w, ob)
     _enqueue("moe_topk_combine", dev, _ptr(yb), row_cap, _ptr(pair_to_row), _ptr(w), t_cap,
              _live(t_live), topk, hidden, _ptr(ob))
@@ -627,18 +634,18 @@ def _check_layer_tensors(xb, topk_ids, w1, w1_scales, w2=None, w2_scales=None, w
         raise ValueError(f"w1 must be [E, 2*inter, {hidden // 2 if mx else hidden}], got {tuple(w1.shape)}")
     inter = two_i // 2
     if mx:
-        _shape(_need(w1_scales, "w1_scales", torch.uint8), "w1_scales", (num_experts, two_i, hidden // 32))
+        _exact(w1_scales, "w1_scales", torch.uint8, (num_experts, two_i, hidden // 32))
     else:
-        _shape(_need(w1_scales, "w1_scales", torch.float32), "w1_scales",
+        _exact(w1_scales, "w1_scales", torch.float32,
                (num_experts, two_i // 128, hidden // 128))
     if w2 is not None:
         if mx:
-            _shape(_need(w2, "w2", torch.uint8), "w2", (num_experts, hidden, inter // 2))
-            _shape(_need(w2_scales, "w2_scales", torch.uint8), "w2_scales",
+            _exact(w2, "w2", torch.uint8, (num_experts, hidden, inter // 2))
+            _exact(w2_scales, "w2_scales", torch.uint8,
                    (num_experts, hidden, inter // 32))
         else:
-            _shape(_need(w2, "w2", torch.uint8), "w2", (num_experts, hidden, inter))
-            _shape(_need(w2_scales, "w2_scales", torch.float32), "w2_scales",
+            _exact(w2, "w2", torch.uint8, (num_experts, hidden, inter))
+            _exact(w2_scales, "w2_scales", torch.float32,
                    (num_experts, hidden // 128, inter // 128))
     return num_experts, inter, topk_ids.shape[1]
 
@@ -653,7 +660,7 @@ def moe_forward(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="fp32", a
     [E, rows, cols/32]; with it ``fmt="mxfp4"`` quantizes both activations to
     MXFP4."""
     lib = load_library()
-    xb = _bf16_view(x, "x")
+    xb = _bf16(x, "x")
     if xb.dim() != 2:
         raise ValueError("x must be [t_cap, hidden]")
     t_cap, hidden = xb.shape
@@ -661,7 +668,7 @@ def moe_forward(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="fp32", a
                                                     weight_fmt)
     if topk_w is None:
         topk_w = torch.ones((t_cap, topk), dtype=torch.float32, device=xb.device)
-    _shape(_need(topk_w, "topk_w", torch.float32), "topk_w", (t_cap, topk))
+    _exact(topk_w, "topk_w", torch.float32, (t_cap, topk))
     prob = _problem(num_experts, hidden, inter, topk, t_cap, align_rows, row_cap, fmt, act,
                     clamp_limit, rounding, expert_start, expert_cap, weight_fmt)
     need = int(lib.moe_workspace_bytes(ctypes.byref(prob)))
@@ -673,9 +680,9 @@ def moe_forward(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="fp32", a
     _need(workspace, "workspace", torch.uint8)
     if out is None:
         out = torch.empty((t_cap, hidden), dtype=torch.int16, device=xb.device)
-    ob = _shape(_bf16_view(out, "out"), "out", (t_cap, hidden))
+    ob = _shape(_bf16(out, "out"), "out", (t_cap, hidden))
     if t_live is not None:
-        _shape(_need(t_live, "t_live", torch.int32), "t_live", (1,))
+        _exact(t_live, "t_live", torch.int32, (1,))
     dev = _same_device(xb, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, ob, workspace, t_live)
     tens = _Tensors(_ptr(xb), _ptr(topk_ids), _ptr(topk_w), _live(t_live), _ptr(w1),
                     _ptr(w1_scales), _ptr(w2), _ptr(w2_scales), _ptr(ob))
@@ -698,7 +705,7 @@ def moe_forward_noalloc(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="
     when ``out`` and ``topk_w`` are given). Calls on one device must not overlap.
     Returns out (BF16 bits int16 [t_cap, H])."""
     lib = load_library()
-    xb = _bf16_view(x, "x")
+    xb = _bf16(x, "x")
     if xb.dim() != 2:
         raise ValueError("x must be [t_cap, hidden]")
     t_cap, hidden = xb.shape
@@ -706,12 +713,12 @@ def moe_forward_noalloc(x, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, fmt="
                                                     weight_fmt)
     if topk_w is None:
         topk_w = torch.ones((t_cap, topk), dtype=torch.float32, device=xb.device)
-    _shape(_need(topk_w, "topk_w", torch.float32), "topk_w", (t_cap, topk))
+    _exact(topk_w, "topk_w", torch.float32, (t_cap, topk))
     if out is None:
         out = torch.empty((t_cap, hidden), dtype=torch.int16, device=xb.device)
-    ob = _shape(_bf16_view(out, "out"), "out", (t_cap, hidden))
+    ob = _shape(_bf16(out, "out"), "out", (t_cap, hidden))
     if t_live is not None:
-        _shape(_need(t_live, "t_live", torch.int32), "t_live", (1,))
+        _exact(t_live, "t_live", torch.int32, (1,))
     dev = _same_device(xb, topk_ids, topk_w, w1, w1_scales, w2, w2_scales, ob, t_live)
     prob = _problem(num_experts, hidden, inter, topk, t_cap, align_rows, row_cap, fmt, act,
                     clamp_limit, rounding, expert_start, expert_cap, weight_fmt)
@@ -727,7 +734,7 @@ def moe_fc1_decode(x, topk_ids, w1, w1_scales, inter, fmt="fp32", act="swiglu",
     """The decode path's first launch alone (routing, activation quantization and
     FC1 with SiLU(gate)*up), writing moe_forward's workspace. Returns the workspace."""
     lib = load_library()
-    xb = _bf16_view(x, "x")
+    xb = _bf16(x, "x")
     if xb.dim() != 2:
         raise ValueError("x must be [t_cap, hidden]")
     t_cap, hidden = xb.shape
@@ -741,7 +748,7 @@ def moe_fc1_decode(x, topk_ids, w1, w1_scales, inter, fmt="fp32", act="swiglu",
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=xb.device)
     _need(workspace, "workspace", torch.uint8)
     if t_live is not None:
-        _shape(_need(t_live, "t_live", torch.int32), "t_live", (1,))
+        _exact(t_live, "t_live", torch.int32, (1,))
     dev = _same_device(xb, topk_ids, w1, w1_scales, workspace, t_live)
     tens = _Tensors(_ptr(xb), _ptr(topk_ids), None, _live(t_live), _ptr(w1), _ptr(w1_scales),
                     None, None, None)
