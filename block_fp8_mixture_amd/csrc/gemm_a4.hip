@@ -17,13 +17,14 @@
 #include "device_common.h"
 #include "gemm_device.h"
 #include "kernels.h"
+#include "mx_stream.h"
 
 namespace moe {
 namespace {
 
 constexpr int kA4Threads = 256;
 constexpr int kA4Waves = kA4Threads / 64;
-constexpr int kA4TileM = 64;  // token rows of a wave task, four 16-row tiles
+constexpr int kA4TileM = 32;  // token rows of a wave task, two 16-row tiles
 constexpr int kA4Tiles = kA4TileM / 16;
 constexpr int kA4TileN = 32;  // weight rows of a wave task, two 16-row tiles
 
@@ -79,59 +80,110 @@ __device__ __forceinline__ int a4_expert_of(const int* s_pref, int E, int u) {
   return lo;
 }
 
-// The K range of a share, in 128-wide steps.
-__device__ __forceinline__ int a4_split(int kb, int s, int shares) { return kb * s / shares; }
+// ---- few rows per expert: weights streamed into the matrix cores -----------
 
-__device__ __forceinline__ v4f mfma_a4(uint4 w, uint32_t ws, uint4 x, uint32_t xs, v4f acc) {
-  const v8i a = {static_cast<int>(w.x), static_cast<int>(w.y), static_cast<int>(w.z),
-                 static_cast<int>(w.w), 0, 0, 0, 0};
-  const v8i b = {static_cast<int>(x.x), static_cast<int>(x.y), static_cast<int>(x.z),
-                 static_cast<int>(x.w), 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, 0, static_cast<int>(ws), 0,
-                                                          static_cast<int>(xs));
+// A wave's operands: two 16-row tiles of weights and up to kA4Tiles of tokens.
+struct A4Rows {
+  const uint8_t* w[2];    // uniform: a tile's first row, its scales
+  const uint8_t* ws[2];
+  uint32_t wrow, wsrow;   // the lane's row in them
+  uint32_t xrow[kA4Tiles], xsrow[kA4Tiles];  // and in A
+};
+
+// acc += the chunks [ch0, ch1) of 256 K values, MT token tiles. The operands
+// of two chunks are loaded together; other waves' loads cover their products.
+template <int MT>
+__device__ __forceinline__ void a4_stream(const W4Args& p, A4Rows t, int g, int ch0, int ch1,
+                                          v4f (&acc)[2][kA4Tiles]) {
+  const int K = p.k;
+  L4Frag w[2][2], x[2][MT];
+  auto load = [&](int ch, int b) {
+    const int c = min(ch, ch1 - 1);  // past the share: its last chunk, unused
+    const L4Lane l = l4_lane(g, c * 256 + 128 >= K);
+    // Opaque, so that the addresses stay a uniform base and a 32-bit offset (as
+    // pointers of their own that step along K they take 60 registers more).
+    asm volatile("" : "+v"(t.wrow), "+v"(t.wsrow));
+#pragma unroll
+    for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(t.xrow[m]), "+v"(t.xsrow[m]));
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      l4_load(x[b][m], p.a, t.xrow[m], static_cast<const uint8_t*>(p.a_scales), t.xsrow[m], c, l);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) l4_load(w[b][i], t.w[i], t.wrow, t.ws[i], t.wsrow, c, l);
+  };
+  auto products = [&](int ch, int b) {
+    const L4Lane l = l4_lane(g, ch * 256 + 128 >= K);
+    const uint32_t z = l.second;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const uint32_t xs = l4_scales(x[b][m], l);
+      const uint4 c1 = x[b][m].c[1];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[i][m] = mfma_l4<0>(w[b][i].c[0], l4_scales(w[b][i], l), x[b][m].c[0], xs, acc[i][m]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        acc[i][m] = mfma_l4<1>(w[b][i].c[1], l4_scales(w[b][i], l), uint4{c1.x & z, c1.y & z, c1.z & z, c1.w & z}, xs, acc[i][m]);
+    }
+  };
+  for (int ch = ch0; ch < ch1; ch += 2) {
+    load(ch, 0);
+    load(ch + 1, 1);
+    products(ch, 0);
+    if (ch + 1 < ch1) products(ch + 1, 1);
+  }
 }
 
-// A wave task is (expert, 64 token rows, 32 weight rows, a share of K); the
+// A wave task is (expert, 32 token rows, 32 weight rows, a share of K); the
 // operands go from global memory straight into the MFMA registers. The S
 // waves of a K split add their partial sums in LDS in wave order, so the
-// result does not depend on which finishes first.
+// result does not depend on which finishes first. Bound by the weights: 8
+// experts of 4 rows, N 4096, K 7168 (125 MB) 27.7 us, 4.5 TB/s. Many waves with
+// few registers (75) beat a pipeline of two chunks within a wave (182 registers,
+// 32.4 us), and whole lines in K order half lines (36.1 us).
 __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
   __shared__ int s_pref[kMaxExperts + 1];
   __shared__ int s_wsum[kA4Waves];
   __shared__ __attribute__((aligned(16))) float s_red[kA4Waves][64 * 4 * 2 * kA4Tiles];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int E = p.num_experts, N = p.n, K = p.k, KB = K / kGroup;
+  const int E = p.num_experts, N = p.n, K = p.k, chunks = (K + 255) / 256;
   a4_prefix(E, [&](int e) { return (a4_rows(p, e) + kA4TileM - 1) / kA4TileM; }, s_pref, s_wsum);
   const int nt = N / kA4TileN;
-  const int tasks = s_pref[E] * nt;
+  const int tasks = __builtin_amdgcn_readfirstlane(s_pref[E]) * nt;
   if (tasks == 0) return;
   int S = 1;
-  while (S < kA4Waves && tasks * S * 2 <= static_cast<int>(gridDim.x) * kA4Waves && S * 2 <= KB) S *= 2;
+  while (S < kA4Waves && tasks * S * 2 <= static_cast<int>(gridDim.x) * kA4Waves && S * 2 <= chunks) S *= 2;
   const int per_wg = kA4Waves / S;
   const int units = (tasks + per_wg - 1) / per_wg;
   const int share = wave & (S - 1);
 
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int t = unit * per_wg + wave / S;
-    const bool live = t < tasks;
+    const int task = unit * per_wg + wave / S;
+    const bool live = task < tasks;
     v4f acc[2][kA4Tiles] = {};
     int rows_here = 0, row0 = 0, n0 = 0, mt = 0;
     if (live) {
-      const int tm = t / nt;
-      n0 = (t - tm * nt) * kA4TileN;
-      const int e = a4_expert_of(s_pref, E, tm);
-      const int m0 = (tm - s_pref[e]) * kA4TileM;
-      rows_here = min(kA4TileM, a4_rows(p, e) - m0);
-      row0 = a4_seg_start(p, e) + m0;
+      // Row tiles of an expert run fastest: they share the weights.
+      const int e = __builtin_amdgcn_readfirstlane(a4_expert_of(s_pref, E, task / nt));
+      const int local = task - s_pref[e] * nt, mtiles = s_pref[e + 1] - s_pref[e];
+      const int m0 = local % mtiles * kA4TileM;
+      n0 = __builtin_amdgcn_readfirstlane(local / mtiles * kA4TileN);
+      rows_here = __builtin_amdgcn_readfirstlane(min(kA4TileM, a4_rows(p, e) - m0));
+      row0 = __builtin_amdgcn_readfirstlane(a4_seg_start(p, e) + m0);
       mt = (rows_here + 15) >> 4;
-      const int64_t wrow = static_cast<int64_t>(e) * N + n0 + r16;
-      const uint8_t* wp = p.w + wrow * (K / 2) + 16 * g;
-      const uint8_t* wsp = p.w_scales + wrow * (K / kMxBlock);
+      const uint32_t pitch = K / 2, spitch = K / kMxBlock;
+      A4Rows t;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = static_cast<int64_t>(e) * N + n0 + 16 * i;
+        t.w[i] = p.w + row * pitch;
+        t.ws[i] = p.w_scales + row * spitch;
+      }
+      t.wrow = r16 * pitch;
+      t.wsrow = r16 * spitch;
       // Source rows; a row past the tile's end or without a source reads row
       // 0, and its results are dropped or zeroed.
-      const uint8_t* xp[kA4Tiles];
-      const uint8_t* xsp[kA4Tiles];
       bool has[kA4Tiles];
 #pragma unroll
       for (int m = 0; m < kA4Tiles; ++m) {
@@ -143,29 +195,13 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
           if (static_cast<unsigned>(src) >= static_cast<unsigned>(p.a_rows)) src = -1;
         }
         has[m] = src >= 0;
-        const int64_t s0 = src < 0 ? 0 : src;
-        xp[m] = p.a + s0 * (K / 2) + 16 * g;
-        xsp[m] = static_cast<const uint8_t*>(p.a_scales) + s0 * (K / kMxBlock);
+        t.xrow[m] = static_cast<uint32_t>(max(src, 0)) * pitch;
+        t.xsrow[m] = static_cast<uint32_t>(max(src, 0)) * spitch;
       }
-      const int kb1 = a4_split(KB, share + 1, S);
-      for (int kb = a4_split(KB, share, S); kb < kb1; ++kb) {
-        uint4 w[2];
-        uint32_t ws[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          w[i] = *reinterpret_cast<const uint4*>(wp + static_cast<int64_t>(16 * i) * (K / 2) + kb * 64);
-          ws[i] = *reinterpret_cast<const uint32_t*>(wsp + static_cast<int64_t>(16 * i) * (K / kMxBlock) + kb * 4) >> (8 * g);
-        }
-#pragma unroll
-        for (int m = 0; m < kA4Tiles; ++m) {
-          if (m < mt) {
-            const uint4 x = *reinterpret_cast<const uint4*>(xp[m] + kb * 64);
-            const uint32_t xs = *reinterpret_cast<const uint32_t*>(xsp[m] + kb * 4) >> (8 * g);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i][m] = mfma_a4(w[i], ws[i], x, xs, acc[i][m]);
-          }
-        }
-      }
+      const int ch0 = __builtin_amdgcn_readfirstlane(chunks * share / S);
+      const int ch1 = __builtin_amdgcn_readfirstlane(chunks * (share + 1) / S);
+      if (mt == 1) a4_stream<1>(p, t, g, ch0, ch1, acc);
+      else a4_stream<2>(p, t, g, ch0, ch1, acc);
 #pragma unroll
       for (int m = 0; m < kA4Tiles; ++m)
         if (!has[m]) acc[0][m] = acc[1][m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -687,8 +723,16 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
   const int rows = g.max_rows > 0 ? g.max_rows : g.row_cap;
   const int live = rows < g.num_experts ? rows : g.num_experts;  // experts with rows, at most
   const int64_t cols = (g.n + kA4TileCols - 1) / kA4TileCols;
-  // Too few 256-row weight slabs for the CUs: K is split instead.
-  if (live * cols < cus) {
+  double mean = static_cast<double>(rows) / live;
+  if (mean > g.max_rows_per_expert) mean = g.max_rows_per_expert;
+  // Few weights: streamed, once per 32 rows, at 4.6 TB/s and 4 us around them;
+  // a round of tiles through LDS takes 1.3 us per 256 K values instead, whatever
+  // it holds. The two are equal, for any K, at some 165 pieces of 256 weight
+  // rows x 32 token rows. Streamed / tiled, us: N 4096, K 7168, experts x rows
+  // 2x4 11/33, 8x4 29/42, 12x4 40/43, 16x4 52/43, 8x32 45/43, 8x64 82/44, 4x100
+  // 82/41, 1x1000 157/65; N 7168, K 2048, 4x16 13/14, 8x16 22/15; N 1024, K 2048,
+  // 32x4 12/15, 64x4 19/16.
+  if (live * cols * static_cast<int64_t>(ceil(mean / kA4TileM)) * 8 < 5 * cus) {
     hipLaunchKernelGGL(gemm_a4_kernel, dim3(static_cast<unsigned>(4 * cus)), dim3(kA4Threads), 0, stream, g);
     return hipGetLastError();
   }
@@ -699,8 +743,6 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
   // rows at 128 / 192 / 256: 172/125/135, 242/201/207, 379/303/318 and
   // 672/572/550; K 2048, N 7168: 90/78/83, 139/118/121, 225/188/186 and
   // 404/350/333.
-  double mean = static_cast<double>(rows) / live;
-  if (mean > g.max_rows_per_expert) mean = g.max_rows_per_expert;
   constexpr int kHeights[4] = {64, 128, 192, 256};
   constexpr double kCost[4] = {0.39, 0.7, 0.8, 1.0};
   int best = 0;
