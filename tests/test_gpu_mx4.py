@@ -732,3 +732,116 @@ def test_weights_quantized_on_the_gpu_serve_the_layer():
     # BF16 tie and, rarely, its quantized code with it; in the 2-norm a tenth
     # of the codes' own step is far beyond that.
     assert np.linalg.norm(got - ref[0]) <= 0.01 * np.linalg.norm(ref[0])
+
+
+# ---- the ranges' ends ------------------------------------------------------------
+
+@pytest.mark.parametrize("t,k", [(5, 3), (40, 4)])
+def test_layer_keeps_a_bad_token_to_itself(t, k):
+    """An infinity or a NaN in one token makes that token's output NaN and
+    leaves the others' bits as they are without it."""
+    x, ids, w, w1, w2 = _exact_layer(90 + t, t, 6, 384, 256, k)
+    args = [up(v) for v in (ids, w, *w1, *w2)]
+    clean = down(moe.moe_forward(up(x), *args, "mxfp4", weight_fmt="mxfp4")[0])
+    bad = x.copy()
+    bad[1, 200], bad[t - 1, 7] = 0x7F80, 0x7FC0
+    got = down(moe.moe_forward(up(bad), *args, "mxfp4", weight_fmt="mxfp4")[0])
+    keep = np.ones(t, bool)
+    keep[[1, t - 1]] = False
+    assert np.array_equal(got[keep], clean[keep])
+    assert np.isnan(oracle.bf16_bits_to_f64(got[~keep])).all()
+
+
+def _big_weights(experts, n, k, seed):
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    w = torch.randint(0, 256, (experts, n, k // 2), dtype=torch.uint8, device=dev(), generator=g)
+    return w, torch.randint(118, 121, (experts, n, k // 32), dtype=torch.uint8, device=dev(), generator=g)
+
+
+@pytest.mark.parametrize("per", [2, 70])
+def test_product_of_weights_past_four_gigabytes(per):
+    """The last expert's codes lie past 2^32 bytes; few rows go through the
+    streaming kernel, more through LDS."""
+    e, n, k = 280, 8192, 4096
+    say(f"mx4 gemm of {e} x {n} x {k}, {per} rows")
+    w, ws = _big_weights(e, n, k, 5)
+    counts = np.zeros(e, np.int32)
+    counts[[0, e - 1]] = per
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    a, asc = _mx(_rng(130, per), 2 * per, k)
+    out = moe.moe_grouped_gemm_mxfp4(up(a), up(asc), "mxfp4", w, ws, up(counts), up(offsets), 2 * per)
+    for x, r in ((0, slice(0, per)), (e - 1, slice(per, 2 * per))):
+        wv = oracle.mxfp4_dequant(down(w[x]), down(ws[x]))
+        av = oracle.mxfp4_dequant(a[r], asc[r])
+        want, mag = av @ wv.T, np.abs(av) @ np.abs(wv).T
+        err = np.abs(oracle.bf16_bits_to_f64(down(out[r])) - want)
+        assert np.all(err <= 2.0 ** -8 * np.abs(want) + k * 2.0 ** -23 * mag)
+
+
+def test_layer_of_weights_past_four_gigabytes():
+    """Two tokens whose experts are the first and the last of 520: both weight
+    tensors are past 2^32 bytes. The same pair of experts alone, as experts 0
+    and 1, gives the same bits."""
+    e, h, i = 520, 4096, 4096
+    w1, w1s = _big_weights(e, 2 * i, h, 6)
+    w2, w2s = _big_weights(e, h, i, 7)
+    g = _rng(131)
+    x = up(_bf16(g.standard_normal((2, h))))
+    tw = up(g.random((2, 2)).astype(np.float32))
+    got = moe.moe_forward(x, _i32([[0, e - 1], [e - 1, 0]]), tw, w1, w1s, w2, w2s, "mxfp4", weight_fmt="mxfp4")[0]
+    two = [v[[0, e - 1]].contiguous() for v in (w1, w1s, w2, w2s)]
+    alone = moe.moe_forward(x, _i32([[0, 1], [1, 0]]), tw, *two, "mxfp4", weight_fmt="mxfp4")[0]
+    assert torch.equal(got, alone) and down(got).any()
+
+
+def test_dequantization_past_two_to_the_32_values():
+    rows, cols = 1 << 20, 4224
+    codes = torch.zeros((rows, cols // 2), dtype=torch.uint8, device=dev())
+    scales = torch.full((rows, cols // 32), 127, dtype=torch.uint8, device=dev())
+    codes[-1] = 0x72
+    codes[rows // 2, 3] = 0x0F
+    out = moe.moe_mxfp4_dequant(codes, scales)
+    assert out[-1, 0::2].eq(1.0).all() and out[-1, 1::2].eq(6.0).all()
+    assert out[rows // 2, 6].item() == -6.0 and not out[:rows // 2].any() and not out[rows // 2 + 1:-1].any()
+
+
+def test_route_of_rows_past_two_to_the_31_elements():
+    t, e, ld = 3000, 40, 800000
+    wide = torch.empty((t, ld), dtype=torch.bfloat16, device=dev())
+    view = wide[:, 5:5 + e]
+    view.copy_(torch.randn((t, e), device=dev()))
+    ids, w = moe.moe_route(view, 4)
+    ids2, w2 = moe.moe_route(view.contiguous(), 4)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+
+
+def test_calls_on_a_device_that_is_not_current(monkeypatch):
+    """With another device current the binding switches to the tensors' (one
+    GPU stands in for two: the binding is told that another is current)."""
+    from block_fp8_mixture_amd import _binding
+    l = torch.randn((3, 40), device=dev())
+    ids, w = moe.moe_route(l, 4)
+    monkeypatch.setattr(_binding, "_current_device", lambda: -1)
+    ids2, w2 = moe.moe_route(l, 4)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
+
+
+def test_route_and_layer_follow_the_current_stream():
+    """Work enqueued under a side stream stays behind what that stream holds."""
+    h, i, e, k, t = 512, 256, 12, 4, 4
+    x, _, _, w1, w2 = _exact_layer(95, t, e, h, i, k)
+    weights = [up(v) for v in (*w1, *w2)]
+    xs, logits = up(x), up(_rng(132).standard_normal((t, e)).astype(np.float32))
+    ids, w = moe.moe_route(logits, k)
+    want = moe.moe_forward(xs, ids, w, *weights, "mxfp4", weight_fmt="mxfp4")[0]
+    side = torch.cuda.Stream()
+    late = torch.zeros_like(logits)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            late.zero_()
+        late.copy_(logits)
+        ids, w = moe.moe_route(late, k)
+        got = moe.moe_forward(xs, ids, w, *weights, "mxfp4", weight_fmt="mxfp4")[0]
+    side.synchronize()
+    assert torch.equal(got, want)
