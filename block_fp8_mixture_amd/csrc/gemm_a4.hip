@@ -238,11 +238,11 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
   }
 }
 
-// ---- large experts: TM x TN output tiles through LDS -----------------------
+// ---- more rows: TM x TN output tiles through LDS -----------------------
 //
-// Four waves, one per SIMD, as 2 (tokens) x 2 (weights): each owns a TM/2 x
-// TN/2 piece, 32 x 32 MFMA tiles whose accumulators stay in registers for the
-// whole K (both scales are applied in the matrix cores, so nothing rescales
+// Four waves, one per SIMD, as 2 (tokens) x 2 (weights): each owns every other
+// 32 of the TM rows and half of the TN columns, 32 x 32 MFMA tiles whose
+// accumulators stay in registers for the whole K (both scales are applied in the matrix cores, so nothing rescales
 // them).
 //
 // A stage is 256 K values of the tile's rows: 128 bytes of each, one whole
@@ -274,6 +274,11 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
 // A tile of at most 64 rows (an expert's last, as a rule) takes stages that load
 // those rows and multiply the first MFMA tile of each wave alone: 0.4 of a
 // whole tile's time (32768 rows over 32 experts, K 7168, N 4096: 543 -> 529 us).
+//
+// Tiles of 64 rows take 128 columns, half the LDS, and two workgroups per CU:
+// twice the stages in flight, and twice the tiles for the CUs where experts are
+// few (64 x 256 tiles, one workgroup per CU, against them: 32 experts of 16 rows, K 7168,
+// N 4096 100 / 91 us, 256 experts of 2 rows, K 6144, N 512 89 / 79 us).
 //
 // Row tiles of an expert run fastest, so that neighbours share a weight slab.
 constexpr int kA4TThreads = 256;
@@ -313,8 +318,8 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   constexpr bool WIDE = G > 1;
   constexpr int U = G == 4 ? 4 : 2;           // stages per loop iteration
   constexpr int WL = TN / 32, XL = TM / 32;   // code loads per wave and stage
-  constexpr int kScRows = TN + 256;           // rows of scales (weight rows first; all lanes load)
-  static_assert(TN + TM <= kScRows, "");
+  constexpr int kScRows = 512;                // rows of scales: 256 for weights, 256 for tokens (all lanes load)
+  static_assert(TN <= 256 && TM <= 256, "");
   static_assert(TM <= kA4TThreads, "one row source per thread");
   __shared__ __attribute__((aligned(1024))) uint8_t s_w0[TN * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t s_w1[TN * 128];
@@ -393,7 +398,6 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   // source and weight rows past N load a valid row, never used. Addresses are
   // a uniform base and a 32-bit offset per lane (an operand's bytes, or one
   // expert's, are below 2^32).
-  static_assert(TN == kA4TThreads, "scale load 0 is the weights'");
   const uint32_t pitch = K / 2, spitch = K / kMxBlock;
   const int chunk = (lane & 7) ^ (((wave & 1) << 2) + (lane >> 4));
   const uint32_t wlane = (8 * wave + (lane >> 3)) * pitch + chunk * 16;
@@ -412,7 +416,7 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     o.w = p.w + row * pitch;
     o.ws = p.w_scales + row * spitch;
     o.blocks = min(TN, N - t.n0) / 32;
-    o.wsoff = static_cast<uint32_t>(min(64 * wave + lane, N - t.n0 - 1)) * spitch;
+    o.wsoff = static_cast<uint32_t>(min(64 * wave + lane, min(TN, N - t.n0) - 1)) * spitch;
     o.xsoff = static_cast<uint32_t>(max(rows[min(64 * wave + lane, TM - 1)], 0)) * spitch;
 #pragma unroll
     for (int i = 0; i < XL; ++i)
@@ -456,14 +460,14 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
 #pragma unroll
       for (int i = 0; i < G / 2; ++i) {
         load_lds16(wb + (kb * 8 + 16 * i) + wo, sc + kScRows * 4 * i + wave * 256);
-        load_lds16(xb + (kb * 8 + 16 * i) + xo, sc + kScRows * 4 * i + TN * 4 + wave * 256);
+        load_lds16(xb + (kb * 8 + 16 * i) + xo, sc + kScRows * 4 * i + 1024 + wave * 256);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int b = min(2 * kb + i, K / kGroup - 1) * 4;
         load_lds4(wb + b + wo, sc + kScRows * i + wave * 64);
-        load_lds4(xb + b + xo, sc + kScRows * i + TN + wave * 64);
+        load_lds4(xb + b + xo, sc + kScRows * i + 256 + wave * 64);
       }
     }
   };
@@ -492,7 +496,7 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
 #pragma unroll
     for (int i = 0; i < NI; ++i) scw[i] = *reinterpret_cast<const uint4*>(sc + (wrow + 32 * i) * 4);
 #pragma unroll
-    for (int j = 0; j < MI; ++j) scx[j] = *reinterpret_cast<const uint4*>(sc + (TN + xrow + 64 * j) * 4);
+    for (int j = 0; j < MI; ++j) scx[j] = *reinterpret_cast<const uint4*>(sc + (256 + xrow + 64 * j) * 4);
   };
   auto read_stage_scales = [&](const uint32_t* sc) {  // not WIDE
 #pragma unroll
@@ -502,8 +506,8 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
     }
 #pragma unroll
     for (int j = 0; j < MI; ++j) {
-      scx[j].x = sc[TN + xrow + 64 * j];
-      scx[j].y = sc[kScRows + TN + xrow + 64 * j];
+      scx[j].x = sc[256 + xrow + 64 * j];
+      scx[j].y = sc[kScRows + 256 + xrow + 64 * j];
     }
   };
   // The words of K block d (128 wide) of the held stages.
@@ -687,15 +691,15 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   __builtin_amdgcn_s_waitcnt(0);  // no load may land after the workgroup's end
 }
 
-template <int TM>
+template <int TM, int TN>
 hipError_t launch_a4_tiled(const W4Args& g, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(device_cu_count()));
+  const dim3 grid(static_cast<unsigned>(device_cu_count() * (TN < 256 ? 2 : 1)));
   if (g.k % 1024 == 0)
-    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, kA4TileCols, 4>), grid, dim3(kA4TThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, TN, 4>), grid, dim3(kA4TThreads), 0, stream, g);
   else if (g.k % 512 == 0)
-    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, kA4TileCols, 2>), grid, dim3(kA4TThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, TN, 2>), grid, dim3(kA4TThreads), 0, stream, g);
   else
-    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, kA4TileCols, 1>), grid, dim3(kA4TThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_a4_tiled_kernel<TM, TN, 1>), grid, dim3(kA4TThreads), 0, stream, g);
   return hipGetLastError();
 }
 
@@ -737,12 +741,12 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
     return hipGetLastError();
   }
   // The tile height with the least expected time; whole tiles of 64, 128, 192
-  // and 256 rows take 0.39, 0.7, 0.8 and 1. Measured, us: a layer of 64 and 512
-  // tokens over 128 experts of 2048 -> 768, top 8, at 64 / 128: 88/90, 104/106;
-  // 32 experts of 80 rows, K 7168, N 4096: 163/113; of 150, 300, 520 and 1040
-  // rows at 128 / 192 / 256: 172/125/135, 242/201/207, 379/303/318 and
-  // 672/572/550; K 2048, N 7168: 90/78/83, 139/118/121, 225/188/186 and
-  // 404/350/333.
+  // and 256 rows take 0.39, 0.7, 0.8 and 1. Measured, us: a layer of 64, 512
+  // and 1024 tokens over 128 experts of 2048 -> 768, top 8, at 64 / 128: 83/90,
+  // 101/105, 137/125; 32 experts of 40, 64 and 80 rows, K 7168, N 4096: 99/105,
+  // 107/109, 152/115; of 150, 300, 520 and 1040 rows at 128 / 192 / 256:
+  // 172/125/135, 242/201/207, 379/303/318 and 672/572/550; K 2048, N 7168:
+  // 90/78/83, 139/118/121, 225/188/186 and 404/350/333.
   constexpr int kHeights[4] = {64, 128, 192, 256};
   constexpr double kCost[4] = {0.39, 0.7, 0.8, 1.0};
   int best = 0;
@@ -755,10 +759,10 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
     }
   }
   switch (best) {
-    case 0: return launch_a4_tiled<64>(g, stream);
-    case 1: return launch_a4_tiled<128>(g, stream);
-    case 2: return launch_a4_tiled<192>(g, stream);
-    default: return launch_a4_tiled<256>(g, stream);
+    case 0: return launch_a4_tiled<64, 128>(g, stream);
+    case 1: return launch_a4_tiled<128, kA4TileCols>(g, stream);
+    case 2: return launch_a4_tiled<192, kA4TileCols>(g, stream);
+    default: return launch_a4_tiled<256, kA4TileCols>(g, stream);
   }
 }
 

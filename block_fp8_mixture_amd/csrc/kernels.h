@@ -128,10 +128,13 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream);
 // routed pairs, in two launches. hq [pairs, I/2] and hs [pairs, I/32] hold the
 // quantized FC2 input between them, a row per pair. Its two sides, us captured,
 // these launches against the general path's (experts, hidden, inter; pairs):
-//   288, 4096, 512:  8: 15 / 34, 32: 27 / 53, 48: 38 / 71, 64: 50 / 68
-//   32, 7168, 2048:  8: 47 / 77, 32: 118..129 / 142..145, 48: 149 / 153, 64: 167..181 / 157..162
-//   64, 2048, 1024:  6: 16 / 31, 24: 34 / 43, 48: 52 / 50, 64: 61 / 51
-//   16, 4096, 4096:  64: 115..127 / 103..106
+//   288, 4096, 512:   8: 15 / 30, 32: 28 / 49, 40: 36 / 59, 48: 39 / 61
+//   32, 7168, 2048:   8: 46 / 62, 32: 113..122 / 118..130, 40: 140 / 138, 48: 151 / 141
+//   64, 2048, 1024:   6: 16 / 29, 24: 34 / 39, 36: 43 / 39, 48: 53 / 49
+//   16, 4096, 4096:   16: 69 / 88, 32: 93 / 94, 48: 103 / 97
+//   8, 4096, 14336:   8: 125 / 149, 32: 176 / 181, 48: 215 / 188
+//   128, 2048, 768:   32: 35 / 39, 48: 47 / 47
+// Over 48 the general path is ahead on average (64: 61 / 51, 127 / 103, 50 / 68).
 constexpr int kL4MaxPairs = 48;
 static_assert(kL4MaxPairs <= 64);  // a pair per lane
 constexpr size_t kLdsBytes = 160 * 1024;  // of a workgroup
