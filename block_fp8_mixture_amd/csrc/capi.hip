@@ -590,7 +590,7 @@ static moe_status forward_impl(const moe_problem* p, const moe_workspace_layout&
 
   hipError_t e = hipSuccess;
   if (p->scale_fmt == MOE_SCALE_MXFP4 && p->expert_cap == 0 &&
-      moe::layer_a4_fits(p->t_cap, p->topk, p->num_experts, p->hidden, p->inter)) {
+      moe::layer_a4_fits(p->t_cap, p->topk, p->hidden)) {
     // A few tokens: the whole layer in two launches.
     moe::LayerA4Args a;
     a.ids = t->topk_ids;

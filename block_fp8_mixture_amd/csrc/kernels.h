@@ -162,7 +162,7 @@ struct LayerA4Args {
   int token_of = 0;           // set by the launcher: pair -> token
 };
 // Whether launch_layer_a4 takes such a layer.
-bool layer_a4_fits(int t_cap, int topk, int num_experts, int hidden, int inter);
+bool layer_a4_fits(int t_cap, int topk, int hidden);
 hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream);
 
 // BF16 values of an MXFP4 tensor of rows x cols.

@@ -343,14 +343,14 @@ __global__ __launch_bounds__(kL2Threads, 4) void layer_a4_fc2_kernel(LayerA4Args
 
 }  // namespace
 
-bool layer_a4_fits(int t_cap, int topk, int num_experts, int hidden, int inter) {
+bool layer_a4_fits(int t_cap, int topk, int hidden) {
   const int64_t pairs = static_cast<int64_t>(t_cap) * topk;
   return pairs >= 1 && pairs <= kL4MaxPairs && l4_token_bytes(hidden, t_cap) + kL1Lds <= kLdsBytes;
 }
 
 hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream) {
   const int pairs = a.t_cap * a.topk;
-  if (!layer_a4_fits(a.t_cap, a.topk, a.num_experts, a.hidden, a.inter)) return hipErrorInvalidValue;
+  if (!layer_a4_fits(a.t_cap, a.topk, a.hidden)) return hipErrorInvalidValue;
   LayerA4Args p = a;
   p.token_of = 65536 / a.topk + 1;  // q * token_of >> 16 is q / topk for q < 64, topk <= 64
   hipLaunchKernelGGL(layer_a4_fc1_kernel,
