@@ -845,3 +845,16 @@ def test_route_and_layer_follow_the_current_stream():
         got = moe.moe_forward(xs, ids, w, *weights, "mxfp4", weight_fmt="mxfp4")[0]
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("t,k,e,start", [(3, 1, 1, 0), (80, 1, 1, 0), (2, 8, 1024, 0), (12, 4, 1024, 0), (1, 48, 60, 0),
+                                         (1, 64, 70, 0), (6, 8, 1030, 6), (7, 3, 5, 4)])
+def test_layer_of_one_and_of_many_experts(t, k, e, start):
+    say(f"mx4 layer {t} tokens, top {k} of {e} experts from {start}")
+    x, ids, w, w1, w2 = _exact_layer(140 + t, t, e, 128, 128, k)
+    own = slice(start, e)
+    w1, w2 = (w1[0][own], w1[1][own]), (w2[0][own], w2[1][own])
+    out = torch.full((t, 128), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_forward(*[up(v) for v in (x, ids, w, *w1, *w2)], "mxfp4", weight_fmt="mxfp4", out=out, expert_start=start)
+    ref = oracle.token_forward_mx4(x, ids, w, w1, w2, e - start, t, expert_start=start)
+    _check_layer(down(out), ref, t, k)
