@@ -14,9 +14,10 @@
 //
 // Measured, captured: 288 experts of 4096 -> 512, top 8: 15.3 us at 1 token
 // (27 MB of weights), 27.2 us at 4 (about 100 MB: 3.7 TB/s over both launches,
-// where a large copy runs at 4.8). Of the first's 15 us about 6 are the bytes;
-// the rest is two launches' ramps, each a chain of ids, weights, quantization,
-// products and a reduction over the waves. 32 experts of 7168 -> 2048: 47 us at
+// where a large copy runs at 4.8). Alone FC1 takes 9.8 and 16.8 us, FC2 6.1 and
+// 9.8. Of the 15 us of 1 token about 6 are the bytes; the rest is two launches'
+// ramps, each a chain of ids, weights, quantization, products and a reduction
+// over the waves. 32 experts of 7168 -> 2048: 47 us at
 // 1 token (187 MB, 4.0 TB/s). FC1 is bound by its instructions where the
 // weights are in cache, so its addresses are 32-bit offsets from uniform bases
 // and its tokens are found with scalar operations: with 64-bit addresses, a
