@@ -65,6 +65,10 @@ bool fmt_ok(int f) {
   return f == MOE_SCALE_FP32 || f == MOE_SCALE_FP32_POW2 || f == MOE_SCALE_UE8M0 || f == MOE_SCALE_MXFP4;
 }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+// What an MXFP4 quantization loads 16 bytes and stores 4 bytes at a time.
+bool mx_quant_aligned(int fmt, const void* in, const void* codes) {
+  return fmt != MOE_SCALE_MXFP4 || (aligned(in, 16) && aligned(codes, 4));
+}
 bool act_ok(int a) {
   return a == MOE_ACT_SWIGLU || a == MOE_ACT_SWIGLU_CLAMP || a == MOE_ACT_SWIGLU_CLAMP_AFTER_SILU;
 }
@@ -203,7 +207,7 @@ moe_status moe_act_quant(const uint16_t* x, int32_t t_cap, const int32_t* t_live
                          void* xs, void* stream) {
   if (t_cap < 0 || !dim128(hidden) || !fmt_ok(fmt) || !rounding_ok(rounding))
     return MOE_ERR_INVALID_ARG;
-  if (t_cap > 0 && (!x || !xq || !xs)) return MOE_ERR_INVALID_ARG;
+  if (t_cap > 0 && (!x || !xq || !xs || !mx_quant_aligned(fmt, x, xq))) return MOE_ERR_INVALID_ARG;
   if (static_cast<int64_t>(t_cap) * (hidden / 128) > INT32_MAX) return MOE_ERR_INVALID_ARG;
   if (t_cap == 0) return MOE_OK;
   return from_hip(moe::launch_act_quant(x, t_cap, t_live_dev, hidden, fmt, rounding, xq, xs,
@@ -344,7 +348,7 @@ moe_status moe_silu_mul_quant(const uint16_t* gate_up, int32_t inter,
   if (act != MOE_ACT_SWIGLU && !(clamp_limit > 0.0f)) return MOE_ERR_INVALID_ARG;
   if (num_experts > moe::kMaxExperts) return MOE_ERR_UNSUPPORTED;  // the kernel's LDS endpoint table
   if (!expert_counts || !expert_offsets) return MOE_ERR_INVALID_ARG;
-  if (row_cap > 0 && (!gate_up || !hq || !hs)) return MOE_ERR_INVALID_ARG;
+  if (row_cap > 0 && (!gate_up || !hq || !hs || !mx_quant_aligned(fmt, gate_up, hq))) return MOE_ERR_INVALID_ARG;
   if (static_cast<int64_t>(row_cap) * (inter / 128) > INT32_MAX) return MOE_ERR_INVALID_ARG;
   if (row_cap == 0) return MOE_OK;
   return from_hip(moe::launch_silu_mul_quant(gate_up, inter, expert_counts, expert_offsets,
@@ -364,7 +368,7 @@ moe_status moe_silu_mul_quant_masked(const uint16_t* gate_up, int32_t inter,
   if (act != MOE_ACT_SWIGLU && !(clamp_limit > 0.0f)) return MOE_ERR_INVALID_ARG;
   const int64_t rows = static_cast<int64_t>(num_experts) * expert_cap;
   if (rows > INT32_MAX / 2 || rows * (inter / 128) > INT32_MAX) return MOE_ERR_INVALID_ARG;
-  if (!masked_m || !gate_up || !hq || !hs) return MOE_ERR_INVALID_ARG;
+  if (!masked_m || !gate_up || !hq || !hs || !mx_quant_aligned(fmt, gate_up, hq)) return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_silu_mul_quant(gate_up, inter, masked_m, nullptr, num_experts,
                                              static_cast<int>(rows), act, clamp_limit, fmt,
                                              rounding, hq, hs, expert_cap, as_stream(stream)));

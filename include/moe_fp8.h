@@ -254,7 +254,8 @@ moe_status moe_align_batched(const int32_t* topk_ids, int32_t t_cap, const int32
  *   xq    device uint8 [t_cap, hidden]; rows t >= t_live untouched
  *   xs    device scales [hidden/128][t_cap] (float or uint8, per `fmt`)
  *   rounding  the quantizer's convention (moe_rounding)
- * MOE_SCALE_MXFP4: xq uint8 [t_cap, hidden/2], xs uint8 [t_cap, hidden/32].
+ * MOE_SCALE_MXFP4: xq uint8 [t_cap, hidden/2], xs uint8 [t_cap, hidden/32]; x
+ * is 16-byte and xq 4-byte aligned (INVALID_ARG otherwise).
  * It also quantizes weights: BF16 [rows, K] to an MXFP4 expert's codes and
  * scale bytes.
  * Errors: INVALID_ARG (hidden not a positive multiple of 128, null pointers,
@@ -379,7 +380,8 @@ moe_status moe_grouped_gemm_mxfp4(const uint8_t* a, const void* a_scales, moe_sc
  *   clamp_limit  used by the clamp variants; must be > 0 there
  *   rounding  moe_rounding; MOE_ROUND_RECIPROCAL rounds SiLU(gate)*up to BF16
  *             before quantizing it
- * MOE_SCALE_MXFP4: hq uint8 [row_cap, inter/2], hs uint8 [row_cap, inter/32].
+ * MOE_SCALE_MXFP4: hq uint8 [row_cap, inter/2], hs uint8 [row_cap, inter/32];
+ * gate_up is 16-byte and hq 4-byte aligned (INVALID_ARG otherwise).
  * Errors: INVALID_ARG (also when row_cap * inter / 128 exceeds 2^31 - 1). */
 moe_status moe_silu_mul_quant(const uint16_t* gate_up, int32_t inter,
                               const int32_t* expert_counts, const int32_t* expert_offsets,

@@ -858,3 +858,19 @@ def test_layer_of_one_and_of_many_experts(t, k, e, start):
     moe.moe_forward(*[up(v) for v in (x, ids, w, *w1, *w2)], "mxfp4", weight_fmt="mxfp4", out=out, expert_start=start)
     ref = oracle.token_forward_mx4(x, ids, w, w1, w2, e - start, t, expert_start=start)
     _check_layer(down(out), ref, t, k)
+
+
+def test_misaligned_quantization_is_refused():
+    """Views one element into a buffer: refused before any launch; scale bytes
+    may lie anywhere."""
+    x = torch.zeros(4 * 256 + 8, dtype=torch.bfloat16, device=dev())
+    with pytest.raises(moe.MoeError):
+        moe.moe_act_quant(x[1:1 + 1024].view(4, 256), "mxfp4")
+    codes = torch.zeros(4 * 128 + 4, dtype=torch.uint8, device=dev())
+    with pytest.raises(moe.MoeError):
+        moe.moe_act_quant(x[:1024].view(4, 256), "mxfp4", xq=codes[1:513].view(4, 128))
+    scales = torch.full((33,), POISON_U8, dtype=torch.uint8, device=dev())
+    v = up(_bf16(_rng(150).standard_normal((4, 256))))
+    xq, xs = moe.moe_act_quant(v, "mxfp4", xs=scales[1:].view(4, 8))
+    xq2, xs2 = moe.moe_act_quant(v, "mxfp4")
+    assert torch.equal(xq, xq2) and torch.equal(xs, xs2) and scales[0].item() == POISON_U8

@@ -71,6 +71,14 @@ def test_mxfp4_format_of_the_stages(lib):
     assert f(FAKE, FAKE, MX, 64, NULL, 1, FAKE, FAKE, FAKE, 4, 16, 256, 256, FAKE, NULL, NULL) == UNSUPPORTED
 
 
+def test_mxfp4_quantization_alignment(lib):
+    q, s, m = lib.moe_act_quant, lib.moe_silu_mul_quant, lib.moe_silu_mul_quant_masked
+    for x, c in ((EIGHT, FAKE), (ODD, FAKE), (FAKE, ODD)):
+        assert q(x, 4, NULL, 256, MX, 0, c, FAKE, NULL) == INVALID
+        assert s(x, 256, FAKE, FAKE, 4, 64, 0, 7.0, MX, 0, c, FAKE, NULL) == INVALID
+        assert m(x, 256, FAKE, 4, 16, 0, 7.0, MX, 0, c, FAKE, NULL) == INVALID
+
+
 def test_mxfp4_gemm_alignment(lib):
     f = lib.moe_grouped_gemm_mxfp4
 
