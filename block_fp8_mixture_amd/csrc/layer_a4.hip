@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kL1Threads, 4) void layer_a4_fc1_kernel(LayerA4Args
   if (k < nt) {
     const int src = 16 * ((c & 15) >> 2) + k;
     const uint2 b = pack_bf16x4(v4f{s_part[0][c >> 4][src][c & 3], s_part[0][2 + (c >> 4)][src][c & 3], 0.0f, 0.0f});  // C1 is BF16
-    const float y = swiglu_any(a.act, bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), a.act_limit, a.rounding);
+    const float y = swiglu_any<true>(a.act, bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), a.act_limit, a.rounding);
     // The block's largest magnitude, over the 32 lanes that hold it (all or
     // none of them are here).
     uint32_t amax = quad_max_u32(__float_as_uint(y) & 0x7FFFFFFFu);

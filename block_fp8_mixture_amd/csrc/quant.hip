@@ -90,9 +90,9 @@ __global__ __launch_bounds__(kSmqThreads) void silu_mul_quant_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if constexpr (decltype(use_lut)::value)
-            y.v[i] = swiglu_lut<ACT>(g8.v[i], u8.v[i], lim, s_lut);
+            y.v[i] = swiglu_lut<ACT, FMT == kMxfp4>(g8.v[i], u8.v[i], lim, s_lut);
           else
-            y.v[i] = swiglu<ACT>(g8.v[i], u8.v[i], lim);
+            y.v[i] = swiglu<ACT, FMT == kMxfp4>(g8.v[i], u8.v[i], lim);
         }
         if (rnd == kReciprocal) {  // the SwiGLU output rounded to BF16 first
 #pragma unroll

@@ -87,17 +87,40 @@ enum Act : int { kSwiglu = 0, kSwigluClamp = 1, kSwigluClampAfterSilu = 2 };
 // before SiLU, or clamp SiLU's output above and up to [-L, L].
 __device__ __forceinline__ double silu_f64(double g) { return g / (1.0 + exp(-g)); }
 
-template <int ACT>
+// KEEP_NAN: the clamps of 4-bit activations keep a NaN, whose block the format
+// can mark (fmin and fmax return their other operand: a NaN gate would become
+// the limit, a NaN up minus the limit, and the token a number). FP8 codes take
+// finite inputs. Gates, ups and the limit are floats, so comparing them as
+// floats gives the same values and costs less than in double (32768 rows of
+// 2048, SiLU and MXFP4 quantization: 74.4 us clamped, 72.9 clamped after SiLU,
+// against 78.5 and 76.8).
+template <bool KEEP_NAN>
+__device__ __forceinline__ double clamp_gate(float g, double lim) {
+  const float l = static_cast<float>(lim);
+  return KEEP_NAN ? (g > l ? l : g) : fmin(static_cast<double>(g), lim);
+}
+template <bool KEEP_NAN>
+__device__ __forceinline__ double clamp_up(float u, double lim) {
+  const float l = static_cast<float>(lim);
+  return KEEP_NAN ? (fabsf(u) > l ? __builtin_copysignf(l, u) : u)
+                  : fmin(fmax(static_cast<double>(u), -lim), lim);
+}
+template <bool KEEP_NAN>
+__device__ __forceinline__ double clamp_silu(double s, double lim) {
+  return KEEP_NAN ? (s > lim ? lim : s) : fmin(s, lim);
+}
+
+template <int ACT, bool KEEP_NAN>
 __device__ __forceinline__ float swiglu(float gf, float uf, double lim) {
   double g = gf, u = uf;
   if (ACT == kSwigluClamp) {
-    g = fmin(g, lim);
-    u = fmin(fmax(u, -lim), lim);
+    g = clamp_gate<KEEP_NAN>(gf, lim);
+    u = clamp_up<KEEP_NAN>(uf, lim);
   }
   double s = silu_f64(g);
   if (ACT == kSwigluClampAfterSilu) {
-    s = fmin(s, lim);
-    u = fmin(fmax(u, -lim), lim);
+    s = clamp_silu<KEEP_NAN>(s, lim);
+    u = clamp_up<KEEP_NAN>(uf, lim);
   }
   return static_cast<float>(s * u);
 }
@@ -134,13 +157,13 @@ __device__ __forceinline__ int silu_lut_index(float g) {
 
 // swiglu<ACT> with the SiLU from `lut` (filled by fill_silu_lut) where it
 // has the gate.
-template <int ACT>
+template <int ACT, bool KEEP_NAN>
 __device__ __forceinline__ float swiglu_lut(float gf, float uf, double lim, const double* lut) {
   float g = gf;
   double u = uf;
   if (ACT == kSwigluClamp) {
-    g = static_cast<float>(fmin(static_cast<double>(gf), lim));  // gf or the limit, both floats
-    u = fmin(fmax(u, -lim), lim);
+    g = static_cast<float>(clamp_gate<KEEP_NAN>(gf, lim));  // gf or the limit, both floats
+    u = clamp_up<KEEP_NAN>(uf, lim);
   }
   const int i = silu_lut_index(g);
   double s;
@@ -149,8 +172,8 @@ __device__ __forceinline__ float swiglu_lut(float gf, float uf, double lim, cons
   else
     s = silu_f64(g);
   if (ACT == kSwigluClampAfterSilu) {
-    s = fmin(s, lim);
-    u = fmin(fmax(u, -lim), lim);
+    s = clamp_silu<KEEP_NAN>(s, lim);
+    u = clamp_up<KEEP_NAN>(uf, lim);
   }
   return static_cast<float>(s * u);
 }
@@ -159,14 +182,15 @@ __device__ __forceinline__ float swiglu_lut(float gf, float uf, double lim, cons
 // reciprocal convention the result is rounded to BF16 (TensorRT-LLM PR
 // #21250, rounding-fix commit message: the fused op's epilogue rounds the
 // SwiGLU output to BF16 before its FP8 quantization).
+template <bool KEEP_NAN = false>
 __device__ __forceinline__ float swiglu_any(int act, float g, float u, double lim, int rnd) {
   float y;
   if (act == kSwigluClamp)
-    y = swiglu<kSwigluClamp>(g, u, lim);
+    y = swiglu<kSwigluClamp, KEEP_NAN>(g, u, lim);
   else if (act == kSwigluClampAfterSilu)
-    y = swiglu<kSwigluClampAfterSilu>(g, u, lim);
+    y = swiglu<kSwigluClampAfterSilu, KEEP_NAN>(g, u, lim);
   else
-    y = swiglu<kSwiglu>(g, u, lim);
+    y = swiglu<kSwiglu, KEEP_NAN>(g, u, lim);
   return rnd == kReciprocal ? round_bf16(y) : y;
 }
 

@@ -109,7 +109,9 @@ typedef enum {
  * clamp after SiLU; vLLM PR #65794, Details: clamp_limit). With limit L:
  *   SWIGLU                   y = silu(g) * u
  *   SWIGLU_CLAMP             y = silu(min(g, L)) * clamp(u, -L, L)
- *   SWIGLU_CLAMP_AFTER_SILU  y = min(silu(g), L) * clamp(u, -L, L)          */
+ *   SWIGLU_CLAMP_AFTER_SILU  y = min(silu(g), L) * clamp(u, -L, L)
+ * With MOE_SCALE_MXFP4 a NaN passes the clamps and marks its block; the FP8
+ * formats expect finite inputs.                                            */
 /* Expert weight formats.
  *   MOE_WEIGHT_E4M3   FP8 E4M3 codes [E, rows, cols] with float32 scales per
  *                     128x128 block [E, rows/128, cols/128] (vLLM PR #59128,
