@@ -37,6 +37,14 @@ __device__ __forceinline__ int a4_rows(const W4Args& p, int e) {
   return segment_rows(s0, s1, p.counts[e], p.row_cap);
 }
 
+// Row of A behind row r, -1 if there is none. The entry's own sign decides:
+// divided first, -1 .. -(a_row_div - 1) would be row 0.
+__device__ __forceinline__ int a4_source(const W4Args& p, int r) {
+  const int v = p.a_row_map ? p.a_row_map[r] : r;
+  const int src = p.a_row_map ? v / p.a_row_div : r;
+  return v >= 0 && src < p.a_rows ? src : -1;
+}
+
 // Exclusive prefix over the experts of units(e), into s_pref[0..E]; all
 // threads of the workgroup call it.
 template <typename Units>
@@ -188,12 +196,7 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
 #pragma unroll
       for (int m = 0; m < kA4Tiles; ++m) {
         const int j = 16 * m + r16;
-        int src = -1;
-        if (j < rows_here) {
-          const int r = row0 + j;
-          src = p.a_row_map ? p.a_row_map[r] / p.a_row_div : r;
-          if (static_cast<unsigned>(src) >= static_cast<unsigned>(p.a_rows)) src = -1;
-        }
+        const int src = j < rows_here ? a4_source(p, row0 + j) : -1;
         has[m] = src >= 0;
         t.xrow[m] = static_cast<uint32_t>(max(src, 0)) * pitch;
         t.xsrow[m] = static_cast<uint32_t>(max(src, 0)) * spitch;
@@ -369,10 +372,7 @@ __global__ __launch_bounds__(kA4TThreads, 1) void gemm_a4_tiled_kernel(W4Args p)
   };
   // Source row of row `tid` of a tile, -1 if it has none.
   auto row_source = [&](const A4Tile& t) {
-    if (tid >= t.rows) return -1;
-    const int r = t.row0 + tid;
-    const int src = p.a_row_map ? p.a_row_map[r] / p.a_row_div : r;
-    return static_cast<unsigned>(src) < static_cast<unsigned>(p.a_rows) ? src : -1;
+    return tid < t.rows ? a4_source(p, t.row0 + tid) : -1;
   };
 
   // Workgroups go round-robin over the 8 XCDs: neighbouring tiles, which share

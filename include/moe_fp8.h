@@ -335,7 +335,9 @@ moe_status moe_grouped_gemm_fp8_masked(const uint8_t* a, const void* a_scales, m
  * With fmt MOE_SCALE_MXFP4 A is an MXFP4 tensor (a [a_rows, k/2], a_scales
  * [a_rows, k/32]), and the matrix cores apply both operands' scales:
  *   C[r, n] = bf16( sum_j a(ar, j) * w(e, n, j) ), accumulated in fp32.
- * All of a, a_scales, w, w_scales and c are then 16-byte aligned.
+ * All of a, a_scales, w, w_scales and c are then 16-byte aligned. A live row
+ * whose a_row_map entry is negative (-1 marks a row without a pair) or past
+ * the end gets zeros.
  *
  *   a, a_scales, fmt, a_rows, a_row_map, a_row_div   as moe_grouped_gemm_fp8
  *   w          device uint8 [num_experts, n, k/2] packed E2M1 codes

@@ -8,8 +8,8 @@ import torch
 
 import block_fp8_mixture_amd as moe
 import oracle
-from tests.gpu_helpers import POISON_U8, dev, down, say, up
-from tests.test_gpu_mx4 import ACTS, _aligned, _bf16, _bf16_any, _exact_layer, _rng
+from tests.gpu_helpers import POISON_BF16, POISON_U8, dev, down, say, up
+from tests.test_gpu_mx4 import ACTS, TILED, _aligned, _bf16, _bf16_any, _exact_layer, _gemm, _rng
 
 pytestmark = pytest.mark.gpu
 
@@ -76,6 +76,33 @@ def test_layer_keeps_a_bad_token_to_itself_under_every_activation(t, k, cap, rou
     keep[[t // 2, t - 1]] = False
     assert np.array_equal(got[keep], clean[keep])
     assert np.isnan(oracle.bf16_bits_to_f64(got[~keep])).all()
+
+
+@pytest.mark.parametrize("counts,n", [([3, 20], 256), ([300, 90], 256), (TILED[0], 8192), (TILED[3], 8192)])
+def test_rows_whose_map_entry_is_negative_or_past_the_end_are_zero(counts, n):
+    """-1 .. -(div - 1) divide to 0 in C; they have no source all the same
+    (-1 is how an alignment marks a row without a pair)."""
+    say(f"mx4 gemm, negative map entries, {counts} n={n}")
+    counts, offsets, row_cap, a, asc, w, ws, row_map = _gemm(counts, n, 512, 1, True, 220)
+    live = np.flatnonzero(row_map >= 0)
+    bad = {int(live[i]): v for i, v in ((0, -1), (2, -3), (5, -2), (7, -4), (9, -2 ** 31), (-1, -1),
+                                        (-2, 4 * len(a)), (-4, 2 ** 31 - 1))}
+    for r, v in bad.items():
+        row_map[r] = v
+    out = torch.full((row_cap, n), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_grouped_gemm_mxfp4(up(a), up(asc), "mxfp4", up(w), up(ws), up(counts), up(offsets), row_cap,
+                               a_row_map=up(row_map), a_row_div=4, out=out)
+    got = down(out)
+    for r in bad:
+        assert not (got[r] & 0x7FFF).any(), (r, bad[r])
+    for e, c in enumerate(counts):  # the rest of the rows keep theirs
+        rows = np.array([r for r in range(offsets[e], offsets[e] + c) if r not in bad], np.int64)
+        if len(rows):
+            src = row_map[rows] // 4
+            av, wv = oracle.mxfp4_dequant(a[src], asc[src]), oracle.mxfp4_dequant(w[e], ws[e])
+            want, mag = av @ wv.T, np.abs(av) @ np.abs(wv).T
+            err = np.abs(oracle.bf16_bits_to_f64(got[rows]) - want)
+            assert np.all(err <= 2.0 ** -8 * np.abs(want) + 512 * 2.0 ** -23 * mag), e
 
 
 @pytest.mark.parametrize("rounding", ["divide", "reciprocal"])
