@@ -162,6 +162,11 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
+// A workgroup's number in a grid of flat_grid.
+__device__ __forceinline__ int64_t flat_block() {
+  return static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+}
+
 __device__ __forceinline__ int clamp_live(const int32_t* t_live_dev, int t_cap) {
   if (t_live_dev == nullptr) return t_cap;
   int t = *t_live_dev;

@@ -12,6 +12,15 @@ constexpr int kStreamMaxRows = 64;    // experts with at most this many rows str
 constexpr int kTiledTileM = 256;      // row tile of the MFMA-tiled GEMM
 constexpr int kColTile = 128;         // column tile (= weight block rows)
 
+// A grid of `blocks` workgroups in order of y, then x (flat_block; up to one
+// row of x more than asked for). A dimension holds fewer than 2^32 threads: the
+// runtime launches what is left of a larger one past that and reports success.
+inline dim3 flat_grid(int64_t blocks) {
+  constexpr int64_t kRow = int64_t{1} << 21;  // of at most 1024 threads: 2^31
+  if (blocks <= kRow) return dim3(static_cast<unsigned>(blocks));
+  return dim3(static_cast<unsigned>(kRow), static_cast<unsigned>((blocks + kRow - 1) / kRow));
+}
+
 // How routed ids become rows: local ids id - expert_start (other ids are
 // dropped); batch_cap > 0 selects the batched layout of batch_cap rows per
 // expert, whose pairs past the capacity are dropped and counted into

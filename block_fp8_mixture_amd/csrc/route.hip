@@ -113,7 +113,7 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 63, sub = lane & (L - 1);
   const int t_live = clamp_live(a.t_live_dev, a.t_cap);
   const int slot = threadIdx.x / L;  // of the workgroup's tokens
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kRtWaves * T) + slot;
+  const int64_t t = flat_block() * (kRtWaves * T) + slot;
   if (t - lane / L >= t_live) return;  // the wave's first token
   const int E = t < t_live ? a.num_experts : 0;
   float x[V];
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kRtThreads) void route_kernel(RouteArgs a) {
 template <int L, int V>
 void route_bg(const RouteArgs& a, hipStream_t stream) {
   const int tokens = kRtThreads / L;  // of a workgroup
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.t_cap) + tokens - 1) / tokens));
+  const dim3 grid = flat_grid((static_cast<int64_t>(a.t_cap) + tokens - 1) / tokens);
   const bool grouped = a.num_groups > 1;
   if (a.bias && grouped)
     hipLaunchKernelGGL((route_kernel<L, V, true, true>), grid, dim3(kRtThreads), 0, stream, a);

@@ -119,3 +119,32 @@ def test_silu_quantization_of_subnormal_products(rounding):
     codes, scales = _quantized(gu, inter, "swiglu", np.inf, rounding)
     assert (scales == 0).any() and (scales > 0).any()
     assert np.array_equal(down(hs), scales) and np.array_equal(down(hq), codes)
+
+
+@pytest.mark.parametrize("tokens,experts,topk,kw", [
+    ((1 << 28) + 48, 2, 1, {}),  # 16 lanes per token
+    ((1 << 26) + 12, 17, 1, dict(num_groups=17, top_groups=17, renormalize=False)),  # 64
+])
+def test_route_past_two_to_the_32_threads(tokens, experts, topk, kw):
+    """More lanes than one dimension of a grid holds: every token is routed,
+    and none past the last."""
+    say(f"route of {tokens} tokens, {experts} experts")
+    l = torch.zeros((tokens, experts), dtype=torch.bfloat16, device=dev())
+    # The picked expert and its logit vary along the tokens.
+    t = torch.arange(tokens, device=dev())
+    pick = (t * 40503 >> 7) % experts
+    l.scatter_(1, pick[:, None], 1.0)
+    l[0::5] *= 2
+    del t
+    ids = torch.full((tokens + 8, topk), -9, dtype=torch.int32, device=dev())
+    w = torch.full((tokens + 8, topk), -9.0, device=dev())
+    moe.moe_route(l, topk, ids=ids[:tokens], weights=w[:tokens], **kw)
+    assert torch.equal(ids[:tokens, 0], pick.int())
+    best = torch.where(torch.arange(tokens, device=dev()) % 5 == 0, 2.0, 1.0)
+    want = 1.0 if kw == {} else None  # a renormalized single pick weighs one
+    if want is None:
+        two, one = (np.exp(v) / (np.exp(v) + experts - 1) for v in (2.0, 1.0))
+        want = torch.where(best == 2.0, two, one).float()
+    # A double rounded once, on both sides of the double's own error.
+    assert (w[:tokens, 0] - want).abs().max().item() <= 2.0 ** -24
+    assert ids[tokens:].eq(-9).all() and w[tokens:].eq(-9.0).all()
