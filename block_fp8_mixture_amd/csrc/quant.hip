@@ -26,7 +26,7 @@ template <int FMT>
 __global__ __launch_bounds__(kThreads) void act_quant_kernel(
     const uint16_t* __restrict__ x, int t_cap, const int32_t* __restrict__ t_live_dev,
     int hidden, uint8_t* __restrict__ xq, void* __restrict__ xs, int rnd) {
-  const int64_t gid = static_cast<int64_t>(blockIdx.x) * kGroupsPerBlock + (threadIdx.x >> 4);
+  const int64_t gid = flat_block() * kGroupsPerBlock + (threadIdx.x >> 4);
   act_quant_group<FMT>(x, t_cap, t_live_dev, hidden, xq, xs, gid, threadIdx.x & 15, rnd);
 }
 
@@ -159,9 +159,9 @@ template <int FMT>
 hipError_t act_quant_fmt(const uint16_t* x, int t_cap, const int32_t* t_live_dev, int hidden,
                          uint8_t* xq, void* xs, int rnd, hipStream_t stream) {
   const int64_t groups = static_cast<int64_t>(t_cap) * (hidden / kGroup);
-  const int blocks = static_cast<int>((groups + kGroupsPerBlock - 1) / kGroupsPerBlock);
+  const int64_t blocks = (groups + kGroupsPerBlock - 1) / kGroupsPerBlock;
   if (blocks == 0) return hipSuccess;
-  hipLaunchKernelGGL(act_quant_kernel<FMT>, dim3(blocks), dim3(kThreads), 0, stream, x, t_cap,
+  hipLaunchKernelGGL(act_quant_kernel<FMT>, flat_grid(blocks), dim3(kThreads), 0, stream, x, t_cap,
                      t_live_dev, hidden, xq, xs, rnd);
   return hipGetLastError();
 }

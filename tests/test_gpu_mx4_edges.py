@@ -148,3 +148,27 @@ def test_route_past_two_to_the_32_threads(tokens, experts, topk, kw):
     # A double rounded once, on both sides of the double's own error.
     assert (w[:tokens, 0] - want).abs().max().item() <= 2.0 ** -24
     assert ids[tokens:].eq(-9).all() and w[tokens:].eq(-9.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "ue8m0"])
+def test_quantization_past_two_to_the_32_threads(fmt):
+    """2^28 groups of 128 and a few rows more (64 GiB of BF16, as a tensor of
+    weights quantized at once may be): the first and last rows and the bytes
+    about the 2^32-thread border are those of a short call."""
+    cols, rows = 1 << 15, (1 << 20) + 3
+    say(f"quantization of {rows} x {cols} {fmt}")
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device=dev())
+    probe = [0, 1, 4097, (1 << 19) + 5, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, rows - 1]
+    g = torch.Generator(device=dev()).manual_seed(9)
+    part = torch.randn((len(probe), cols), generator=g, device=dev()).bfloat16()
+    x[probe] = part
+    want_q, want_s = moe.moe_act_quant(part, fmt)
+    xq, xs = moe.moe_act_quant(x, fmt, xq=torch.full((rows, want_q.shape[1]), POISON_U8, dtype=torch.uint8, device=dev()))
+    assert torch.equal(xq[probe], want_q)
+    assert torch.equal(xs[probe] if fmt == "mxfp4" else xs[:, probe], want_s)
+    rest = torch.ones(rows, dtype=torch.bool, device=dev())
+    rest[probe] = False
+    for lo in range(0, rows, 1 << 17):  # zeros everywhere else
+        assert not xq[lo:lo + (1 << 17)][rest[lo:lo + (1 << 17)]].any(), lo
+    del x, xq, xs
+    torch.cuda.empty_cache()
