@@ -29,9 +29,10 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
     const float* __restrict__ topk_w, int t_cap, const int32_t* __restrict__ t_live_dev,
     int topk, int hidden, uint16_t* __restrict__ out) {
   const int n_cb = (hidden + kCols - 1) / kCols;
-  const int t = blockIdx.x / n_cb;
-  const int c = (blockIdx.x % n_cb) * kCols + threadIdx.x * 8;
-  if (c >= hidden) return;
+  const uint32_t b = static_cast<uint32_t>(flat_block());  // at most 2^31 + 2^21
+  const int t = static_cast<int>(b / n_cb);
+  const int c = static_cast<int>(b % n_cb) * kCols + threadIdx.x * 8;
+  if (c >= hidden || t >= t_cap) return;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
@@ -80,7 +81,7 @@ hipError_t launch_topk_combine(const uint16_t* y, int row_cap, const int32_t* pa
   if (t_cap == 0) return hipSuccess;
   const int64_t blocks = static_cast<int64_t>(t_cap) * ((hidden + kCols - 1) / kCols);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(combine_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, y, row_cap,
+  hipLaunchKernelGGL(combine_kernel, flat_grid(blocks), dim3(kThreads), 0, stream, y, row_cap,
                      pair_to_row, topk_w, t_cap, t_live_dev, topk, hidden, out);
   return hipGetLastError();
 }

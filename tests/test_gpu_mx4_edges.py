@@ -172,3 +172,19 @@ def test_quantization_past_two_to_the_32_threads(fmt):
         assert not xq[lo:lo + (1 << 17)][rest[lo:lo + (1 << 17)]].any(), lo
     del x, xq, xs
     torch.cuda.empty_cache()
+
+
+def test_combine_past_two_to_the_32_threads():
+    """2^25 workgroups of 128 threads and a few more, as the last step of a
+    layer of that many tokens: every token has its row, rows behind the last stay."""
+    tokens, hidden, rows = (1 << 25) + 21, 128, 1000
+    say(f"combine of {tokens} tokens of {hidden}")
+    y = torch.randn((rows, hidden), device=dev()).bfloat16()
+    pair_to_row = ((torch.arange(tokens, device=dev()) * 40503 >> 3) % (rows + 1) - 1).int()  # -1: none
+    w = torch.ones((tokens, 1), device=dev())
+    out = torch.full((tokens + 4, hidden), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_topk_combine(y, pair_to_row, w, out=out[:tokens])
+    want = torch.cat([y.view(torch.int16), torch.zeros((1, hidden), dtype=torch.int16, device=dev())])
+    for lo in range(0, tokens, 1 << 22):
+        assert torch.equal(out[lo:min(lo + (1 << 22), tokens)], want[pair_to_row[lo:lo + (1 << 22)].long()]), lo
+    assert out[tokens:].eq(POISON_BF16).all()
