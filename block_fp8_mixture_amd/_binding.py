@@ -38,6 +38,9 @@ def decode_layer_applies(t_cap, topk, hidden, inter, weight_fmt="e4m3"):
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "capacity too small",
            4: "HIP runtime error"}
 
+# ctypes keeps the low 32 bits of a larger int32 argument without a word.
+_PAST_INT32 = "sizes must be below 2**31"
+
 _lock = threading.Lock()
 _lib = None
 
@@ -287,6 +290,9 @@ def moe_route(logits, topk, score="softmax", bias=None, renormalize=True, scale=
         raise ValueError("the columns of logits must be contiguous and its rows apart")
     if score not in SCORES:
         raise ValueError(f"score must be one of {list(SCORES)}")
+    num_groups, top_groups, group_top = int(num_groups), int(top_groups), int(group_top)
+    if (t_cap | num_experts | topk | num_groups | top_groups | group_top) >> 31 not in (0, -1):
+        raise ValueError(_PAST_INT32)
     if bias is not None:
         _exact(bias, "bias", torch.float32, (num_experts,))
     if ids is None:
@@ -297,7 +303,7 @@ def moe_route(logits, topk, score="softmax", bias=None, renormalize=True, scale=
     _exact(weights, "weights", torch.float32, (t_cap, topk))
     dev = _same_device(logits, bias, ids, weights, t_live)
     router = _Router(num_experts, topk, SCORES[score], int(bool(renormalize)), float(scale),
-                     int(num_groups), int(top_groups), int(group_top))
+                     num_groups, top_groups, group_top)
     _enqueue("moe_route", dev, ctypes.byref(router), _ptr(logits), LOGIT_TYPES[logits.dtype], ld,
              _ptr(bias), t_cap, _live(t_live), _ptr(ids), _ptr(weights))
     return ids, weights
@@ -311,6 +317,8 @@ def moe_mxfp4_dequant(codes, scales, out=None):
     if not shape or shape[-1] < 16 or shape[-1] % 16:
         raise ValueError("codes must be [..., cols / 2] with cols a multiple of 32")
     lead, cols = shape[:-1], 2 * shape[-1]
+    if cols >> 31:
+        raise ValueError(_PAST_INT32)
     _exact(scales, "scales", torch.uint8, lead + (cols // 32,))
     if out is None:
         out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
