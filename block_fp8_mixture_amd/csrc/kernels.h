@@ -121,7 +121,7 @@ struct W4Args {
   int seg_cap;
   int num_experts;
   int row_cap;
-  int max_rows_per_expert;  // host bound on counts[e]: selects the kernels, never the result
+  int max_rows_per_expert;  // host bound on counts[e]: selects the kernels (MXFP4 activations: and the order of a row's sum)
   int n;
   int k;
   uint16_t* c;

@@ -337,7 +337,10 @@ moe_status moe_grouped_gemm_fp8_masked(const uint8_t* a, const void* a_scales, m
  *   C[r, n] = bf16( sum_j a(ar, j) * w(e, n, j) ), accumulated in fp32.
  * All of a, a_scales, w, w_scales and c are then 16-byte aligned. A live row
  * whose a_row_map entry is negative (-1 marks a row without a pair) or past
- * the end gets zeros.
+ * the end gets zeros. The order in which a row's products are added follows
+ * the launch (row_cap, max_rows_per_expert, the rows of the other experts), so
+ * low bits may differ between two calls that differ in these; the same call
+ * gives the same bits.
  *
  *   a, a_scales, fmt, a_rows, a_row_map, a_row_div   as moe_grouped_gemm_fp8
  *   w          device uint8 [num_experts, n, k/2] packed E2M1 codes
@@ -347,7 +350,8 @@ moe_status moe_grouped_gemm_fp8_masked(const uint8_t* a, const void* a_scales, m
  *              (expert_counts is masked_m, expert_offsets is not read, expert
  *              e's rows start at e*expert_cap, row_cap = num_experts*expert_cap)
  *   max_rows_per_expert  host-side bound on any counts[e] (0 = row_cap); it
- *              only selects which kernels are launched, never the result
+ *              only selects which kernels are launched, with FP8 activations
+ *              never the result
  *   c          device BF16 [row_cap, n]; only live rows written
  * Errors: INVALID_ARG (n or k not positive multiples of 128, null pointers,
  * a_row_div < 1, unknown fmt, a_rows < 1 with rows to compute, a batched

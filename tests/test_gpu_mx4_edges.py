@@ -9,7 +9,8 @@ import torch
 import block_fp8_mixture_amd as moe
 import oracle
 from tests.gpu_helpers import POISON_BF16, POISON_U8, dev, down, say, up
-from tests.test_gpu_mx4 import ACTS, TILED, _aligned, _bf16, _bf16_any, _exact_layer, _gemm, _rng
+from tests.test_gpu_mx4 import (ACTS, TILED, _aligned, _bf16, _bf16_any, _check_gemm, _exact_layer, _gemm,
+                                _rng)
 
 pytestmark = pytest.mark.gpu
 
@@ -103,6 +104,36 @@ def test_rows_whose_map_entry_is_negative_or_past_the_end_are_zero(counts, n):
             want, mag = av @ wv.T, np.abs(av) @ np.abs(wv).T
             err = np.abs(oracle.bf16_bits_to_f64(got[rows]) - want)
             assert np.all(err <= 2.0 ** -8 * np.abs(want) + 512 * 2.0 ** -23 * mag), e
+
+
+@pytest.mark.parametrize("counts,align,bounds", [([40, 200, 3, 64], 16, (0, 200, 256, 1024)),
+                                                  ([16, 15, 3, 16], 128, (0, 16, 64, 1024))])
+def test_product_alone_among_others_and_under_other_bounds(counts, align, bounds):
+    """An expert's rows alone, among other experts' and under other host
+    bounds: within the bound of the product each time (the order of a row's sum
+    follows the launch), and the same bits when the same call is made again.
+    Scales 2**50 apart, so that the sums do round."""
+    n, k = 8192, 1024
+    counts, offsets, _, a, asc, w, ws, _ = _gemm(counts, n, k, align, False, 230)
+    g = _rng(231)
+    asc, ws = (g.integers(100, 150, v.shape).astype(np.uint8) for v in (asc, ws))
+    dw, dws = up(w), up(ws)
+    calls = [(slice(0, 4), b) for b in bounds]
+    calls += [(slice(e, e + 1), b) for e in range(4) for b in (0, int(counts[e]))]
+    for own, bound in calls:
+        say(f"mx4 gemm of experts {own.start}..{own.stop - 1} under bound {bound}")
+        c, first = counts[own], int(offsets[own.start])
+        o = offsets[own.start:own.stop + 1] - np.int32(first)
+        cap = int(o[-1])
+        av, asv = a[first:first + cap], asc[first:first + cap]
+        bits = []
+        for _ in range(2):
+            out = torch.full((cap, n), POISON_BF16, dtype=torch.int16, device=dev())
+            moe.moe_grouped_gemm_mxfp4(up(av), up(asv), "mxfp4", dw[own], dws[own], up(c), up(o), cap,
+                                       max_rows_per_expert=bound, out=out)
+            bits.append(out)
+        assert torch.equal(*bits)
+        _check_gemm(bits[0], c, o, av, asv, w[own], ws[own], None, k)
 
 
 @pytest.mark.parametrize("rounding", ["divide", "reciprocal"])
