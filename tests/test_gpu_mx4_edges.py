@@ -8,6 +8,7 @@ import torch
 
 import block_fp8_mixture_amd as moe
 import oracle
+from block_fp8_mixture_amd import _binding
 from tests.gpu_helpers import POISON_BF16, POISON_U8, dev, down, say, up
 from tests.test_gpu_mx4 import (ACTS, TILED, _aligned, _bf16, _bf16_any, _check_gemm, _exact_layer, _gemm,
                                 _rng)
@@ -219,3 +220,58 @@ def test_combine_past_two_to_the_32_threads():
     for lo in range(0, tokens, 1 << 22):
         assert torch.equal(out[lo:min(lo + (1 << 22), tokens)], want[pair_to_row[lo:lo + (1 << 22)].long()]), lo
     assert out[tokens:].eq(POISON_BF16).all()
+
+
+def test_every_entry_point_is_given_the_current_stream(monkeypatch):
+    """The handle each call passes to the library, under a side stream and
+    outside it."""
+    handles = {}
+
+    class Library:
+        def __getattr__(self, name):
+            fn = getattr(real, name)
+
+            def call(*args):
+                handles[name] = args[-1]
+                return fn(*args)
+            return call
+
+    real = moe.load_library()
+    monkeypatch.setattr(_binding, "_lib", Library())
+    e, h, i, k, t = 3, 256, 128, 2, 5
+    x, _, _, w1, w2 = _exact_layer(250, t, e, h, i, k)
+    xs, weights = up(x), [up(v) for v in (*w1, *w2)]
+    logits = torch.randn((t, e), device=dev())
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def calls():
+        ids, tw = moe.moe_route(logits, k)
+        al = moe.moe_align(ids, e)
+        xq, sc = moe.moe_act_quant(xs, "mxfp4")
+        moe.moe_mxfp4_dequant(xq, sc)
+        rows = al["row_to_pair"].numel()
+        c1 = moe.moe_grouped_gemm_mxfp4(xq, sc, "mxfp4", *weights[:2], al["counts"], al["offsets"], rows,
+                                        a_row_map=al["row_to_pair"], a_row_div=k)
+        hq, hs = moe.moe_silu_mul_quant(c1, al["counts"], al["offsets"], fmt="mxfp4")
+        y = moe.moe_grouped_gemm_mxfp4(hq, hs, "mxfp4", *weights[2:], al["counts"], al["offsets"], rows)
+        out = moe.moe_topk_combine(y, al["pair_to_row"], tw)
+        full = moe.moe_forward(xs, ids, tw, *weights, "mxfp4", weight_fmt="mxfp4")[0]
+        moe.moe_forward_noalloc(xs, ids, tw, *weights, "mxfp4", weight_fmt="mxfp4")
+        al2 = moe.moe_align_batched(ids, e, t)
+        moe.moe_silu_mul_quant_masked(torch.zeros((e * t, 2 * i), dtype=torch.bfloat16, device=dev()), al2["masked_m"], t,
+                                      fmt="mxfp4")
+        return out, full
+
+    names = {"moe_route", "moe_align", "moe_align_batched", "moe_act_quant", "moe_mxfp4_dequant",
+             "moe_grouped_gemm_mxfp4", "moe_silu_mul_quant", "moe_silu_mul_quant_masked", "moe_topk_combine",
+             "moe_forward", "moe_forward_noalloc"}
+    with torch.cuda.stream(side):
+        a = calls()
+    side.synchronize()
+    assert {n: handles[n] for n in names} == dict.fromkeys(names, side.cuda_stream)
+    handles.clear()
+    b = calls()
+    torch.cuda.synchronize()
+    assert {n: handles[n] for n in names} == dict.fromkeys(names, torch.cuda.current_stream().cuda_stream)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))

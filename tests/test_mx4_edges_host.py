@@ -1,10 +1,13 @@
 """Host-only checks of the routing and 4-bit entry points at the edges of their
 arguments. Meta tensors have a shape and no memory; the GPU check comes last."""
 
+import types
+
 import pytest
 import torch
 
 import block_fp8_mixture_amd as moe
+from block_fp8_mixture_amd import _binding as B
 
 
 def _meta(shape, dtype):
@@ -31,3 +34,55 @@ def test_sizes_past_int32_are_refused():
                 moe.moe_route(l, 2, **{name: v})
     with pytest.raises(ValueError, match="GPU"):
         moe.moe_route(l, 2)
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_switch_to_the_tensors_device_and_take_its_stream(monkeypatch, current):
+    """With the tensors on device 1: entered if another device is current, for
+    the call alone, and the stream is device 1's."""
+    entered, state = [], {"current": current}
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            entered.append(self.device)
+            self.before, state["current"] = state["current"], self.device.index
+
+        def __exit__(self, *_):
+            state["current"] = self.before
+
+    seen = []
+    lib = types.SimpleNamespace(f=lambda *args: seen.append((args, state["current"])) or 0)
+    monkeypatch.setattr(B, "_lib", lib)
+    monkeypatch.setattr(B, "_current_device", lambda: state["current"])
+    monkeypatch.setattr(B, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    device = torch.device("cuda", 1)
+    B._enqueue("f", device, 7, 8)
+    assert seen == [((7, 8, 1001), 1)]
+    assert entered == ([] if current == 1 else [device]) and state["current"] == current
+
+
+def test_a_failed_call_leaves_the_current_device(monkeypatch):
+    """A refusal on another device raises and the device is as before."""
+    left = []
+
+    class Device:
+        def __init__(self, device):
+            pass
+
+        def __enter__(self):
+            pass
+
+        def __exit__(self, *_):
+            left.append(True)
+
+    monkeypatch.setattr(B, "_lib", types.SimpleNamespace(f=lambda *args: 1))
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    with pytest.raises(moe.MoeError, match="invalid argument"):
+        B._enqueue("f", torch.device("cuda", 1))
+    assert left == [True]
