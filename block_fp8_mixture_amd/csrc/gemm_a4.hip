@@ -145,9 +145,10 @@ __device__ __forceinline__ void a4_stream(const W4Args& p, A4Rows t, int g, int 
 // operands go from global memory straight into the MFMA registers. The S
 // waves of a K split add their partial sums in LDS in wave order, so the
 // result does not depend on which finishes first. Bound by the weights: 8
-// experts of 4 rows, N 4096, K 7168 (125 MB) 27.7 us, 4.5 TB/s. Many waves with
-// few registers (75) beat a pipeline of two chunks within a wave (182 registers,
-// 32.4 us), and whole lines in K order half lines (36.1 us).
+// experts of 4 rows, N 4096, K 7168 (125 MB) 37.8 us from HBM (3.3 TB/s), 28
+// to 29 where the last-level cache holds them from the call before (4.4 TB/s).
+// There many waves with few registers (75) beat a pipeline of two chunks within
+// a wave (182 registers, 32.4 us), and whole lines in K order half lines (36.1).
 __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
   __shared__ int s_pref[kMaxExperts + 1];
   __shared__ int s_wsum[kA4Waves];
@@ -280,8 +281,8 @@ __global__ __launch_bounds__(kA4Threads, 2) void gemm_a4_kernel(W4Args p) {
 //
 // Tiles of 64 rows take 128 columns, half the LDS, and two workgroups per CU:
 // twice the stages in flight, and twice the tiles for the CUs where experts are
-// few (64 x 256 tiles, one workgroup per CU, against them: 32 experts of 16 rows, K 7168,
-// N 4096 100 / 91 us, 256 experts of 2 rows, K 6144, N 512 89 / 79 us).
+// few (64 x 256 tiles, one workgroup per CU, against them, the same inputs each time: 32
+// experts of 16 rows, K 7168, N 4096 100 / 91 us, 256 experts of 2 rows, K 6144, N 512 89 / 79).
 //
 // Row tiles of an expert run fastest, so that neighbours share a weight slab.
 constexpr int kA4TThreads = 256;
@@ -729,13 +730,15 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream) {
   const int64_t cols = (g.n + kA4TileCols - 1) / kA4TileCols;
   double mean = static_cast<double>(rows) / live;
   if (mean > g.max_rows_per_expert) mean = g.max_rows_per_expert;
-  // Few weights: streamed, once per 32 rows, at 4.6 TB/s and 4 us around them;
-  // a round of tiles through LDS takes 1.3 us per 256 K values instead, whatever
-  // it holds. The two are equal, for any K, at some 165 pieces of 256 weight
-  // rows x 32 token rows. Streamed / tiled, us: N 4096, K 7168, experts x rows
-  // 2x4 11/33, 8x4 29/42, 12x4 40/43, 16x4 52/43, 8x32 45/43, 8x64 82/44, 4x100
-  // 82/41, 1x1000 157/65; N 7168, K 2048, 4x16 13/14, 8x16 22/15; N 1024, K 2048,
-  // 32x4 12/15, 64x4 19/16.
+  // Few weights: streamed, once per 32 rows, at 3.5 to 5 TB/s and some us around
+  // them; a round of tiles through LDS takes 1.3 us per 256 K values instead,
+  // whatever it holds. The two meet, for any K, at about 160 pieces of 256 weight
+  // rows x 32 token rows. Streamed / tiled, us, weights from HBM: N 4096, K 7168,
+  // experts x rows 1x1 11/20, 2x4 12/33, 8x4 38/38, 12x4 54/44, 16x4 72/49, 8x32
+  // 55/41, 8x64 94/47, 4x100 82/38, 1x1000 156/56; N 7168, K 2048 4x16 14/13, 8x16
+  // 23/16; N 1024, K 2048 32x4 13/13, 64x4 20/17; N 512, K 6144 32x2 16/30, 64x2
+  // 33/34, 128x2 61/45. Of these the rule loses 8x32, whose pieces hold two row
+  // tiles, and 1 us or less of the others.
   if (live * cols * static_cast<int64_t>(ceil(mean / kA4TileM)) * 8 < 5 * cus) {
     hipLaunchKernelGGL(gemm_a4_kernel, dim3(static_cast<unsigned>(4 * cus)), dim3(kA4Threads), 0, stream, g);
     return hipGetLastError();

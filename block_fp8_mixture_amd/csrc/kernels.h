@@ -137,13 +137,15 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream);
 // routed pairs, in two launches. hq [pairs, I/2] and hs [pairs, I/32] hold the
 // quantized FC2 input between them, a row per pair. Its two sides, us captured,
 // these launches against the general path's (experts, hidden, inter; pairs):
-//   288, 4096, 512:   8: 15 / 30, 32: 28 / 49, 40: 36 / 59, 48: 39 / 61
-//   32, 7168, 2048:   8: 46 / 62, 32: 113..122 / 118..130, 40: 140 / 138, 48: 151 / 141
-//   64, 2048, 1024:   6: 16 / 29, 24: 34 / 39, 36: 43 / 39, 48: 53 / 49
-//   16, 4096, 4096:   16: 69 / 88, 32: 93 / 94, 48: 103 / 97
-//   8, 4096, 14336:   8: 125 / 149, 32: 176 / 181, 48: 215 / 188
-//   128, 2048, 768:   32: 35 / 39, 48: 47 / 47
-// Over 48 the general path is ahead on average (64: 61 / 51, 127 / 103, 50 / 68).
+//   288, 4096, 512:   8: 15 / 31, 32: 28 / 49, 48: 39 / 61, 64: 49 / 66
+//   128, 2048, 768:   16: 23 / 32, 32: 34 / 39, 48: 46 / 46, 64: 57 / 54
+//   64, 2048, 1024:   6: 16 / 29, 24: 33 / 39, 36: 42 / 39, 48: 52 / 49, 60: 59 / 50
+//   32, 7168, 2048:   8: 47 / 62, 32: 130 / 132, 40: 140 / 135, 48: 151 / 140, 64: 168 / 150
+//   16, 4096, 4096:   16: 66 / 87, 32: 96 / 95, 48: 104 / 97, 64: 111 / 98
+//   8, 4096, 14336:   8: 114 / 142, 32: 175 / 180, 48: 214 / 187, 64: 239 / 191
+// The pairs alone decide. Where they meet differs: some 32 pairs with up to 64
+// experts, past 64 with 288. At 48 the two launches lose up to 13 % with few
+// experts and win a third with many; at 64 they lose 6 to 20 % on five of six.
 constexpr int kL4MaxPairs = 48;
 static_assert(kL4MaxPairs <= 64);  // a pair per lane
 constexpr size_t kLdsBytes = 160 * 1024;  // of a workgroup

@@ -12,8 +12,9 @@
 // byte 255, the format's NaN, and zero codes: E2M1 has neither, and the byte
 // makes every value of the block NaN wherever it is read. Elements round to
 // nearest, ties to the even code (v_cvt_scalef32_pk_fp4_*, checked against
-// the grid for scale bytes 0..254, also at the ties; half a step is 1/8 of a
-// value at most within a binade).
+// the grid for scale bytes 0..254, also at the ties): with one mantissa bit a
+// value in [1, 6] times the scale is off by a fifth of itself at most (2.5
+// becomes 2, 5 becomes 4), a saturated one by less than a quarter.
 #pragma once
 
 #include "device_common.h"

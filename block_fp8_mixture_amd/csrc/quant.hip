@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kSmqThreads) void silu_mul_quant_kernel(
 
 // The BF16 values of an MXFP4 tensor: 16 columns per thread, an 8-byte load of
 // codes and a 32-byte store. Every value of the format with a scale byte up to
-// 251 is a BF16 value (2 significant bits; 0.5 x 2^-127 is a BF16 subnormal);
+// 252 (the quantizer's largest but the NaN's) is a BF16 value (2 significant bits; 0.5 x 2^-127 is a BF16 subnormal);
 // what lies past BF16's largest becomes infinity.
 __global__ __launch_bounds__(kThreads) void mxfp4_dequant_kernel(const uint8_t* __restrict__ codes,
                                                                  const uint8_t* __restrict__ scales,

@@ -268,7 +268,8 @@ moe_status moe_act_quant(const uint16_t* x, int32_t t_cap, const int32_t* t_live
 
 /* The BF16 values of an MXFP4 tensor (activations or weights): out[r, c] =
  * e2m1(code of column c of row r) * 2^(scales[r, c/32] - 127), NaN under scale
- * byte 255. Exact up to scale byte 251; beyond BF16's range, infinity.
+ * byte 255. Exact up to scale byte 252, the largest that a quantization gives
+ * a finite block; beyond BF16's range, infinity.
  *   codes   device uint8 [rows, cols/2], 8-byte aligned
  *   scales  device uint8 [rows, cols/32]
  *   out     device BF16 [rows, cols], 16-byte aligned
@@ -355,8 +356,9 @@ moe_status moe_grouped_gemm_fp8_masked(const uint8_t* a, const void* a_scales, m
  *   c          device BF16 [row_cap, n]; only live rows written
  * Errors: INVALID_ARG (n or k not positive multiples of 128, null pointers,
  * a_row_div < 1, unknown fmt, a_rows < 1 with rows to compute, a batched
- * row_cap other than num_experts*expert_cap, max_rows_per_expert < 0); UNSUPPORTED (num_experts above
- * 1024, a_rows * k or n * k at or above 2^32). */
+ * row_cap other than num_experts*expert_cap, max_rows_per_expert < 0, with
+ * MXFP4 activations a misaligned pointer); UNSUPPORTED (num_experts above
+ * 1024, k above 32768, a_rows * k or n * k at or above 2^32). */
 moe_status moe_grouped_gemm_mxfp4(const uint8_t* a, const void* a_scales, moe_scale_fmt fmt,
                                   int32_t a_rows, const int32_t* a_row_map, int32_t a_row_div,
                                   const uint8_t* w, const uint8_t* w_scales,

@@ -275,3 +275,41 @@ def test_every_entry_point_is_given_the_current_stream(monkeypatch):
     torch.cuda.synchronize()
     assert {n: handles[n] for n in names} == dict.fromkeys(names, torch.cuda.current_stream().cuda_stream)
     assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("t,h", [(16, 15360), (48, 128)])
+def test_few_token_layer_captured_at_its_limits(t, h):
+    """The most tokens, and the most LDS a workgroup of theirs takes (128 KB of
+    codes): every replay as the eager call, with other work between."""
+    say(f"mx4 layer of {t} x {h}, captured")
+    x, ids, w, w1, w2 = _exact_layer(260 + t, t, 5, h, 128, 1)
+    args = [up(v) for v in (ids, w, *w1, *w2)]
+    xs, out = up(x), torch.empty((t, h), dtype=torch.int16, device=dev())
+    ws = torch.empty(moe.moe_workspace_bytes(5, h, 128, 1, t, fmt="mxfp4", weight_fmt="mxfp4"), dtype=torch.uint8,
+                     device=dev())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        moe.moe_forward(xs, *args, "mxfp4", weight_fmt="mxfp4", out=out, workspace=ws)
+    side.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        moe.moe_forward(xs, *args, "mxfp4", weight_fmt="mxfp4", out=out, workspace=ws)
+    for trial in range(3):
+        xs.copy_(up(x).roll(trial, 0))
+        out.fill_(POISON_BF16)
+        graph.replay()
+        eager = moe.moe_forward(up(x).roll(trial, 0), *args, "mxfp4", weight_fmt="mxfp4")[0]
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), trial
+
+
+@pytest.mark.parametrize("counts,n,k", [([3, 40], 128, 32640), ([300], 128, 32768), ([1], 1 << 20, 128),
+                                        ([70], 1 << 18, 256)])
+def test_product_of_the_longest_rows_and_the_most_columns(counts, n, k):
+    """K up to 32768, past which a call is refused, and N far past K."""
+    say(f"mx4 gemm {counts} n={n} k={k}")
+    counts, offsets, row_cap, a, asc, w, ws, _ = _gemm(counts, n, k, 16, False, 270)
+    out = torch.full((row_cap, n), POISON_BF16, dtype=torch.int16, device=dev())
+    moe.moe_grouped_gemm_mxfp4(up(a), up(asc), "mxfp4", up(w), up(ws), up(counts), up(offsets), row_cap, out=out)
+    _check_gemm(out, counts, offsets, a, asc, w, ws, None, k)

@@ -86,3 +86,10 @@ def test_a_failed_call_leaves_the_current_device(monkeypatch):
     with pytest.raises(moe.MoeError, match="invalid argument"):
         B._enqueue("f", torch.device("cuda", 1))
     assert left == [True]
+
+
+def test_product_of_rows_past_32768_is_refused():
+    lib, fake = moe.load_library(), 0x1000  # never dereferenced: the refusal comes first
+    for k, status in ((32768, 0), (32896, 2)):
+        assert lib.moe_grouped_gemm_mxfp4(fake, fake, 4, 64, None, 1, fake, fake, fake, fake, 0, 4, 0, 0, 128, k, fake,
+                                          None) == status
