@@ -144,8 +144,8 @@ hipError_t launch_grouped_gemm_a4(const W4Args& g, hipStream_t stream);
 //   16, 4096, 4096:   16: 66 / 87, 32: 96 / 95, 48: 104 / 97, 64: 111 / 98
 //   8, 4096, 14336:   8: 114 / 142, 32: 175 / 180, 48: 214 / 187, 64: 239 / 191
 // The pairs alone decide. Where they meet differs: some 32 pairs with up to 64
-// experts, past 64 with 288. At 48 the two launches lose up to 13 % with few
-// experts and win a third with many; at 64 they lose 6 to 20 % on five of six.
+// experts, past 64 with 288. At 48 the two launches lose up to 15 % with few
+// experts and win a third with many; at 64 they lose 6 to 25 % on five of six.
 constexpr int kL4MaxPairs = 48;
 static_assert(kL4MaxPairs <= 64);  // a pair per lane
 constexpr size_t kLdsBytes = 160 * 1024;  // of a workgroup
