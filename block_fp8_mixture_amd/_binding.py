@@ -11,6 +11,9 @@ _LIB_NAME = "libmoefp8.so"
 
 SCALE_FMTS = {"fp32": 0, "pow2": 1, "ue8m0": 2, "mxfp4": 4}
 ROUNDINGS = {"divide": 0, "reciprocal": 1}
+# Types of norm weights and of 4-bit weights before their quantization, and of their scales.
+ELEM_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+INT4_GROUPS = (32, 64, 128)
 ACTS = {"swiglu": 0, "swiglu_clamp": 1, "swiglu_clamp_after_silu": 2}
 WEIGHT_FMTS = {"e4m3": 0, "mxfp4": 1}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -74,6 +77,11 @@ class _Router(ctypes.Structure):
                 ("scale", _f32), ("num_groups", _i32), ("top_groups", _i32), ("group_top", _i32)]
 
 
+class _Int4Weights(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("zeros", _vp), ("scale_type", ctypes.c_int),
+                ("group", _i32), ("num_experts", _i32), ("n", _i32), ("k", _i32)]
+
+
 class _Layout(ctypes.Structure):
     _fields_ = [("expert_counts", ctypes.c_size_t), ("expert_offsets", ctypes.c_size_t),
                 ("row_to_pair", ctypes.c_size_t), ("pair_to_row", ctypes.c_size_t),
@@ -89,6 +97,15 @@ _SIGNATURES = {
     "moe_route": (ctypes.c_int, [ctypes.POINTER(_Router), _vp, ctypes.c_int, ctypes.c_int64, _vp, _i32,
                                  _vp, _vp, _vp, _vp]),
     "moe_mxfp4_dequant": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, _i32, _vp, _vp]),
+    "moe_rmsnorm_quant": (ctypes.c_int, [_vp, ctypes.c_int64, _vp, _vp, ctypes.c_int, ctypes.c_double, _i32,
+                                         _vp, _i32, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp]),
+    "moe_int4_quant": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int64, _i32, _i32, ctypes.c_int, _vp, _vp,
+                                      _vp, _vp]),
+    "moe_int4_dequant": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, ctypes.c_int64, _i32, _i32, _vp, _vp]),
+    "moe_gemm_int4": (ctypes.c_int, [_vp, _i32, _vp, ctypes.POINTER(_Int4Weights), ctypes.c_int, _f32, _vp,
+                                     _vp]),
+    "moe_grouped_gemm_int4": (ctypes.c_int, [_vp, _i32, _vp, _i32, ctypes.POINTER(_Int4Weights), _vp, _vp,
+                                             _i32, _i32, _i32, ctypes.c_int, _f32, _vp, _vp]),
     "moe_align": (ctypes.c_int, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                  _vp]),
     "moe_align_batched": (ctypes.c_int, [_vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
@@ -326,6 +343,244 @@ def moe_mxfp4_dequant(codes, scales, out=None):
     dev = _same_device(codes, scales, ob)
     _enqueue("moe_mxfp4_dequant", dev, _ptr(codes), _ptr(scales), codes.numel() * 2 // cols, cols,
              _ptr(ob))
+    return out
+
+
+def moe_rmsnorm_quant(x, weight, eps=1e-6, fmt="fp32", residual=None, t_live=None, residual_out=None,
+                      y=None, xq=None, xs=None, rounding="divide"):
+    """RMS norm of x [t_cap, H] BF16 (columns contiguous, rows a multiple of 8
+    elements apart) with the residual's addition and the quantization of its
+    output. Returns (y BF16 [t_cap, H], xq, xs, residual_out): xq and xs as
+    moe_act_quant(y, fmt) (None with ``fmt=None``), residual_out BF16 x + residual
+    (None without a residual). ``y=False``: no BF16 output (None). residual_out
+    may be ``residual`` itself."""
+    lib = load_library()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    if x.dtype not in (torch.bfloat16, torch.int16):
+        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError("x must be [t_cap, hidden]")
+    t_cap, hidden = x.shape
+    if (t_cap | hidden) >> 31:
+        raise ValueError(_PAST_INT32)
+    ld = x.stride(0) if t_cap > 1 else hidden
+    if (hidden > 1 and x.stride(1) != 1) or ld < hidden:
+        raise ValueError("the columns of x must be contiguous and its rows apart")
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("weight must be a float32 or bfloat16 tensor")
+    _exact(weight, "weight", weight.dtype, (hidden,))
+    eps = float(eps)
+    if not 0.0 <= eps < float("inf"):
+        raise ValueError("eps must be finite and not negative")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if residual is not None:
+        _shape(_bf16(residual, "residual"), "residual", (t_cap, hidden))
+        if residual_out is None:
+            residual_out = torch.empty((t_cap, hidden), dtype=torch.bfloat16, device=x.device)
+        _shape(_bf16(residual_out, "residual_out"), "residual_out", (t_cap, hidden))
+    if y is None:
+        y = torch.empty((t_cap, hidden), dtype=torch.bfloat16, device=x.device)
+    elif y is False:
+        y = None
+    if y is not None:
+        _shape(_bf16(y, "y"), "y", (t_cap, hidden))
+    if fmt is None:
+        if xq is not None or xs is not None:
+            raise ValueError("xq and xs need a fmt")
+        if y is None:
+            raise ValueError("without y there must be a fmt")
+    else:
+        _fmt(fmt)
+        if xq is None:
+            xq = torch.empty((t_cap, _code_cols(hidden, fmt)), dtype=torch.uint8, device=x.device)
+        if xs is None:
+            xs = torch.empty(_scale_shape(t_cap, hidden, fmt), dtype=_scale_dtype(fmt), device=x.device)
+        _exact(xq, "xq", torch.uint8, (t_cap, _code_cols(hidden, fmt)))
+        _exact(xs, "xs", _scale_dtype(fmt), _scale_shape(t_cap, hidden, fmt))
+    dev = _same_device(x, weight, residual, residual_out, y, xq, xs, t_live)
+    _enqueue("moe_rmsnorm_quant", dev, _ptr(x), ld, _ptr(residual), _ptr(weight), ELEM_TYPES[weight.dtype],
+             eps, t_cap, _live(t_live), hidden, _fmt(fmt or "fp32"), _rounding(rounding),
+             _ptr(residual_out), _ptr(y), _ptr(xq), _ptr(xs))
+    return y, xq, xs, residual_out
+
+
+def _int4_group(cols, groups, name):
+    """Columns per group of ``groups`` scales in a row of ``cols`` columns."""
+    group = cols // groups if groups else 0
+    if group not in INT4_GROUPS or group * groups != cols:
+        raise ValueError(f"{name} must have a scale per 32, 64 or 128 columns ({cols} columns, {groups} scales)")
+    return group
+
+
+def _int4_scale_type(scales, name):
+    if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
+    return ELEM_TYPES[scales.dtype]
+
+
+def moe_int4_quant(w, group=128, symmetric=True, scale_dtype=torch.bfloat16, codes=None, scales=None,
+                   zeros=None):
+    """4-bit integer weights of w [..., K] (float32, bfloat16 or float16), a scale
+    (bfloat16 or float16) per ``group`` (32, 64 or 128) columns and, if not
+    ``symmetric``, a zero point. Returns (codes uint8 [..., K/2], scales [...,
+    K/group], zeros uint8 [..., K/group] or None)."""
+    lib = load_library()
+    if not isinstance(w, torch.Tensor) or w.dtype not in ELEM_TYPES:
+        raise TypeError(f"w must be a tensor of one of {list(ELEM_TYPES)}")
+    _need(w, "w", w.dtype)
+    if group not in INT4_GROUPS:
+        raise ValueError(f"group must be one of {INT4_GROUPS}")
+    if w.dim() < 1 or w.shape[-1] < group or w.shape[-1] % group:
+        raise ValueError("w must be [..., K] with K a multiple of the group")
+    lead, cols = tuple(w.shape[:-1]), w.shape[-1]
+    if cols >> 31:
+        raise ValueError(_PAST_INT32)
+    if codes is None:
+        codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device)
+    if scales is None:
+        scales = torch.empty(lead + (cols // group,), dtype=scale_dtype, device=w.device)
+    if symmetric and zeros is not None:
+        raise ValueError("symmetric weights have no zero points")
+    if not symmetric and zeros is None:
+        zeros = torch.empty(lead + (cols // group,), dtype=torch.uint8, device=w.device)
+    _exact(codes, "codes", torch.uint8, lead + (cols // 2,))
+    scale_type = _int4_scale_type(scales, "scales")
+    _exact(scales, "scales", scales.dtype, lead + (cols // group,))
+    if zeros is not None:
+        _exact(zeros, "zeros", torch.uint8, lead + (cols // group,))
+    dev = _same_device(w, codes, scales, zeros)
+    _enqueue("moe_int4_quant", dev, _ptr(w), ELEM_TYPES[w.dtype], w.numel() // cols, cols, int(group),
+             scale_type, _ptr(codes), _ptr(scales), _ptr(zeros))
+    return codes, scales, zeros
+
+
+def moe_int4_dequant(codes, scales, zeros=None, out=None):
+    """BF16 values of 4-bit integer weights: codes uint8 [..., K/2], scales
+    (bfloat16 or float16) and zeros (uint8 or None: 8) [..., K/group]. Returns
+    BF16 [..., K] (or ``out``)."""
+    lib = load_library()
+    shape = tuple(_need(codes, "codes", torch.uint8).shape)
+    scale_type = _int4_scale_type(scales, "scales")
+    if not shape or scales.dim() != len(shape):
+        raise ValueError("codes must be [..., K / 2] and scales [..., K / group]")
+    lead, cols = shape[:-1], 2 * shape[-1]
+    if cols >> 31:
+        raise ValueError(_PAST_INT32)
+    group = _int4_group(cols, scales.shape[-1], "codes")
+    _exact(scales, "scales", scales.dtype, lead + (cols // group,))
+    if zeros is not None:
+        _exact(zeros, "zeros", torch.uint8, lead + (cols // group,))
+    if out is None:
+        out = torch.empty(lead + (cols,), dtype=torch.bfloat16, device=codes.device)
+    ob = _shape(_bf16(out, "out"), "out", lead + (cols,))
+    dev = _same_device(codes, scales, zeros, ob)
+    _enqueue("moe_int4_dequant", dev, _ptr(codes), _ptr(scales), scale_type, _ptr(zeros),
+             codes.numel() * 2 // cols, cols, group, _ptr(ob))
+    return out
+
+
+def _int4_weights(w, scales, zeros, num_experts, n):
+    """The C structure of checked weights whose leading shape is ``w.shape[:-1]``."""
+    k = 2 * w.shape[-1]
+    scale_type = _int4_scale_type(scales, "w_scales")
+    if scales.dim() != w.dim():
+        raise ValueError("w_scales must be [..., N, K / group]")
+    group = _int4_group(k, scales.shape[-1], "w")
+    _exact(scales, "w_scales", scales.dtype, tuple(w.shape[:-1]) + (k // group,))
+    if zeros is not None:
+        _exact(zeros, "w_zeros", torch.uint8, tuple(w.shape[:-1]) + (k // group,))
+    if (n | k) >> 31:
+        raise ValueError(_PAST_INT32)
+    return _Int4Weights(_ptr(w), _ptr(scales), _ptr(zeros), scale_type, group, num_experts, n, k)
+
+
+def _gate(act, n):
+    """(value of moe_act, columns of the output)."""
+    if act is None:
+        return -1, n
+    if act not in ACTS:
+        raise ValueError(f"act must be None or one of {list(ACTS)}")
+    if n % 2:
+        raise ValueError("a gated product needs an even N")
+    return ACTS[act], n // 2
+
+
+def moe_gemm_int4(x, w, w_scales, w_zeros=None, act=None, clamp_limit=float("inf"), t_live=None, out=None):
+    """Product of BF16 rows x [T, K] with 4-bit integer weights: w uint8 [N, K/2],
+    w_scales (bfloat16 or float16) and w_zeros (uint8 or None) [N, K/group], from
+    a single row (a matrix-vector product) to many. With ``act`` rows [0, N/2) of
+    w are gates and [N/2, N) ups, and the result is the activation's. Returns BF16
+    [T, N] (gated [T, N/2]), rows past ``t_live`` untouched."""
+    lib = load_library()
+    xb = _bf16(x, "x")
+    if xb.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    _need(w, "w", torch.uint8, ndim=2)
+    rows, k = xb.shape
+    n = w.shape[0]
+    if 2 * w.shape[1] != k:
+        raise ValueError("x and w disagree on K")
+    if rows >> 31:
+        raise ValueError(_PAST_INT32)
+    weights = _int4_weights(w, w_scales, w_zeros, 1, n)
+    act_value, out_n = _gate(act, n)
+    if out is None:
+        out = torch.empty((rows, out_n), dtype=torch.bfloat16, device=xb.device)
+    ob = _shape(_bf16(out, "out"), "out", (rows, out_n))
+    if t_live is not None:
+        _exact(t_live, "t_live", torch.int32, (1,))
+    dev = _same_device(xb, w, w_scales, w_zeros, ob, t_live)
+    _enqueue("moe_gemm_int4", dev, _ptr(xb), rows, _live(t_live), ctypes.byref(weights), act_value,
+             float(clamp_limit), _ptr(ob))
+    return out
+
+
+def moe_grouped_gemm_int4(a, w, w_scales, counts, offsets=None, row_cap=None, w_zeros=None, a_row_map=None,
+                          a_row_div=1, expert_cap=0, max_rows_per_expert=0, act=None,
+                          clamp_limit=float("inf"), out=None):
+    """Product of BF16 rows with every expert's 4-bit integer weights over its
+    live rows: a [a_rows, K], w uint8 [E, N, K/2], w_scales and w_zeros [E, N,
+    K/group], counts, offsets and row_cap as moe_align makes them (with
+    ``expert_cap`` > 0 the batched layout: counts = masked_m, no offsets).
+    Gated as moe_gemm_int4. Returns BF16 [row_cap, N] (gated [row_cap, N/2]),
+    rows that are not live untouched."""
+    lib = load_library()
+    ab = _bf16(a, "a")
+    if ab.dim() != 2:
+        raise ValueError("a must be [a_rows, K]")
+    _need(w, "w", torch.uint8, ndim=3)
+    num_experts, n, k2 = w.shape
+    a_rows = ab.shape[0]
+    if ab.shape[1] != 2 * k2:
+        raise ValueError("a and w disagree on K")
+    weights = _int4_weights(w, w_scales, w_zeros, num_experts, n)
+    act_value, out_n = _gate(act, n)
+    _exact(counts, "counts", torch.int32, (num_experts,))
+    expert_cap, a_row_div, max_rows = int(expert_cap), int(a_row_div), int(max_rows_per_expert)
+    if expert_cap > 0:
+        row_cap = num_experts * expert_cap if row_cap is None else row_cap
+        offsets = None
+    else:
+        if offsets is None or row_cap is None:
+            raise ValueError("the aligned layout needs offsets and row_cap")
+        _exact(offsets, "offsets", torch.int32, (num_experts + 1,))
+    if (a_rows | row_cap | expert_cap | a_row_div | max_rows) >> 31 not in (0, -1):
+        raise ValueError(_PAST_INT32)
+    if out is None:
+        out = torch.empty((max(row_cap, 1), out_n), dtype=torch.bfloat16, device=ab.device)
+    ob = _bf16(out, "out")
+    if ob.dim() != 2 or ob.shape[1] != out_n or ob.shape[0] < row_cap:
+        raise ValueError(f"out must be [>= {row_cap}, {out_n}], got {tuple(ob.shape)}")
+    if a_row_map is not None:
+        _min_numel(_need(a_row_map, "a_row_map", torch.int32), "a_row_map", row_cap)
+    elif a_rows < row_cap:
+        raise ValueError("without a row map, a needs row_cap rows")
+    dev = _same_device(ab, w, w_scales, w_zeros, counts, offsets, ob, a_row_map)
+    _enqueue("moe_grouped_gemm_int4", dev, _ptr(ab), a_rows, _ptr(a_row_map), a_row_div,
+             ctypes.byref(weights), _ptr(counts), _ptr(offsets), expert_cap, row_cap, max_rows, act_value,
+             float(clamp_limit), _ptr(ob))
     return out
 
 

@@ -94,6 +94,12 @@ int64_t min_row_cap64(int64_t t_cap, int64_t topk, int64_t num_experts, int64_t 
   return (pairs + used * (align_rows - 1)) / align_rows * align_rows;
 }
 
+// Whether [a, a + an) and [b, b + bn) share a byte (a null pointer has none).
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && an && bn && x < y + bn && y < x + an;
+}
+
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
@@ -212,6 +218,170 @@ moe_status moe_act_quant(const uint16_t* x, int32_t t_cap, const int32_t* t_live
   if (t_cap == 0) return MOE_OK;
   return from_hip(moe::launch_act_quant(x, t_cap, t_live_dev, hidden, fmt, rounding, xq, xs,
                                         as_stream(stream)));
+}
+
+moe_status moe_rmsnorm_quant(const uint16_t* x, int64_t ld, const uint16_t* residual,
+                             const void* weight, moe_elem_type weight_type, double eps, int32_t t_cap,
+                             const int32_t* t_live_dev, int32_t hidden, moe_scale_fmt fmt,
+                             moe_rounding rounding, uint16_t* residual_out, uint16_t* y, uint8_t* xq,
+                             void* xs, void* stream) {
+  if (t_cap < 0 || !dim128(hidden) || !fmt_ok(fmt) || !rounding_ok(rounding) || ld < hidden || ld % 8 != 0 ||
+      (weight_type != MOE_ELEM_FP32 && weight_type != MOE_ELEM_BF16) || !(eps >= 0.0 && eps - eps == 0.0))
+    return MOE_ERR_INVALID_ARG;
+  if (hidden > moe::kMaxNormHidden) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(t_cap) * (hidden / 128) > INT32_MAX ||
+      ld > INT64_MAX / 8 / (t_cap > 0 ? t_cap : 1))
+    return MOE_ERR_INVALID_ARG;
+  if (!residual != !residual_out || !xq != !xs || (!y && !xq && t_cap > 0)) return MOE_ERR_INVALID_ARG;
+  if (t_cap == 0) return MOE_OK;
+  const bool mx = fmt == MOE_SCALE_MXFP4;
+  if (!x || !weight || !aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(residual_out, 16) || !aligned(y, 16) || !aligned(xq, mx ? 4 : 8) ||
+      !aligned(xs, fmt == MOE_SCALE_FP32 || fmt == MOE_SCALE_FP32_POW2 ? 4 : 1))
+    return MOE_ERR_INVALID_ARG;
+  // A thread reads its columns of a row before it writes them: an output may
+  // stand in an input's place, but not beside it.
+  const size_t n = static_cast<size_t>(t_cap) * hidden, bytes = 2 * n;
+  const size_t x_bytes = 2 * (static_cast<size_t>(t_cap - 1) * ld + hidden);
+  const size_t q_bytes = code_bytes(fmt, n), s_bytes = n / 128 * scale_bytes(fmt);
+  const size_t w_bytes = static_cast<size_t>(hidden) * (weight_type == MOE_ELEM_FP32 ? 4 : 2);
+  for (const void* o : {static_cast<const void*>(residual_out), static_cast<const void*>(y)}) {
+    if ((overlap(o, bytes, x, x_bytes) && !(o == x && ld == hidden)) ||
+        (overlap(o, bytes, residual, bytes) && o != residual) || overlap(o, bytes, weight, w_bytes) ||
+        overlap(o, bytes, xq, q_bytes) || overlap(o, bytes, xs, s_bytes) ||
+        overlap(o, bytes, t_live_dev, sizeof(int32_t)))
+      return MOE_ERR_INVALID_ARG;
+  }
+  if (overlap(residual_out, bytes, y, bytes) || overlap(xq, q_bytes, xs, s_bytes)) return MOE_ERR_INVALID_ARG;
+  const struct { const void* p; size_t n; } quant[] = {{xq, q_bytes}, {xs, s_bytes}};
+  for (const auto& q : quant)
+    if (overlap(q.p, q.n, x, x_bytes) || overlap(q.p, q.n, residual, bytes) ||
+        overlap(q.p, q.n, weight, w_bytes) || overlap(q.p, q.n, t_live_dev, sizeof(int32_t)))
+      return MOE_ERR_INVALID_ARG;
+  moe::NormArgs a;
+  a.x = x;
+  a.ld = ld;
+  a.residual = residual;
+  a.weight = weight;
+  a.weight_f32 = weight_type == MOE_ELEM_FP32;
+  a.eps = eps;
+  a.t_cap = t_cap;
+  a.t_live_dev = t_live_dev;
+  a.hidden = hidden;
+  a.fmt = fmt;
+  a.rounding = rounding;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.xq = xq;
+  a.xs = xs;
+  return from_hip(moe::launch_rmsnorm(a, as_stream(stream)));
+}
+
+// The layout of 4-bit integer weights: a group of the three, whole groups.
+static bool int4_layout_ok(int32_t cols, int32_t group, int scale_type) {
+  return (group == 32 || group == 64 || group == 128) && cols > 0 && cols % group == 0 &&
+         (scale_type == MOE_ELEM_BF16 || scale_type == MOE_ELEM_FP16);
+}
+
+moe_status moe_int4_quant(const void* w, moe_elem_type type, int64_t rows, int32_t cols, int32_t group,
+                          moe_elem_type scale_type, uint8_t* codes, uint16_t* scales, uint8_t* zeros,
+                          void* stream) {
+  if ((type != MOE_ELEM_FP32 && type != MOE_ELEM_BF16 && type != MOE_ELEM_FP16) || rows < 0 ||
+      !int4_layout_ok(cols, group, scale_type) || rows > INT64_MAX / 8 / cols)
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!w || !codes || !scales || !aligned(w, 16) || !aligned(codes, 4) || !aligned(scales, 2))
+    return MOE_ERR_INVALID_ARG;
+  moe::Int4QuantArgs a;
+  a.w = w;
+  a.type = type;
+  a.rows = rows;
+  a.cols = cols;
+  a.group = group;
+  a.scale_f16 = scale_type == MOE_ELEM_FP16;
+  a.codes = codes;
+  a.scales = scales;
+  a.zeros = zeros;
+  return from_hip(moe::launch_int4_quant(a, as_stream(stream)));
+}
+
+moe_status moe_int4_dequant(const uint8_t* codes, const uint16_t* scales, moe_elem_type scale_type,
+                            const uint8_t* zeros, int64_t rows, int32_t cols, int32_t group,
+                            uint16_t* out, void* stream) {
+  if (rows < 0 || !int4_layout_ok(cols, group, scale_type) || rows > INT64_MAX / 8 / cols)
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned(codes, 8) || !aligned(scales, 2) || !aligned(out, 16))
+    return MOE_ERR_INVALID_ARG;
+  return from_hip(moe::launch_int4_dequant(codes, scales, scale_type == MOE_ELEM_FP16, zeros, rows, cols,
+                                           group, out, as_stream(stream)));
+}
+
+static moe_status gemm_int4_checked(moe::Int4GemmArgs* g, const moe_int4_weights* w, moe_act act,
+                                    float clamp_limit, void* stream) {
+  if (!w || w->num_experts < 1 || w->n < 1 || !int4_layout_ok(w->k, w->group, w->scale_type) ||
+      (act != MOE_ACT_NONE && (!act_ok(act) || w->n % 2 != 0)) ||
+      ((act == MOE_ACT_SWIGLU_CLAMP || act == MOE_ACT_SWIGLU_CLAMP_AFTER_SILU) && !(clamp_limit > 0.0f)))
+    return MOE_ERR_INVALID_ARG;
+  if (w->num_experts > moe::kMaxExperts || w->k > moe::kMaxInt4K ||
+      static_cast<int64_t>(w->n) * w->k >= (int64_t{1} << 32))
+    return MOE_ERR_UNSUPPORTED;
+  if (g->row_cap == 0) return MOE_OK;
+  if (!g->a || g->a_rows < 1 || !g->c || !w->codes || !w->scales || !aligned(g->a, 16) ||
+      !aligned(w->codes, 16) || !aligned(w->scales, 2) || !aligned(g->c, 2))
+    return MOE_ERR_INVALID_ARG;
+  g->w = w->codes;
+  g->scales = w->scales;
+  g->zeros = w->zeros;
+  g->scale_f16 = w->scale_type == MOE_ELEM_FP16;
+  g->group = w->group;
+  g->num_experts = w->num_experts;
+  g->n = w->n;
+  g->k = w->k;
+  g->act = act;
+  g->limit = clamp_limit;
+  return from_hip(moe::launch_gemm_int4(*g, as_stream(stream)));
+}
+
+moe_status moe_gemm_int4(const uint16_t* a, int32_t rows, const int32_t* t_live_dev,
+                         const moe_int4_weights* w, moe_act act, float clamp_limit, uint16_t* c,
+                         void* stream) {
+  if (rows < 0 || rows > INT32_MAX / 2 || !w || w->num_experts != 1) return MOE_ERR_INVALID_ARG;
+  moe::Int4GemmArgs g{};
+  g.a = a;
+  g.a_rows = rows;
+  g.a_row_div = 1;
+  g.counts = t_live_dev;  // a masked batch of one expert
+  g.seg_cap = rows;
+  g.row_cap = rows;
+  g.max_rows_per_expert = rows;
+  g.c = c;
+  return gemm_int4_checked(&g, w, act, clamp_limit, stream);
+}
+
+moe_status moe_grouped_gemm_int4(const uint16_t* a, int32_t a_rows, const int32_t* a_row_map,
+                                 int32_t a_row_div, const moe_int4_weights* w,
+                                 const int32_t* expert_counts, const int32_t* expert_offsets,
+                                 int32_t expert_cap, int32_t row_cap, int32_t max_rows_per_expert,
+                                 moe_act act, float clamp_limit, uint16_t* c, void* stream) {
+  if (!w || a_rows < 0 || a_row_div < 1 || row_cap < 0 || row_cap > INT32_MAX / 2 || expert_cap < 0 ||
+      max_rows_per_expert < 0 || !expert_counts || (!expert_offsets && expert_cap == 0))
+    return MOE_ERR_INVALID_ARG;
+  if (expert_cap > 0 && static_cast<int64_t>(expert_cap) * w->num_experts != row_cap)
+    return MOE_ERR_INVALID_ARG;
+  moe::Int4GemmArgs g{};
+  g.a = a;
+  g.a_rows = a_rows;
+  g.a_row_map = a_row_map;
+  g.a_row_div = a_row_div;
+  g.counts = expert_counts;
+  g.offsets = expert_offsets;
+  g.seg_cap = expert_cap;
+  g.row_cap = row_cap;
+  const int32_t seg = expert_cap > 0 ? expert_cap : row_cap;
+  g.max_rows_per_expert = (max_rows_per_expert == 0 || max_rows_per_expert > seg) ? seg : max_rows_per_expert;
+  g.c = c;
+  return gemm_int4_checked(&g, w, act, clamp_limit, stream);
 }
 
 static moe_status gemm_checked(const moe::GemmArgs& g, void* stream) {

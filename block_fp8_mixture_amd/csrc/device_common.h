@@ -131,6 +131,16 @@ __device__ __forceinline__ uint32_t cvt_pk_e4m3(float a, float b) {
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xFFFFu;
 }
 
+// The same, a NaN to E4M3's NaN (0x7F with x's sign).
+__device__ __forceinline__ uint32_t cvt_e4m3_nan_bits(float x) {
+  return x != x ? (__float_as_uint(x) >> 24 & 0x80u) | 0x7Fu : 0u;
+}
+__device__ __forceinline__ uint32_t cvt_pk_e4m3_nan(float a, float b) {
+  const uint32_t na = cvt_e4m3_nan_bits(a), nb = cvt_e4m3_nan_bits(b);
+  const uint32_t v = cvt_pk_e4m3(a, b);
+  return (na ? na : v & 0xFFu) | (nb ? nb : v >> 8) << 8;
+}
+
 // ---- wave helpers ------------------------------------------------------------
 
 // Max over aligned groups of `width` lanes (16, 32 or 64). Inside a 16-lane

@@ -1,0 +1,78 @@
+// Device helpers of 4-bit integer weights w = s (q - z) as BF16 matrix
+// operands.
+//
+// A code q becomes the BF16 value 16 + q by putting its four bits at the top
+// of a mantissa of exponent 4 (0x4180 | q << 3): one shift and one and-or for two
+// codes, exact. A group's sum then is s (sum a (16 + q) - (16 + z) sum a), with
+// sum a from the matrix cores too (an operand of ones); 16 rather than a larger
+// offset keeps the part that cancels within a few times the part that stays.
+#pragma once
+
+#include "device_common.h"
+#include "gemm_device.h"
+#include "kernels.h"
+
+namespace moe {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ v4f mfma_bf16(uint4 a, uint4 b, v4f acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                 acc, 0, 0, 0);
+}
+
+// Eight codes (one word) as 16 + q, in the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 int4_operand(uint32_t c) {
+  constexpr uint32_t kMask = 0x00780078u, kOne = 0x41804180u;
+  return uint4{(c << 3 & kMask) | kOne, (c >> 1 & kMask) | kOne, (c >> 5 & kMask) | kOne,
+               (c >> 9 & kMask) | kOne};
+}
+// Eight BF16 values in that order.
+__device__ __forceinline__ uint4 int4_order(uint4 x) {
+  return uint4{__builtin_amdgcn_perm(x.z, x.x, 0x05040100u), __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
+               __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
+}
+
+// Transposes the 4 x 4 words that the wave's four rows of 16 lanes hold: word j
+// of row g becomes word g of row j.
+__device__ __forceinline__ uint4 row_transpose(uint4 w) {
+  auto s0 = __builtin_amdgcn_permlane16_swap(w.x, w.y, false, false);
+  auto s1 = __builtin_amdgcn_permlane16_swap(w.z, w.w, false, false);
+  auto t0 = __builtin_amdgcn_permlane32_swap(s0[0], s1[0], false, false);
+  auto t1 = __builtin_amdgcn_permlane32_swap(s0[1], s1[1], false, false);
+  return uint4{t0[0], t1[0], t0[1], t1[1]};
+}
+
+__device__ __forceinline__ float int4_scale(uint32_t bits, int f16) {
+  const float h = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
+  return f16 ? h : bf16_to_f32(bits);
+}
+
+// SiLU(gate) * up in fp32; a NaN passes the clamps.
+__device__ __forceinline__ float int4_gated(int act, float g, float u, float lim) {
+  if (act == 1) g = g > lim ? lim : g;
+  float s = g / (1.0f + expf(-g));
+  if (act == 2) s = s > lim ? lim : s;
+  if (act != 0) u = fabsf(u) > lim ? __builtin_copysignf(lim, u) : u;
+  return s * u;
+}
+
+// First row and live rows of expert e (no counts: all rows are one expert's).
+__device__ __forceinline__ int int4_seg_start(const Int4GemmArgs& p, int e) {
+  return !p.counts ? 0 : p.seg_cap > 0 ? e * p.seg_cap : p.offsets[e];
+}
+__device__ __forceinline__ int int4_rows(const Int4GemmArgs& p, int e) {
+  if (!p.counts) return p.row_cap;
+  const int s0 = int4_seg_start(p, e);
+  const int s1 = p.seg_cap > 0 ? s0 + p.seg_cap : p.offsets[e + 1];
+  return segment_rows(s0, s1, p.counts[e], p.row_cap);
+}
+// Row of A behind row r, -1 if there is none (the entry's own sign decides:
+// divided first, -1 .. -(a_row_div - 1) would be row 0).
+__device__ __forceinline__ int int4_source(const Int4GemmArgs& p, int r) {
+  const int v = p.a_row_map ? p.a_row_map[r] : r;
+  const int src = p.a_row_map ? v / p.a_row_div : r;
+  return v >= 0 && src < p.a_rows ? src : -1;
+}
+
+}  // namespace moe

@@ -180,6 +180,73 @@ hipError_t launch_layer_a4(const LayerA4Args& a, hipStream_t stream);
 hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                 uint16_t* out, hipStream_t stream);
 
+// RMS norm with the residual's addition and the quantization of its output
+// (moe_norm's fields in the C ABI).
+struct NormArgs {
+  const uint16_t* x;
+  int64_t ld;                // elements between x's rows
+  const uint16_t* residual;  // [t_cap, hidden] or nullptr
+  const void* weight;        // [hidden]
+  int weight_f32;
+  double eps;
+  int t_cap;
+  const int32_t* t_live_dev;
+  int hidden;
+  int fmt;
+  int rounding;
+  uint16_t* residual_out;    // set iff residual is
+  uint16_t* y;               // or nullptr
+  uint8_t* xq;               // or nullptr: no quantization
+  void* xs;
+};
+constexpr int kMaxNormHidden = 32768;  // a row in the registers of 1024 threads
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// 4-bit integer weights: codes [rows, cols/2], scales (BF16 or FP16) and zero
+// points (bytes, or nullptr: 8) [rows, cols/group].
+enum ElemType : int { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2 };
+struct Int4QuantArgs {
+  const void* w;
+  int type;                  // ElemType
+  int64_t rows;
+  int cols;
+  int group;                 // 32, 64 or 128
+  int scale_f16;
+  uint8_t* codes;
+  uint16_t* scales;
+  uint8_t* zeros;            // nullptr: symmetric
+};
+hipError_t launch_int4_quant(const Int4QuantArgs& a, hipStream_t stream);
+hipError_t launch_int4_dequant(const uint8_t* codes, const uint16_t* scales, int scale_f16,
+                               const uint8_t* zeros, int64_t rows, int cols, int group, uint16_t* out,
+                               hipStream_t stream);
+
+// Products of BF16 rows with such weights.
+constexpr int kMaxInt4K = 131072;
+struct Int4GemmArgs {
+  const uint16_t* a;
+  int a_rows;
+  const int32_t* a_row_map;  // or nullptr: identity
+  int a_row_div;
+  const uint8_t* w;          // [num_experts, n, k/2]
+  const uint16_t* scales;    // [num_experts, n, k/group]
+  const uint8_t* zeros;      // [num_experts, n, k/group] or nullptr: 8
+  int scale_f16;
+  int group;
+  const int32_t* counts;     // nullptr: one expert owns all row_cap rows
+  const int32_t* offsets;    // not read when seg_cap > 0
+  int seg_cap;
+  int num_experts;
+  int row_cap;
+  int max_rows_per_expert;   // host bound on counts[e]
+  int n;
+  int k;
+  int act;                   // Act, or -1: none
+  float limit;
+  uint16_t* c;               // [row_cap, n], gated [row_cap, n/2]
+};
+hipError_t launch_gemm_int4(const Int4GemmArgs& a, hipStream_t stream);
+
 // Top-k routing from router logits (the fields as moe_router's and
 // moe_route's in the C ABI).
 enum Score : int { kSoftmax = 0, kSigmoid = 1 };

@@ -29,7 +29,8 @@ __device__ __forceinline__ Vals8 unpack_bf16x8(uint4 raw) {
 
 // Quantizes the 8 values this lane holds against the group's scale; returns
 // the 8 codes packed little-endian and writes the stored scale when asked.
-template <int FMT>
+// KEEP_NAN: a NaN gets the format's NaN code (else it is one of the largest).
+template <int FMT, bool KEEP_NAN = false>
 __device__ __forceinline__ uint2 quantize8(const Vals8& x, float* scale_out, int rnd) {
   float amax = 0.0f;
 #pragma unroll
@@ -41,6 +42,12 @@ __device__ __forceinline__ uint2 quantize8(const Vals8& x, float* scale_out, int
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = scale_apply(x.v[i], s, inv, FMT, rnd);
   uint2 out;
+  if constexpr (KEEP_NAN) {
+    out.x = cvt_pk_e4m3_nan(q[0], q[1]) | (cvt_pk_e4m3_nan(q[2], q[3]) << 16);
+    out.y = cvt_pk_e4m3_nan(q[4], q[5]) | (cvt_pk_e4m3_nan(q[6], q[7]) << 16);
+    *scale_out = s;
+    return out;
+  }
   out.x = cvt_pk_e4m3(q[0], q[1]) | (cvt_pk_e4m3(q[2], q[3]) << 16);
   out.y = cvt_pk_e4m3(q[4], q[5]) | (cvt_pk_e4m3(q[6], q[7]) << 16);
   *scale_out = s;

@@ -15,6 +15,12 @@
  *   moe_topk_combine   top-k weighted sum of the expert outputs back to tokens, BF16
  *   moe_forward        all of the above on one stream
  *
+ * Around it: moe_rmsnorm_quant, the norm in front of the layer with the
+ * residual's addition and the quantization in one pass; and 4-bit integer
+ * weights with group scales (moe_int4_quant, moe_int4_dequant) and their
+ * products with BF16 tokens, dense (moe_gemm_int4) and per expert
+ * (moe_grouped_gemm_int4).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Pointers marked "device" are HIP device (or managed) memory owned by the
@@ -129,10 +135,19 @@ typedef enum {
 } moe_weight_fmt;
 
 typedef enum {
+  MOE_ACT_NONE = -1, /* no gate: moe_gemm_int4 and moe_grouped_gemm_int4 only */
   MOE_ACT_SWIGLU = 0,
   MOE_ACT_SWIGLU_CLAMP = 1,
   MOE_ACT_SWIGLU_CLAMP_AFTER_SILU = 2
 } moe_act;
+
+/* Types of values (norm weights; 4-bit weights before their quantization and
+ * their scales). */
+typedef enum {
+  MOE_ELEM_FP32 = 0,
+  MOE_ELEM_BF16 = 1,
+  MOE_ELEM_FP16 = 2
+} moe_elem_type;
 
 /* Scores of the router (moe_route). */
 typedef enum {
@@ -277,6 +292,123 @@ moe_status moe_act_quant(const uint16_t* x, int32_t t_cap, const int32_t* t_live
  * misaligned pointers). */
 moe_status moe_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
                              uint16_t* out, void* stream);
+
+/* RMS norm of the live tokens with the residual's addition and moe_act_quant
+ * of its output, in one pass. With h = bf16(x + residual), or x where residual
+ * is NULL:
+ *   residual_out = h
+ *   y = bf16( fl32( h / sqrt(mean(h^2) + eps) * weight ) )
+ *   (xq, xs) = moe_act_quant(y, fmt, rounding)
+ * The addition is in fp32; the mean, the root and the products in double,
+ * rounded once to fp32 and then to BF16. y is what its codes are made of, so
+ * the results are those of an addition, a norm and moe_act_quant in a row. A
+ * row with a NaN or an infinity in h gives NaN where the formula does; in FP8
+ * a NaN gets E4M3's NaN code (the group's scale goes by the other values).
+ *
+ *   x            device BF16 [t_cap, hidden], rows `ld` elements apart
+ *   residual     device BF16 [t_cap, hidden] or NULL
+ *   weight       device [hidden], BF16 or FP32
+ *   eps          finite, >= 0
+ *   residual_out device BF16 [t_cap, hidden]; NULL exactly where residual is.
+ *                It may be `residual` itself, or x if ld = hidden
+ *   y            device BF16 [t_cap, hidden] or NULL; it may be x (if ld =
+ *                hidden) or residual, if these are not also residual_out
+ *   xq, xs       as moe_act_quant, or both NULL: no quantization (fmt and
+ *                rounding are checked all the same)
+ * Rows t >= t_live are untouched. All but xs are 16-byte aligned (xq 4-byte
+ * for MXFP4, 8-byte for FP8), ld is a multiple of 8.
+ * Errors: INVALID_ARG (hidden not a positive multiple of 128, ld < hidden or
+ * not a multiple of 8, null or misaligned pointers, unknown enum values, eps,
+ * no output, one of residual and residual_out alone, one of xq and xs alone,
+ * outputs that overlap an input or each other in another way than above),
+ * UNSUPPORTED (hidden above 32768). */
+moe_status moe_rmsnorm_quant(const uint16_t* x, int64_t ld, const uint16_t* residual,
+                             const void* weight, moe_elem_type weight_type, double eps, int32_t t_cap,
+                             const int32_t* t_live_dev, int32_t hidden, moe_scale_fmt fmt,
+                             moe_rounding rounding, uint16_t* residual_out, uint16_t* y, uint8_t* xq,
+                             void* xs, void* stream);
+
+/* 4-bit integer weights with group scales, the values
+ *   w(n, k) = s(n, k / group) * (q(n, k) - z(n, k / group)),  q in 0 .. 15:
+ * codes two per byte with the even column in the low nibble, [rows, cols/2];
+ * one scale (BF16 or FP16) and, where there are zero points, one byte per
+ * `group` (32, 64 or 128) consecutive columns, [rows, cols/group] each. Without
+ * zero points z = 8. A zero point may be any byte.
+ *
+ * moe_int4_quant makes them of FP32, BF16 or FP16 weights w [rows, cols]. With T
+ * the rounding to the scales' type and rne to the nearest integer, ties to even:
+ *   zeros NULL:  s = T(fl32(amax / 7)),  q = rne(w / s) + 8
+ *   zeros given: s = T(fl32(fl32(hi - lo) / 15)),  z = rne(-lo / s),
+ *                q = rne(w / s) + z,  lo = min(least, 0), hi = max(largest, 0)
+ * z and q clamped to 0 .. 15, w / s by the stored s and exact. A group whose s
+ * is zero gets codes and zero point of value zero (q = z = 8, or 0). A group
+ * that holds an infinity or a NaN, or whose s is beyond its type, gets the same
+ * codes and the scale NaN, so that all that reads it is NaN.
+ *   w      device [rows, cols] of `type`, 16-byte aligned
+ *   codes  device uint8 [rows, cols/2], 4-byte aligned
+ *   scales device [rows, cols/group] of `scale_type` (BF16 or FP16)
+ *   zeros  device uint8 [rows, cols/group], or NULL: symmetric
+ * moe_int4_dequant gives back their BF16 values, rounded once.
+ *   codes 8-byte, out 16-byte aligned
+ * Errors: INVALID_ARG (rows < 0, cols not a positive multiple of group, another
+ * group, type or scale_type, null or misaligned pointers). */
+moe_status moe_int4_quant(const void* w, moe_elem_type type, int64_t rows, int32_t cols, int32_t group,
+                          moe_elem_type scale_type, uint8_t* codes, uint16_t* scales, uint8_t* zeros,
+                          void* stream);
+moe_status moe_int4_dequant(const uint8_t* codes, const uint16_t* scales, moe_elem_type scale_type,
+                            const uint8_t* zeros, int64_t rows, int32_t cols, int32_t group,
+                            uint16_t* out, void* stream);
+
+/* Device tensors of 4-bit integer weights: [num_experts, n, .] of the layout above. */
+typedef struct {
+  const uint8_t* codes;     /* [num_experts, n, k/2], 16-byte aligned */
+  const uint16_t* scales;   /* [num_experts, n, k/group] */
+  const uint8_t* zeros;     /* [num_experts, n, k/group] or NULL */
+  moe_elem_type scale_type; /* BF16 or FP16 */
+  int32_t group;            /* 32, 64 or 128 */
+  int32_t num_experts;
+  int32_t n;
+  int32_t k;                /* a multiple of group */
+} moe_int4_weights;
+
+/* Product of BF16 rows with 4-bit integer weights (not quantizing the rows):
+ *   S[r, n] = sum_g s[n, g] * sum_{j in group g} a[r, j] * (q[n, j] - z[n, g])
+ *   act MOE_ACT_NONE:  c[r, n] = bf16(S[r, n])
+ *   otherwise, with N = n / 2 (moe_act's formulas, in fp32):
+ *                      c[r, i] = bf16(act(gate = S[r, i], up = S[r, N + i]))
+ * A group's sum, the scaling and the sum over the groups are in fp32 and
+ * rounded once. The product takes sum a (16 + q) - (16 + z) sum a for a
+ * group's sum: a row with a NaN or an infinity gives NaN, and fp32 must hold 31
+ * times a group's sum of magnitudes. A NaN passes the clamps. Any n >= 1 (even
+ * where gated) and any number of rows. The order of a sum may depend on the
+ * launch (rows, max_rows_per_expert): low bits may differ between calls that
+ * differ in these; the same call gives the same bits.
+ *
+ * moe_gemm_int4: one matrix (num_experts = 1).
+ *   a           device BF16 [rows, k], 16-byte aligned
+ *   t_live_dev  live rows on the device, clamped to [0, rows], or NULL: rows
+ *   c           device BF16 [rows, n] (gated [rows, n/2]); rows past the live
+ *               ones untouched
+ * moe_grouped_gemm_int4: the live rows of every expert, as
+ * moe_grouped_gemm_mxfp4 takes them (aligned or, with expert_cap > 0, batched
+ * layout; a live row whose a_row_map entry is negative or past the end has
+ * zeros for its row of a, so gets zeros).
+ *   a, a_rows, a_row_map, a_row_div, expert_counts, expert_offsets, expert_cap,
+ *   row_cap, max_rows_per_expert  as moe_grouped_gemm_mxfp4
+ *   c           device BF16 [row_cap, n] (gated [row_cap, n/2]); only live rows
+ *               written
+ * Errors: INVALID_ARG (sizes, null or misaligned pointers, another group,
+ * scale_type or act, an odd n or, for the clamped activations, a clamp_limit
+ * that is not > 0 where gated, the layouts' as moe_grouped_gemm_mxfp4),
+ * UNSUPPORTED (num_experts above 1024, k above 131072, n * k at or above 2^32). */
+moe_status moe_gemm_int4(const uint16_t* a, int32_t rows, const int32_t* t_live_dev,
+                         const moe_int4_weights* w, moe_act act, float clamp_limit, uint16_t* c,
+                         void* stream);
+moe_status moe_grouped_gemm_int4(const uint16_t* a, int32_t a_rows, const int32_t* a_row_map,
+                                 int32_t a_row_div, const moe_int4_weights* w,
+                                 const int32_t* expert_counts, const int32_t* expert_offsets,
+                                 int32_t expert_cap, int32_t row_cap, int32_t max_rows_per_expert,
+                                 moe_act act, float clamp_limit, uint16_t* c, void* stream);
 
 /* Grouped FP8 x FP8 GEMM with per-block scales, over the live rows of every
  * expert segment only (vLLM PR #59128, Purpose and SM90-on-H200: both grouped

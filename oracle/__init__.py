@@ -38,6 +38,7 @@ from .align import align, align_batched
 from .moe import (ACTS, MX_BLOCK, WEIGHT_FMTS, combine, forward, gemm_rows_mxfp4,
                   grouped_gemm, mxfp4_dequant, silu_mul_quant, swiglu, token_forward,
                   unquantized_reference)
+from .int4 import gemm_int4, int4_quantize, int4_values, rmsnorm, scale_round, scale_values
 from .mx4 import gemm_rows_mx4, mxfp4_quantize, route, token_forward_mx4
 
 __all__ = [
@@ -48,4 +49,5 @@ __all__ = [
     "scales_to_f64", "align", "align_batched", "ACTS", "combine", "forward", "grouped_gemm",
     "silu_mul_quant", "swiglu", "token_forward", "unquantized_reference",
     "gemm_rows_mx4", "mxfp4_quantize", "route", "token_forward_mx4",
+    "gemm_int4", "int4_quantize", "int4_values", "rmsnorm", "scale_round", "scale_values",
 ]
