@@ -31,7 +31,7 @@ __device__ __forceinline__ bool int4_unit(const Int4GemmArgs& p, int u, int* exp
   for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
     const int e = e0 + lane;
     const int c = e < p.num_experts ? int4_rows(p, e) : 0;
-    const int tiles = (c + TM - 1) / TM;
+    const int tiles = c <= p.few ? (c + TM - 1) / TM : 0;
     int incl = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -187,6 +187,271 @@ __global__ __launch_bounds__(kI4Threads) void int4_stream_kernel(Int4GemmArgs p)
   }
 }
 
+
+// ---- many rows per expert: tiles of BF16 rows through LDS ---------------------
+//
+// Here the matrix cores bound the product, and a sum per group outside them
+// would cost as many instructions as they have to spare. So the weights enter
+// them as the BF16 values bf16(s (q - z)) that moe_int4_dequant gives, made in
+// registers as they are needed: each rounding is 2^-9 of its weight, over K
+// weights a random error of about what the output's own rounding is.
+//
+// A code becomes a float by v_cvt_pk_f32_fp8: the E4M3 byte 0 .. 15 stands for
+// q 2^-9. fma(q 2^-9, 2^9 s, -s z) is exact, two at a time rounded to BF16: 19
+// instructions for 8 codes, against four 32x32x16 MFMAs of 32 cycles each that
+// use them.
+//
+// A workgroup of four waves owns 32 TT rows of A and 128 NT weight rows, a wave
+// all of the rows and 32 NT of the weight rows, whose codes it loads straight
+// into registers (a tile of few rows of A and many weight rows moves the least:
+// a weight is a quarter of an activation). The rows of A pass through LDS, two
+// buffers of 128 K values. K order: the lanes of half h hold the 128 K values
+// from 128 h of 256, so that a lane needs few scales and a row's 128-byte lines
+// are loaded whole.
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v2f __attribute__((ext_vector_type(2)));
+
+constexpr int kTlThreads = 256;
+
+__device__ __forceinline__ v16f mfma_bf16_32(uint4 a, uint4 b, v16f acc) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                 acc, 0, 0, 0);
+}
+
+// The eight weights of a word: s9 = 2^9 s, sz = -s z.
+__device__ __forceinline__ uint4 int4_weights(uint32_t c, float s9, float sz) {
+  const uint32_t even = c & 0x0F0F0F0Fu, odd = c >> 4 & 0x0F0F0F0Fu;
+  const v2f e0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(even), false);
+  const v2f e1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(even), true);
+  const v2f o0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(odd), false);
+  const v2f o1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(odd), true);
+  auto w = [&](float q) { return __builtin_fmaf(q, s9, sz); };
+  const uint2 a = pack_bf16x4(v4f{w(e0[0]), w(o0[0]), w(e0[1]), w(o0[1])});
+  const uint2 b = pack_bf16x4(v4f{w(e1[0]), w(o1[0]), w(e1[1]), w(o1[1])});
+  return uint4{a.x, a.y, b.x, b.y};
+}
+
+// Tile of this workgroup: workgroups go round-robin over the 8 XCDs; an XCD
+// takes consecutive tiles, an expert's row tiles of one column tile first, so
+// that its L2 serves their weights and the rows' next column tiles.
+struct Int4Tile {
+  int expert, row0, rows, col_tile;
+};
+template <int TM>
+__device__ __forceinline__ bool int4_tile(const Int4GemmArgs& p, int col_tiles, Int4Tile* t) {
+  const int lane = threadIdx.x & 63;
+  int64_t units = 0;
+  if (!p.counts) {
+    units = (p.row_cap + TM - 1) / TM;
+  } else {
+    for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
+      const int e = e0 + lane;
+      int c = e < p.num_experts ? int4_rows(p, e) : 0;
+      c = c > p.few ? (c + TM - 1) / TM : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d, 64);
+      units += c;
+    }
+  }
+  const int64_t total = units * col_tiles, per = (total + 7) / 8;
+  const int64_t id = flat_block(), at = (id & 7) * per + (id >> 3);
+  if ((id >> 3) >= per || at >= total) return false;
+  if (!p.counts) {
+    t->expert = 0;
+    t->row0 = static_cast<int>(at % units) * TM;
+    t->rows = min(TM, p.row_cap - t->row0);
+    t->col_tile = static_cast<int>(at / units);
+    return true;
+  }
+  int64_t before = 0;
+  for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
+    const int e = e0 + lane;
+    const int c = e < p.num_experts ? int4_rows(p, e) : 0;
+    const int tiles = c > p.few ? (c + TM - 1) / TM : 0;
+    int incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += v;
+    }
+    const int all = __shfl(incl, 63, 64);
+    if (at < (before + all) * col_tiles) {
+      const int l = __builtin_ctzll(__ballot((before + incl) * col_tiles > at));
+      const int mine = __shfl(tiles, l, 64), rows = __shfl(c, l, 64);
+      const int local = static_cast<int>(at - (before + __shfl(incl, l, 64) - mine) * col_tiles);
+      t->expert = e0 + l;
+      t->row0 = local % mine * TM;
+      t->rows = min(TM, rows - t->row0);
+      t->col_tile = local / mine;
+      return true;
+    }
+    before += all;
+  }
+  return false;
+}
+
+template <int G, int TT, int NT, bool GATED>
+__global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs p) {
+  constexpr int TM = 32 * TT;               // rows of A
+  constexpr int NC = GATED ? NT / 2 : NT;   // 32-column tiles of the output per wave
+  constexpr int AL = TM * 16 / kTlThreads;  // 16-byte loads of A per thread and step
+  constexpr int NS = 128 / G;               // scales of a lane per 256 K values
+  __shared__ __attribute__((aligned(256))) uint8_t s_a[2][TM * 256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r32 = lane & 31, h = lane >> 5;
+  const int K = p.k, out_n = GATED ? p.n / 2 : p.n, groups = K / G;
+  Int4Tile t;
+  if (!int4_tile<TM>(p, (out_n + 128 * NC - 1) / (128 * NC), &t)) return;
+  const int expert = __builtin_amdgcn_readfirstlane(t.expert), rows = __builtin_amdgcn_readfirstlane(t.rows);
+  const int row0 = __builtin_amdgcn_readfirstlane(t.row0) + int4_seg_start(p, expert);
+  const int n0 = __builtin_amdgcn_readfirstlane(t.col_tile) * 128 * NC + wave * 32 * NC;
+
+  // Rows of A: thread tid loads chunk tid % 16 of row tid / 16 + 16 i. Rows
+  // without a source load one that exists; their output is not this product's.
+  const uint16_t* a[AL];
+#pragma unroll
+  for (int i = 0; i < AL; ++i) {
+    const int r = (tid >> 4) + 16 * i;
+    const int src = r < rows ? int4_source(p, row0 + r) : -1;
+    a[i] = p.a + static_cast<int64_t>(max(src, 0)) * K;
+  }
+  const int chunk = tid & 15;
+  const int ak = 128 * (chunk >> 3) + 8 * (chunk & 7);  // its first K value of 256, in the first step
+  uint4 ra[AL];
+  auto load_a = [&](int b, int step) {
+    const int k = 256 * b + 64 * step + ak;
+    const int at = k < K ? k : 0;
+#pragma unroll
+    for (int i = 0; i < AL; ++i) ra[i] = *reinterpret_cast<const uint4*>(a[i] + at);
+    if (k >= K) {
+#pragma unroll
+      for (int i = 0; i < AL; ++i) ra[i] = uint4{0, 0, 0, 0};
+    }
+  };
+  const int put = (tid >> 4) * 256 + ((chunk ^ ((tid >> 4) & 15)) << 4);
+  auto store_a = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < AL; ++i) *reinterpret_cast<uint4*>(&s_a[buf][put + 4096 * i]) = ra[i];
+  };
+
+  // Weights: rows past the last take its place.
+  const uint8_t* wb = p.w + static_cast<int64_t>(expert) * p.n * (K / 2);
+  const uint16_t* sb = p.scales + static_cast<int64_t>(expert) * p.n * groups;
+  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(expert) * p.n * groups : nullptr;
+  uint32_t wo[NT], so[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int c = min(n0 + 32 * (n % NC) + r32, out_n - 1) + (GATED && n >= NC ? out_n : 0);
+    wo[n] = static_cast<uint32_t>(c) * static_cast<uint32_t>(K / 2);
+    so[n] = static_cast<uint32_t>(c) * static_cast<uint32_t>(groups);
+  }
+  uint4 w[NT][4];
+  uint32_t sc[NT][NS], zr[NT][NS];
+  auto load_w = [&](int b, int n, int i) {
+    const uint32_t at = 128 * b + 64 * h + 16 * i;
+    w[n][i] = *reinterpret_cast<const uint4*>(wb + (wo[n] + (2 * at < static_cast<uint32_t>(K) ? at : 0u)));
+  };
+  auto load_s = [&](int b, int n) {
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      const int at = min((256 * b + 128 * h) / G + q, groups - 1);
+      sc[n][q] = sb[so[n] + at];
+      zr[n][q] = zb ? zb[so[n] + at] : 8u;
+    }
+  };
+
+  v16f acc[NT][TT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < TT; ++m) acc[n][m] = v16f{};
+
+  const int blocks = (K + 255) / 256;
+  load_a(0, 0);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    load_s(0, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_w(0, n, i);
+  }
+  store_a(0);
+  lds_barrier();
+  const int get = r32 * 256;
+  for (int b = 0; b < blocks; ++b) {
+    const int nb = min(b + 1, blocks - 1);
+    float s9[NT][NS], sz[NT][NS];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int q = 0; q < NS; ++q) {
+        const float s = int4_scale(sc[n][q], p.scale_f16);
+        s9[n][q] = s * 512.0f;
+        sz[n][q] = -s * static_cast<float>(zr[n][q]);
+      }
+      load_s(nb, n);
+    }
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      // (past the end: the last block's again, unused)
+      load_a(step == 0 ? b : nb, step ^ 1);
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii) {
+        const int i = 2 * step + ii;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint4 x[TT];
+          const int at = get + (((8 * h + 4 * ii + j) ^ (r32 & 15)) << 4);
+#pragma unroll
+          for (int m = 0; m < TT; ++m) x[m] = *reinterpret_cast<const uint4*>(&s_a[step][at + 8192 * m]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t c = j == 0 ? w[n][i].x : j == 1 ? w[n][i].y : j == 2 ? w[n][i].z : w[n][i].w;
+            const uint4 f = int4_weights(c, s9[n][i * NS / 4], sz[n][i * NS / 4]);
+#pragma unroll
+            for (int m = 0; m < TT; ++m) acc[n][m] = mfma_bf16_32(f, x[m], acc[n][m]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) load_w(nb, n, i);
+      }
+      store_a(step ^ 1);
+      lds_barrier();
+    }
+  }
+
+  // A lane holds weight rows 8 v + 4 h .. + 3 (v = 0 .. 3) of its row of A.
+#pragma unroll
+  for (int m = 0; m < TT; ++m) {
+    const int r = 32 * m + r32;
+    if (r >= rows) continue;
+    const bool some = int4_source(p, row0 + r) >= 0;
+    uint16_t* c = p.c + static_cast<int64_t>(row0 + r) * out_n;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        v4f o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          o[k] = acc[n][m][4 * v + k];
+          if constexpr (GATED) o[k] = int4_gated(p.act, o[k], acc[n + NC][m][4 * v + k], p.limit);
+        }
+        uint2 bits = pack_bf16x4(o);
+        if (!some) bits = uint2{0, 0};
+        const int col = n0 + 32 * n + 8 * v + 4 * h;
+        if (p.vector_out) {
+          if (col < out_n) *reinterpret_cast<uint2*>(c + col) = bits;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (col + k < out_n) c[col + k] = static_cast<uint16_t>((k < 2 ? bits.x : bits.y) >> (16 * (k & 1)));
+        }
+      }
+    }
+  }
+}
+
 template <int G, int MT, bool GATED>
 hipError_t stream_launch(const Int4GemmArgs& p, hipStream_t stream) {
   constexpr int TM = 16 * MT;
@@ -199,25 +464,48 @@ hipError_t stream_launch(const Int4GemmArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int G, int TT, int NT, bool GATED>
+hipError_t tiled_launch(const Int4GemmArgs& p, hipStream_t stream) {
+  constexpr int TM = 32 * TT, NC = GATED ? NT / 2 : NT;
+  const int out_n = GATED ? p.n / 2 : p.n;
+  const int64_t used = p.num_experts < p.row_cap / (p.few + 1) ? p.num_experts : p.row_cap / (p.few + 1);
+  const int64_t units = p.counts ? p.row_cap / TM + used : (p.row_cap + TM - 1) / TM;
+  // A multiple of 8: every XCD's share rounded up.
+  const int64_t tasks = (units * ((out_n + 128 * NC - 1) / (128 * NC)) + 7) / 8 * 8;
+  hipLaunchKernelGGL((int4_tiled_kernel<G, TT, NT, GATED>), flat_grid(tasks), dim3(kTlThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
 template <int G, bool GATED>
-hipError_t stream_rows(const Int4GemmArgs& p, hipStream_t stream) {
-  if (p.max_rows_per_expert <= 16) return stream_launch<G, 1, GATED>(p, stream);
-  if (p.max_rows_per_expert <= 32) return stream_launch<G, 2, GATED>(p, stream);
-  return stream_launch<G, 4, GATED>(p, stream);
+hipError_t gemm_launch(Int4GemmArgs p, hipStream_t stream) {
+  const int out_n = GATED ? p.n / 2 : p.n;
+  p.vector_out = out_n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 7) == 0;
+  if (p.max_rows_per_expert <= kInt4FewRows) {
+    p.few = INT32_MAX;  // whatever the counts say
+    if (p.max_rows_per_expert <= 16) return stream_launch<G, 1, GATED>(p, stream);
+    if (p.max_rows_per_expert <= 32) return stream_launch<G, 2, GATED>(p, stream);
+    return stream_launch<G, 4, GATED>(p, stream);
+  }
+  p.few = kInt4FewRows;
+  if (p.counts) {
+    const hipError_t e = stream_launch<G, 4, GATED>(p, stream);
+    if (e != hipSuccess) return e;
+  }
+  return tiled_launch<G, 4, 4, GATED>(p, stream);
 }
 
 template <int G>
-hipError_t stream_act(const Int4GemmArgs& p, hipStream_t stream) {
-  return p.act >= 0 ? stream_rows<G, true>(p, stream) : stream_rows<G, false>(p, stream);
+hipError_t gemm_act(const Int4GemmArgs& p, hipStream_t stream) {
+  return p.act >= 0 ? gemm_launch<G, true>(p, stream) : gemm_launch<G, false>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_gemm_int4(const Int4GemmArgs& p, hipStream_t stream) {
   switch (p.group) {
-    case 32: return stream_act<32>(p, stream);
-    case 64: return stream_act<64>(p, stream);
-    default: return stream_act<128>(p, stream);
+    case 32: return gemm_act<32>(p, stream);
+    case 64: return gemm_act<64>(p, stream);
+    default: return gemm_act<128>(p, stream);
   }
 }
 

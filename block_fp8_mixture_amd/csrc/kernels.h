@@ -244,7 +244,12 @@ struct Int4GemmArgs {
   int act;                   // Act, or -1: none
   float limit;
   uint16_t* c;               // [row_cap, n], gated [row_cap, n/2]
+  int few = 0;               // set by the launcher: rows of an expert that streams
+  int vector_out = 0;        // set by the launcher: four columns of c at once
 };
+// Experts of at most this many rows have their weights streamed, exact; more
+// rows multiply weights rounded to BF16.
+constexpr int kInt4FewRows = 64;
 hipError_t launch_gemm_int4(const Int4GemmArgs& a, hipStream_t stream);
 
 // Top-k routing from router logits (the fields as moe_router's and
