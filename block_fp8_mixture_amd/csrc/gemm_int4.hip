@@ -7,6 +7,8 @@
 // holds row l % 16 and the K values 8 (l / 16) .. + 7) and weight rows as its
 // second (alike); lane l of the result holds weight row l % 16 and rows of A
 // 4 (l / 16) + v, so a lane needs one row's scales.
+#include <utility>
+
 #include "int4_device.h"
 
 namespace moe {
@@ -214,6 +216,16 @@ typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kTlThreads = 256;
 
+// f(integral_constant 0), .., f(integral_constant N - 1).
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_seq(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_seq(f, std::make_integer_sequence<int, N>{});
+}
+
 __device__ __forceinline__ v16f mfma_bf16_32(uint4 a, uint4 b, v16f acc) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                  acc, 0, 0, 0);
@@ -296,7 +308,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   constexpr int TM = 32 * TT;               // rows of A
   constexpr int NC = GATED ? NT / 2 : NT;   // 32-column tiles of the output per wave
   constexpr int AL = TM * 16 / kTlThreads;  // 16-byte loads of A per thread and step
-  constexpr int NS = 128 / G;               // scales of a lane per 256 K values
+  constexpr int NS = 128 / G;               // scales of a lane and weight row per 256 K values
   __shared__ __attribute__((aligned(256))) uint8_t s_a[2][TM * 256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5;
@@ -318,27 +330,25 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   }
   const int chunk = tid & 15;
   const int ak = 128 * (chunk >> 3) + 8 * (chunk & 7);  // its first K value of 256, in the first step
-  uint4 ra[AL];
-  auto load_a = [&](int b, int step) {
+  u32x4 ra0[AL], ra1[AL];  // of the first and the second step
+  auto load_a = [&](u32x4 (&ra)[AL], int b, int step) {  // (past K: the row's start)
     const int k = 256 * b + 64 * step + ak;
     const int at = k < K ? k : 0;
 #pragma unroll
-    for (int i = 0; i < AL; ++i) ra[i] = *reinterpret_cast<const uint4*>(a[i] + at);
-    if (k >= K) {
-#pragma unroll
-      for (int i = 0; i < AL; ++i) ra[i] = uint4{0, 0, 0, 0};
-    }
+    for (int i = 0; i < AL; ++i) ra[i] = *reinterpret_cast<const u32x4*>(a[i] + at);
   };
   const int put = (tid >> 4) * 256 + ((chunk ^ ((tid >> 4) & 15)) << 4);
-  auto store_a = [&](int buf) {
+  auto store_a = [&](const u32x4 (&ra)[AL], int step) {
 #pragma unroll
-    for (int i = 0; i < AL; ++i) *reinterpret_cast<uint4*>(&s_a[buf][put + 4096 * i]) = ra[i];
+    for (int i = 0; i < AL; ++i) *reinterpret_cast<u32x4*>(&s_a[step][put + 4096 * i]) = ra[i];
   };
 
   // Weights: rows past the last take its place.
   const uint8_t* wb = p.w + static_cast<int64_t>(expert) * p.n * (K / 2);
   const uint16_t* sb = p.scales + static_cast<int64_t>(expert) * p.n * groups;
-  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(expert) * p.n * groups : nullptr;
+  // (without zero points the loads read bytes of the scales, unused)
+  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(expert) * p.n * groups
+                              : reinterpret_cast<const uint8_t*>(sb);
   uint32_t wo[NT], so[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -346,19 +356,31 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
     wo[n] = static_cast<uint32_t>(c) * static_cast<uint32_t>(K / 2);
     so[n] = static_cast<uint32_t>(c) * static_cast<uint32_t>(groups);
   }
+  const int blocks = (K + 255) / 256;
   uint4 w[NT][4];
-  uint32_t sc[NT][NS], zr[NT][NS];
-  auto load_w = [&](int b, int n, int i) {
-    const uint32_t at = 128 * b + 64 * h + 16 * i;
+  auto load_w = [&](int b, int n, int i) {  // (past K: the row's start)
+    const uint32_t at = 128 * min(b, blocks - 1) + 64 * h + 16 * i;
     w[n][i] = *reinterpret_cast<const uint4*>(wb + (wo[n] + (2 * at < static_cast<uint32_t>(K) ? at : 0u)));
   };
-  auto load_s = [&](int b, int n) {
-#pragma unroll
-    for (int q = 0; q < NS; ++q) {
-      const int at = min((256 * b + 128 * h) / G + q, groups - 1);
-      sc[n][q] = sb[so[n] + at];
-      zr[n][q] = zb ? zb[so[n] + at] : 8u;
-    }
+  // A lane's scale in use, and the next as stored. Columns past K have the scale
+  // zero: A's row is read from its start there. Selects go by masks: branches
+  // would cut the MFMAs' schedule.
+  uint32_t sc[NT], zr[NT];
+  float s9[NT], sz[NT];
+  uint32_t is_f16 = p.scale_f16 ? ~0u : 0u, has_z = p.zeros ? ~0u : 0u;
+  asm volatile("" : "+v"(is_f16), "+v"(has_z));
+  auto load_s = [&](int n, int k) {
+    const int at = min((k + 128 * h) / G, groups - 1);
+    sc[n] = sb[so[n] + at];
+    zr[n] = zb[so[n] + at];
+  };
+  auto use_s = [&](int n, int k) {
+    const uint32_t half = __float_as_uint(static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sc[n]))));
+    const uint32_t bits = (half & is_f16) | (sc[n] << 16 & ~is_f16);
+    const uint32_t keep = static_cast<uint32_t>((k + 128 * h - K) >> 31);
+    const float s = __uint_as_float(bits & keep);
+    s9[n] = s * 512.0f;
+    sz[n] = -s * static_cast<float>((zr[n] & has_z) | (8u & ~has_z));
   };
 
   v16f acc[NT][TT];
@@ -367,57 +389,79 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
 #pragma unroll
     for (int m = 0; m < TT; ++m) acc[n][m] = v16f{};
 
-  const int blocks = (K + 255) / 256;
-  load_a(0, 0);
+  load_a(ra0, 0, 0);
+  load_a(ra1, 0, 1);
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    load_s(0, n);
+    load_s(n, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_w(0, n, i);
   }
-  store_a(0);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    use_s(n, 0);
+    load_s(n, NS > 1 ? G : 256);
+  }
+  store_a(ra0, 0);
   lds_barrier();
   const int get = r32 * 256;
+  // Row fragments of block (step, q): K values 8 q .. of both halves' 64.
+  auto read_x = [&](uint4 (&x)[TT], int step, int q) {
+    const int at = get + (((8 * h + q) ^ (r32 & 15)) << 4);
+#pragma unroll
+    for (int m = 0; m < TT; ++m) x[m] = *reinterpret_cast<const uint4*>(&s_a[step][at + 8192 * m]);
+  };
+  auto weights = [&](int n, int i, int j) {
+    const uint32_t c = j == 0 ? w[n][i].x : j == 1 ? w[n][i].y : j == 2 ? w[n][i].z : w[n][i].w;
+    return int4_weights(c, s9[n], sz[n]);
+  };
+  uint4 x[2][TT];
+  read_x(x[0], 0, 0);
+  uint4 f = weights(0, 0, 0);
   for (int b = 0; b < blocks; ++b) {
-    const int nb = min(b + 1, blocks - 1);
-    float s9[NT][NS], sz[NT][NS];
+    // 16 blocks of 8 K values per half: the MFMAs of a weight tile go between
+    // the instructions that make the next tile's weights, so that neither waits
+    // for the other.
+    static_for<16>([&](auto block) __attribute__((always_inline)) {
+        constexpr int step = block / 8, q = block % 8, i = block / 4, j = block % 4;
+        // The rows of the step after the next (past the end: the last block's
+        // again, unused). The next step's are written three blocks before its
+        // first and read in this step's last block, past a barrier.
+        if constexpr (block == 0) load_a(ra0, min(b + 1, blocks - 1), 0);
+        if constexpr (block == 8) load_a(ra1, min(b + 1, blocks - 1), 1);
+        if constexpr (block == 5) store_a(ra1, 1);
+        if constexpr (block == 13) store_a(ra0, 0);
+        if (q == 7) lds_barrier();
+        read_x(x[(q + 1) & 1], q == 7 ? step ^ 1 : step, (q + 1) & 7);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int q = 0; q < NS; ++q) {
-        const float s = int4_scale(sc[n][q], p.scale_f16);
-        s9[n][q] = s * 512.0f;
-        sz[n][q] = -s * static_cast<float>(zr[n][q]);
-      }
-      load_s(nb, n);
-    }
-#pragma unroll
-    for (int step = 0; step < 2; ++step) {
-      // (past the end: the last block's again, unused)
-      load_a(step == 0 ? b : nb, step ^ 1);
-#pragma unroll
-      for (int ii = 0; ii < 2; ++ii) {
-        const int i = 2 * step + ii;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 x[TT];
-          const int at = get + (((8 * h + 4 * ii + j) ^ (r32 & 15)) << 4);
-#pragma unroll
-          for (int m = 0; m < TT; ++m) x[m] = *reinterpret_cast<const uint4*>(&s_a[step][at + 8192 * m]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint32_t c = j == 0 ? w[n][i].x : j == 1 ? w[n][i].y : j == 2 ? w[n][i].z : w[n][i].w;
-            const uint4 f = int4_weights(c, s9[n][i * NS / 4], sz[n][i * NS / 4]);
-#pragma unroll
-            for (int m = 0; m < TT; ++m) acc[n][m] = mfma_bf16_32(f, x[m], acc[n][m]);
+        for (int n = 0; n < NT; ++n) {
+          // The last of a scale's weights were made in the slot before: the next
+          // scale, q' of block b', and the load of the one after it.
+          if constexpr (j == 3 && (i + 1) % (4 / NS) == 0) {
+            constexpr int to = (i + 1) / (4 / NS), after = to + 1;
+            use_s(n, 256 * (b + to / NS) + G * (to % NS));
+            load_s(n, 256 * (b + after / NS) + G * (after % NS));
           }
+          const uint4 next = n + 1 < NT ? weights(n + 1, i, j) : weights(0, (i + (j == 3)) & 3, (j + 1) & 3);
+#pragma unroll
+          for (int m = 0; m < TT; ++m) acc[n][m] = mfma_bf16_32(f, x[q & 1][m], acc[n][m]);
+          f = next;
+        }
+        // (word 3 of chunk i is in use until the block's third slot)
+        if (j == 3) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) load_w(b + 1, n, i);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) load_w(nb, n, i);
-      }
-      store_a(step ^ 1);
-      lds_barrier();
-    }
+        for (int k = 0; k < NT * TT; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                             // MFMA
+          __builtin_amdgcn_sched_group_barrier(0x002, q == 0 || j == 3 ? 6 : 5, 0);      // VALU
+          if (k < TT) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 // LDS read
+          if (q == 5 && k < AL) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);       // LDS write
+          if (q == 0 || j == 3) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);       // load
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    });
   }
 
   // A lane holds weight rows 8 v + 4 h .. + 3 (v = 0 .. 3) of its row of A.
