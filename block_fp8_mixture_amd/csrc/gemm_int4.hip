@@ -231,17 +231,43 @@ __device__ __forceinline__ v16f mfma_bf16_32(uint4 a, uint4 b, v16f acc) {
                                                  acc, 0, 0, 0);
 }
 
-// The eight weights of a word: s9 = 2^9 s, sz = -s z.
-__device__ __forceinline__ uint4 int4_weights(uint32_t c, float s9, float sz) {
-  const uint32_t even = c & 0x0F0F0F0Fu, odd = c >> 4 & 0x0F0F0F0Fu;
-  const v2f e0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(even), false);
-  const v2f e1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(even), true);
-  const v2f o0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(odd), false);
-  const v2f o1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(odd), true);
+// The eight weights of a word, s9 = 2^9 s, sz = -s z, in four steps that go between
+// MFMAs.
+struct Int4Unpack {
+  uint32_t even, odd;
+  v2f e0, e1, o0, o1;
+  uint4 f;
+};
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), bf16x2));
+}
+template <int STEP>
+__device__ __forceinline__ void int4_unpack(Int4Unpack& u, uint32_t c, float s9, float sz) {
   auto w = [&](float q) { return __builtin_fmaf(q, s9, sz); };
-  const uint2 a = pack_bf16x4(v4f{w(e0[0]), w(o0[0]), w(e0[1]), w(o0[1])});
-  const uint2 b = pack_bf16x4(v4f{w(e1[0]), w(o1[0]), w(e1[1]), w(o1[1])});
-  return uint4{a.x, a.y, b.x, b.y};
+  if constexpr (STEP == 0) {
+    u.even = c & 0x0F0F0F0Fu;
+    u.odd = c >> 4 & 0x0F0F0F0Fu;
+    u.e0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.even), false);
+    u.o0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.odd), false);
+  } else if constexpr (STEP == 1) {
+    u.e1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.even), true);
+    u.o1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.odd), true);
+    u.e0[0] = w(u.e0[0]);
+    u.o0[0] = w(u.o0[0]);
+    u.e0[1] = w(u.e0[1]);
+  } else if constexpr (STEP == 2) {
+    u.o0[1] = w(u.o0[1]);
+    u.f.x = pack_bf16x2(u.e0[0], u.o0[0]);
+    u.e1[0] = w(u.e1[0]);
+    u.o1[0] = w(u.o1[0]);
+    u.f.y = pack_bf16x2(u.e0[1], u.o0[1]);
+  } else {
+    u.e1[1] = w(u.e1[1]);
+    u.o1[1] = w(u.o1[1]);
+    u.f.z = pack_bf16x2(u.e1[0], u.o1[0]);
+    u.f.w = pack_bf16x2(u.e1[1], u.o1[1]);
+  }
 }
 
 // Tile of this workgroup: workgroups go round-robin over the 8 XCDs; an XCD
@@ -308,9 +334,14 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   constexpr int TM = 32 * TT;               // rows of A
   constexpr int NC = GATED ? NT / 2 : NT;   // 32-column tiles of the output per wave
   constexpr int AL = TM * 16 / kTlThreads;  // 16-byte loads of A per thread and step
+  constexpr int WL = 2 * NT;                // and of codes
   constexpr int NS = 128 / G;               // scales of a lane and weight row per 256 K values
-  __shared__ __attribute__((aligned(256))) uint8_t s_a[2][TM * 256];
+  constexpr int kABytes = TM * 256, kWBytes = NT * 2048;  // of a step; codes: of one wave
+  __shared__ __attribute__((aligned(256))) uint8_t s_buf[2 * kABytes + 8 * kWBytes];
+  __shared__ uint8_t s_some[TM];
+  uint8_t* const s_a = s_buf;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint8_t* const s_w = s_buf + 2 * kABytes + wave * (2 * kWBytes);
   const int r32 = lane & 31, h = lane >> 5;
   const int K = p.k, out_n = GATED ? p.n / 2 : p.n, groups = K / G;
   Int4Tile t;
@@ -318,61 +349,82 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   const int expert = __builtin_amdgcn_readfirstlane(t.expert), rows = __builtin_amdgcn_readfirstlane(t.rows);
   const int row0 = __builtin_amdgcn_readfirstlane(t.row0) + int4_seg_start(p, expert);
   const int n0 = __builtin_amdgcn_readfirstlane(t.col_tile) * 128 * NC + wave * 32 * NC;
+  const int blocks = (K + 255) / 256;
 
   // Rows of A: thread tid loads chunk tid % 16 of row tid / 16 + 16 i. Rows
-  // without a source load one that exists; their output is not this product's.
+  // without a source load one that exists; their output is zero.
   const uint16_t* a[AL];
 #pragma unroll
   for (int i = 0; i < AL; ++i) {
     const int r = (tid >> 4) + 16 * i;
     const int src = r < rows ? int4_source(p, row0 + r) : -1;
     a[i] = p.a + static_cast<int64_t>(max(src, 0)) * K;
+    if ((tid & 15) == 0) s_some[r] = src >= 0;
   }
   const int chunk = tid & 15;
   const int ak = 128 * (chunk >> 3) + 8 * (chunk & 7);  // its first K value of 256, in the first step
-  u32x4 ra0[AL], ra1[AL];  // of the first and the second step
-  auto load_a = [&](u32x4 (&ra)[AL], int b, int step) {  // (past K: the row's start)
-    const int k = 256 * b + 64 * step + ak;
-    const int at = k < K ? k : 0;
-#pragma unroll
-    for (int i = 0; i < AL; ++i) ra[i] = *reinterpret_cast<const u32x4*>(a[i] + at);
+  u32x4 ra[AL];
+  auto at_a = [&](int b, int step) {  // (past K: the row's start)
+    const int k = 256 * min(b, blocks - 1) + 64 * step + ak;
+    return k < K ? k : 0;
   };
+  auto load_a = [&](int at, int i) { ra[i] = *reinterpret_cast<const u32x4*>(a[i] + at); };
   const int put = (tid >> 4) * 256 + ((chunk ^ ((tid >> 4) & 15)) << 4);
-  auto store_a = [&](const u32x4 (&ra)[AL], int step) {
-#pragma unroll
-    for (int i = 0; i < AL; ++i) *reinterpret_cast<u32x4*>(&s_a[step][put + 4096 * i]) = ra[i];
+  auto store_a = [&](int step, int i) {
+    *reinterpret_cast<u32x4*>(s_a + step * kABytes + put + 4096 * i) = ra[i];
+  };
+  // Fragments of A's rows of block q: K values 8 q .. of both halves' 64.
+  const int get = r32 * 256;
+  auto read_a = [&](u32x4& x, int step, int q, int m) {
+    const int at = get + (((8 * h + q) ^ (r32 & 15)) << 4);
+    x = *reinterpret_cast<const u32x4*>(s_a + step * kABytes + at + 8192 * m);
   };
 
-  // Weights: rows past the last take its place.
+  // Codes go through LDS too, each wave its own: four neighbouring lanes load 64
+  // bytes of a row, 16 rows a load (a lane with a row of its own, as the operand
+  // has it, asks for 64 lines). Chunk 2 h' + i' of a row's step, the 32 K values
+  // 128 h' + 64 step + 32 i', is in slot chunk ^ (row / 4 % 4): 16 rows' reads
+  // of a chunk meet no bank twice. Weight rows past the last take its place.
   const uint8_t* wb = p.w + static_cast<int64_t>(expert) * p.n * (K / 2);
-  const uint16_t* sb = p.scales + static_cast<int64_t>(expert) * p.n * groups;
-  // (without zero points the loads read bytes of the scales, unused)
-  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(expert) * p.n * groups
-                              : reinterpret_cast<const uint8_t*>(sb);
-  uint32_t wo[NT], so[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int c = min(n0 + 32 * (n % NC) + r32, out_n - 1) + (GATED && n >= NC ? out_n : 0);
-    wo[n] = static_cast<uint32_t>(c) * static_cast<uint32_t>(K / 2);
-    so[n] = static_cast<uint32_t>(c) * static_cast<uint32_t>(groups);
-  }
-  const int blocks = (K + 255) / 256;
-  uint4 w[NT][4];
-  auto load_w = [&](int b, int n, int i) {  // (past K: the row's start)
-    const uint32_t at = 128 * min(b, blocks - 1) + 64 * h + 16 * i;
-    w[n][i] = *reinterpret_cast<const uint4*>(wb + (wo[n] + (2 * at < static_cast<uint32_t>(K) ? at : 0u)));
+  auto weight_row = [&](int n, int r) {
+    return static_cast<uint32_t>(min(n0 + 32 * (n % NC) + r, out_n - 1) + (GATED && n >= NC ? out_n : 0));
   };
+  uint32_t wo[WL];
+#pragma unroll
+  for (int k = 0; k < WL; ++k) wo[k] = weight_row(k >> 1, 16 * (k & 1) + (lane >> 2)) * static_cast<uint32_t>(K / 2);
+  const int wchunk = (lane & 3) ^ (lane >> 4);
+  u32x4 rw[WL];
+  auto at_w = [&](int b, int step) {  // (past K: the row's start)
+    const uint32_t at = 128 * min(b, blocks - 1) + 32 * step + 64 * (wchunk >> 1) + 16 * (wchunk & 1);
+    return 2 * at < static_cast<uint32_t>(K) ? at : 0u;
+  };
+  auto load_w = [&](uint32_t at, int k) { rw[k] = *reinterpret_cast<const u32x4*>(wb + (wo[k] + at)); };
+  auto store_w = [&](int step, int k) {
+    *reinterpret_cast<u32x4*>(s_w + step * kWBytes + 1024 * k + 16 * lane) = rw[k];
+  };
+  u32x4 w[2][NT];  // by the chunk's parity
+  auto read_w = [&](u32x4& to, int step, int ii, int n) {
+    const int at = r32 * 64 + (((2 * h + ii) ^ (r32 >> 2 & 3)) << 4);
+    to = *reinterpret_cast<const u32x4*>(s_w + step * kWBytes + 2048 * n + at);
+  };
+
   // A lane's scale in use, and the next as stored. Columns past K have the scale
   // zero: A's row is read from its start there. Selects go by masks: branches
-  // would cut the MFMAs' schedule.
-  uint32_t sc[NT], zr[NT];
+  // would cut the MFMAs' schedule. Without zero points the loads read bytes of
+  // the scales, unused.
+  const uint16_t* sb = p.scales + static_cast<int64_t>(expert) * p.n * groups;
+  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(expert) * p.n * groups
+                              : reinterpret_cast<const uint8_t*>(sb);
+  uint32_t so[NT], sc[NT], zr[NT];
   float s9[NT], sz[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) so[n] = weight_row(n, r32) * static_cast<uint32_t>(groups);
   uint32_t is_f16 = p.scale_f16 ? ~0u : 0u, has_z = p.zeros ? ~0u : 0u;
   asm volatile("" : "+v"(is_f16), "+v"(has_z));
   auto load_s = [&](int n, int k) {
-    const int at = min((k + 128 * h) / G, groups - 1);
-    sc[n] = sb[so[n] + at];
-    zr[n] = zb[so[n] + at];
+    const uint32_t at = so[n] + min((k + 128 * h) / G, groups - 1);
+    sc[n] = sb[at];
+    zr[n] = zb[at];
   };
   auto use_s = [&](int n, int k) {
     const uint32_t half = __float_as_uint(static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sc[n]))));
@@ -389,88 +441,102 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
 #pragma unroll
     for (int m = 0; m < TT; ++m) acc[n][m] = v16f{};
 
-  load_a(ra0, 0, 0);
-  load_a(ra1, 0, 1);
+  int aa = at_a(0, 0);
+  uint32_t aw = at_w(0, 0);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    load_s(n, 0);
+  for (int i = 0; i < AL; ++i) load_a(aa, i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_w(0, n, i);
+  for (int k = 0; k < WL; ++k) load_w(aw, k);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) load_s(n, 0);
+  aa = at_a(0, 1);
+  aw = at_w(0, 1);
+#pragma unroll
+  for (int i = 0; i < AL; ++i) {
+    store_a(0, i);
+    load_a(aa, i);
+  }
+#pragma unroll
+  for (int k = 0; k < WL; ++k) {
+    store_w(0, k);
+    load_w(aw, k);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     use_s(n, 0);
     load_s(n, NS > 1 ? G : 256);
   }
-  store_a(ra0, 0);
   lds_barrier();
-  const int get = r32 * 256;
-  // Row fragments of block (step, q): K values 8 q .. of both halves' 64.
-  auto read_x = [&](uint4 (&x)[TT], int step, int q) {
-    const int at = get + (((8 * h + q) ^ (r32 & 15)) << 4);
+  u32x4 x[2][TT];
 #pragma unroll
-    for (int m = 0; m < TT; ++m) x[m] = *reinterpret_cast<const uint4*>(&s_a[step][at + 8192 * m]);
-  };
-  auto weights = [&](int n, int i, int j) {
-    const uint32_t c = j == 0 ? w[n][i].x : j == 1 ? w[n][i].y : j == 2 ? w[n][i].z : w[n][i].w;
-    return int4_weights(c, s9[n], sz[n]);
-  };
-  uint4 x[2][TT];
-  read_x(x[0], 0, 0);
-  uint4 f = weights(0, 0, 0);
+  for (int m = 0; m < TT; ++m) read_a(x[0][m], 0, 0, m);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) read_w(w[0][n], 0, 0, n);
+  Int4Unpack u[2];  // the weights in use and the next tile's
+  static_for<4>([&](auto k) __attribute__((always_inline)) { int4_unpack<k>(u[0], w[0][0][0], s9[0], sz[0]); });
   for (int b = 0; b < blocks; ++b) {
-    // 16 blocks of 8 K values per half: the MFMAs of a weight tile go between
-    // the instructions that make the next tile's weights, so that neither waits
-    // for the other.
+    // 16 blocks of 8 K values per half, 8 a step: the MFMAs of a weight tile go
+    // between the instructions that make the next tile's weights, so that neither
+    // waits for the other. The loads and LDS writes are spread over the blocks
+    // (in bursts the waves wait for each other's, with the matrix cores idle): a
+    // register is written to the next step's buffer and loaded for the step after
+    // it (past the end: the last ones again, unused).
     static_for<16>([&](auto block) __attribute__((always_inline)) {
-        constexpr int step = block / 8, q = block % 8, i = block / 4, j = block % 4;
-        // The rows of the step after the next (past the end: the last block's
-        // again, unused). The next step's are written three blocks before its
-        // first and read in this step's last block, past a barrier.
-        if constexpr (block == 0) load_a(ra0, min(b + 1, blocks - 1), 0);
-        if constexpr (block == 8) load_a(ra1, min(b + 1, blocks - 1), 1);
-        if constexpr (block == 5) store_a(ra1, 1);
-        if constexpr (block == 13) store_a(ra0, 0);
-        if (q == 7) lds_barrier();
-        read_x(x[(q + 1) & 1], q == 7 ? step ^ 1 : step, (q + 1) & 7);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          // The last of a scale's weights were made in the slot before: the next
-          // scale, q' of block b', and the load of the one after it.
-          if constexpr (j == 3 && (i + 1) % (4 / NS) == 0) {
-            constexpr int to = (i + 1) / (4 / NS), after = to + 1;
-            use_s(n, 256 * (b + to / NS) + G * (to % NS));
-            load_s(n, 256 * (b + after / NS) + G * (after % NS));
+      constexpr int step = block / 8, q = block % 8, i = block / 4, j = block % 4;
+      if constexpr (q == 0) {
+        aa = at_a(b + 1, step);
+        aw = at_w(b + 1, step);
+      }
+      if constexpr (q == 7) lds_barrier();
+      // Slot k: an MFMA and what goes beside it, in this order.
+      static_for<NT * TT>([&](auto k) __attribute__((always_inline)) {
+        constexpr int n = k / TT, m = k % TT, slot = block * NT + n;
+        acc[n][m] = mfma_bf16_32(u[slot & 1].f, __builtin_bit_cast(uint4, x[q & 1][m]), acc[n][m]);
+        // The rows' fragments of the next block, and the next chunk of codes.
+        if constexpr (k < TT) read_a(x[(q + 1) & 1][k], q == 7 ? step ^ 1 : step, (q + 1) & 7, k);
+        if constexpr (j == 3 && k >= TT && k < TT + NT)
+          read_w(w[(i + 1) & 1][k - TT], q < 4 ? step : step ^ 1, (i + 1) & 1, k - TT);
+        // Pieces of A and of the codes, in the last block none: it reads the next
+        // step's, past a barrier.
+        constexpr int kPieces = AL + WL, kHalf = NT * TT / 2;
+        constexpr int p0 = q * kPieces / 7, p1 = q < 7 ? (q + 1) * kPieces / 7 : p0;
+        constexpr int piece = p0 + (k - kHalf) / 2;
+        if constexpr (k >= kHalf && piece < p1) {
+          if constexpr ((k - kHalf) % 2 == 0) {
+            if constexpr (piece < AL) store_a(step ^ 1, piece);
+            else store_w(step ^ 1, piece - AL);
+          } else {
+            if constexpr (piece < AL) load_a(aa, piece);
+            else load_w(aw, piece - AL);
           }
-          const uint4 next = n + 1 < NT ? weights(n + 1, i, j) : weights(0, (i + (j == 3)) & 3, (j + 1) & 3);
-#pragma unroll
-          for (int m = 0; m < TT; ++m) acc[n][m] = mfma_bf16_32(f, x[q & 1][m], acc[n][m]);
-          f = next;
         }
-        // (word 3 of chunk i is in use until the block's third slot)
-        if (j == 3) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) load_w(b + 1, n, i);
+        // The last of a scale's weights were made in the slot before: the next
+        // scale, and the load of the one after it.
+        if constexpr (m == 0 && j == 3 && (i + 1) % (4 / NS) == 0) {
+          constexpr int to = (i + 1) / (4 / NS), after = to + 1;
+          use_s(n, 256 * (b + to / NS) + G * (to % NS));
+          load_s(n, 256 * (b + after / NS) + G * (after % NS));
         }
-#pragma unroll
-        for (int k = 0; k < NT * TT; ++k) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                             // MFMA
-          __builtin_amdgcn_sched_group_barrier(0x002, q == 0 || j == 3 ? 6 : 5, 0);      // VALU
-          if (k < TT) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                 // LDS read
-          if (q == 5 && k < AL) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);       // LDS write
-          if (q == 0 || j == 3) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);       // load
-        }
+        constexpr int nn = (n + 1) % NT, ni = n + 1 < NT ? i : (i + (j == 3)) & 3, nj = n + 1 < NT ? j : (j + 1) & 3;
+        static_for<4 / TT>([&](auto l) __attribute__((always_inline)) {
+          int4_unpack<4 / TT * m + l>(u[(slot + 1) & 1], w[ni & 1][nn][nj], s9[nn], sz[nn]);
+        });
         __builtin_amdgcn_sched_barrier(0);
+      });
     });
   }
 
-  // A lane holds weight rows 8 v + 4 h .. + 3 (v = 0 .. 3) of its row of A.
+  // Output, through LDS so that a row's columns leave in whole lines. A lane
+  // holds weight rows 8 v + 4 h .. + 3 (v = 0 .. 3) of its row of A; a wave's
+  // rows of 32 NC columns lie in chunks of 8 columns, chunk c in slot c ^ row % 16
+  // (NC = 2: of half as long rows, c ^ row / 2 % 8).
+  constexpr int kRow = 64 * NC, kChunks = 4 * NC;
+  static_assert(4 * TM * kRow <= 2 * kABytes + 8 * kWBytes && (NC == 4 || NC == 2), "");
+  lds_barrier();  // other waves still read A's rows
+  uint8_t* const s_c = s_buf + wave * (TM * kRow);
+  auto slot = [&](int c, int row) { return (c ^ (NC == 4 ? row & 15 : row >> 1 & 7)) << 4; };
 #pragma unroll
   for (int m = 0; m < TT; ++m) {
-    const int r = 32 * m + r32;
-    if (r >= rows) continue;
-    const bool some = int4_source(p, row0 + r) >= 0;
-    uint16_t* c = p.c + static_cast<int64_t>(row0 + r) * out_n;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
 #pragma unroll
@@ -481,17 +547,22 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
           o[k] = acc[n][m][4 * v + k];
           if constexpr (GATED) o[k] = int4_gated(p.act, o[k], acc[n + NC][m][4 * v + k], p.limit);
         }
-        uint2 bits = pack_bf16x4(o);
-        if (!some) bits = uint2{0, 0};
-        const int col = n0 + 32 * n + 8 * v + 4 * h;
-        if (p.vector_out) {
-          if (col < out_n) *reinterpret_cast<uint2*>(c + col) = bits;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (col + k < out_n) c[col + k] = static_cast<uint16_t>((k < 2 ? bits.x : bits.y) >> (16 * (k & 1)));
-        }
+        *reinterpret_cast<uint2*>(s_c + (32 * m + r32) * kRow + slot(4 * n + v, r32) + 8 * h) = pack_bf16x4(o);
       }
+    }
+  }
+  const int c = lane % kChunks, col = n0 + 8 * c;
+  for (int r = lane / kChunks; r < rows; r += 64 / kChunks) {
+    uint4 bits = *reinterpret_cast<const uint4*>(s_c + r * kRow + slot(c, r));
+    if (!s_some[r]) bits = uint4{0, 0, 0, 0};
+    uint16_t* to = p.c + static_cast<int64_t>(row0 + r) * out_n + col;
+    if (p.vector_out) {
+      if (col < out_n) *reinterpret_cast<uint4*>(to) = bits;
+    } else {
+      const uint32_t u[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (col + k < out_n) to[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k & 1)));
     }
   }
 }
@@ -523,7 +594,7 @@ hipError_t tiled_launch(const Int4GemmArgs& p, hipStream_t stream) {
 template <int G, bool GATED>
 hipError_t gemm_launch(Int4GemmArgs p, hipStream_t stream) {
   const int out_n = GATED ? p.n / 2 : p.n;
-  p.vector_out = out_n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 7) == 0;
+  p.vector_out = out_n % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
   if (p.max_rows_per_expert <= kInt4FewRows) {
     p.few = INT32_MAX;  // whatever the counts say
     if (p.max_rows_per_expert <= 16) return stream_launch<G, 1, GATED>(p, stream);

@@ -245,7 +245,7 @@ struct Int4GemmArgs {
   float limit;
   uint16_t* c;               // [row_cap, n], gated [row_cap, n/2]
   int few = 0;               // set by the launcher: rows of an expert that streams
-  int vector_out = 0;        // set by the launcher: four columns of c at once
+  int vector_out = 0;        // set by the launcher: eight columns of c at once
 };
 // Experts of at most this many rows have their weights streamed, exact; more
 // rows multiply weights rounded to BF16.
