@@ -14,181 +14,302 @@
 namespace moe {
 namespace {
 
-constexpr int kI4Threads = 256;
-constexpr int kI4Waves = kI4Threads / 64;
+// f(integral_constant 0), .., f(integral_constant N - 1).
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_seq(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_seq(f, std::make_integer_sequence<int, N>{});
+}
 
-// The expert and the token tile of work unit u: units are the 16 MT-row tiles of
-// the experts in order. False if there are fewer.
-template <int TM>
-__device__ __forceinline__ bool int4_unit(const Int4GemmArgs& p, int u, int* expert, int* row0, int* rows) {
-  if (!p.counts) {
-    *expert = 0;
-    *row0 = u * TM;
-    *rows = min(TM, p.row_cap - *row0);
-    return *rows > 0;
-  }
-  // Each wave scans the experts 64 at a time.
+// The expert and the row tile of work unit u, units being the TM-row tiles, in
+// order, of the experts that have rows and `many` more than p.few (or not). Every
+// wave scans the counts, 256 experts at a time; *total: the units of them all, if
+// asked for.
+struct Int4Unit {
+  int expert, row0, rows;  // first row and rows of the tile
+};
+__device__ __forceinline__ int int4_tiles(const Int4GemmArgs& p, int e, int tm, bool many) {
+  const int c = e < p.num_experts ? min(p.counts[e], p.row_cap) : 0;
+  return c > 0 && (c > p.few) == many ? (c + tm - 1) / tm : 0;
+}
+template <int TM, bool MANY>
+__device__ __forceinline__ int64_t int4_units(const Int4GemmArgs& p) {
+  if (!p.counts) return (p.row_cap + TM - 1) / TM;
   const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
-    const int e = e0 + lane;
-    const int c = e < p.num_experts ? int4_rows(p, e) : 0;
-    const int tiles = c <= p.few ? (c + TM - 1) / TM : 0;
-    int incl = tiles;
+  int64_t units = 0;
+  for (int e0 = 0; e0 < p.num_experts; e0 += 256) {
+    int c = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
+    for (int i = 0; i < 4; ++i) c += int4_tiles(p, e0 + 64 * i + lane, TM, MANY);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d, 64);
+    units += c;
+  }
+  return units;
+}
+template <int TM, bool MANY>
+__device__ __forceinline__ bool int4_unit(const Int4GemmArgs& p, int64_t u, Int4Unit* t) {
+  if (!p.counts) {
+    if (u * TM >= p.row_cap) return false;
+    t->expert = 0;
+    t->row0 = static_cast<int>(u) * TM;
+    t->rows = min(TM, p.row_cap - t->row0);
+    return true;
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int e0 = 0; e0 < p.num_experts; e0 += 256) {
+    int tiles[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tiles[i] = int4_tiles(p, e0 + 64 * i + lane, TM, MANY);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int incl = tiles[i];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += v;
+      }
+      const int all = __builtin_amdgcn_readlane(incl, 63);
+      if (u < before + all) {
+        const int l = __builtin_ctzll(__ballot(before + incl > u));
+        const int first = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles[i], l);
+        const int e = e0 + 64 * i + l, at = static_cast<int>(u - before - first) * TM;
+        t->expert = e;
+        t->row0 = int4_seg_start(p, e) + at;
+        t->rows = min(TM, int4_rows(p, e) - at);
+        return t->rows > 0;
+      }
+      before += all;
     }
-    const int all = __shfl(incl, 63, 64);
-    if (u < before + all) {
-      const uint64_t past = __ballot(before + incl > u);
-      const int l = __builtin_ctzll(past);
-      const int tile = u - before - (__shfl(incl, l, 64) - __shfl(tiles, l, 64));
-      *expert = e0 + l;
-      *row0 = tile * TM;
-      *rows = min(TM, __shfl(c, l, 64) - *row0);
-      return true;
-    }
-    before += all;
   }
   return false;
 }
 
-// R weight tiles of 16 rows (gated: tile 0 gate rows, tile 1 the up rows of the
-// same columns), MT row tiles of A; the waves share K.
-template <int G, int MT, bool GATED>
-__global__ __launch_bounds__(kI4Threads) void int4_stream_kernel(Int4GemmArgs p) {
-  constexpr int R = 2;
-  __shared__ v4f s_sum[kI4Waves][R][MT][64];
+// ---- few rows per expert: weights streamed, exact -------------------------------
+//
+// A wave streams 16 R weight rows over its share of K straight into operands of
+// 16x16x32 MFMAs, D blocks of 128 K values ahead (their loads, in order, hide
+// each other's latency); the rows of A of a block pass through LDS of the wave's
+// own, which turns whole-line loads into operands and needs no barrier. The waves
+// of a workgroup share K and add up their sums at the end.
+//
+// Groups of fewer than 128 columns: a lane's 16 bytes are 32 columns of one
+// group, but an instruction's 32 K values have to be of one group in every lane,
+// so the wave's four rows of lanes swap words (row_transpose), and their scales
+// likewise: row g loads group g's, and all get every group's.
+
+// XL: row tiles of four rows of A. R: weight tiles of 16 rows (gated: the second
+// half up rows of the first half's columns). W: waves.
+template <int G, int XL, int R, int D, int W, bool GATED>
+__device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t* lds, const Int4Unit& t,
+                                                 int tile) {
+  constexpr int MT = (XL + 3) / 4, NC = GATED ? R / 2 : R;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int out_n = GATED ? p.n / 2 : p.n;
-  const int col_tiles = (out_n + (GATED ? 16 : 16 * R) - 1) / (GATED ? 16 : 16 * R);
-  const int64_t task = flat_block();
-  const int unit = static_cast<int>(task / col_tiles), tile = static_cast<int>(task % col_tiles);
-  int expert, row0, rows;
-  if (!int4_unit<16 * MT>(p, unit, &expert, &row0, &rows)) return;
-  expert = __builtin_amdgcn_readfirstlane(expert);
-  row0 = __builtin_amdgcn_readfirstlane(row0) + int4_seg_start(p, expert);
-  rows = __builtin_amdgcn_readfirstlane(rows);
-  const int K = p.k, groups = K / G;
+  const int K = p.k, out_n = GATED ? p.n / 2 : p.n, groups = K / G;
+  const int blocks = (K + 127) / 128;
+  const int b0 = static_cast<int>(static_cast<unsigned>(blocks * wave) / W);
+  const int b1 = static_cast<int>(static_cast<unsigned>(blocks * (wave + 1)) / W);
+  uint8_t* const s_x = lds + wave * (MT * 4096);
 
-  // Lanes past the last weight row take the last one's place.
-  int wrow[R];
+  // Weight rows past the last take its place.
+  const uint8_t* wb = p.w + static_cast<int64_t>(t.expert) * p.n * (K / 2);
+  const uint16_t* sb = p.scales + static_cast<int64_t>(t.expert) * p.n * groups;
+  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(t.expert) * p.n * groups : nullptr;
+  uint32_t wo[R], so[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = min((GATED ? tile : tile * R + r) * 16 + col, out_n - 1);
-    wrow[r] = GATED && r ? c + out_n : c;
+    const int c = min(16 * (NC * tile + r % NC) + col, out_n - 1) + (GATED && r >= NC ? out_n : 0);
+    wo[r] = static_cast<uint32_t>(c) * static_cast<uint32_t>(K / 2);
+    so[r] = static_cast<uint32_t>(c) * static_cast<uint32_t>(groups);
   }
-  const uint8_t* w[R];
-  const uint16_t* sc[R];
-  const uint8_t* zr[R];
+  // Rows of A: load i covers rows 4 i .. + 3, 256 bytes of each. Rows without a
+  // source load one that exists; their output is zero.
+  const int live = (t.rows + 3) >> 2;
+  uint32_t ao[XL];  // in units of 64 bytes, of which a row is a multiple
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t at = static_cast<int64_t>(expert) * p.n + wrow[r];
-    w[r] = p.w + at * (K / 2);
-    sc[r] = p.scales + at * groups;
-    zr[r] = p.zeros ? p.zeros + at * groups : nullptr;
+  for (int i = 0; i < XL; ++i) {
+    const int r = 4 * i + g;
+    ao[i] = 0;
+    if (r < t.rows) ao[i] = static_cast<uint32_t>(max(int4_source(p, t.row0 + r), 0)) * static_cast<uint32_t>(K / 32);
   }
-  const uint16_t* a[MT];
+
+  // Past K loads are of the row's start, and the scale is zero.
+  u32x4 w[D][R], x[D][XL];
+  uint32_t sc[D][R], zr[D][R];
+  auto load = [&](auto d, int b) __attribute__((always_inline)) {
+    const int k = 128 * min(b, b1 - 1);
+    const uint32_t wk = k + 32 * g < K ? k / 2 + 16 * g : 0;
+    const uint8_t* xa = reinterpret_cast<const uint8_t*>(p.a) + (k + 8 * col < K ? 2 * k + 16 * col : 0);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = 16 * m + col;
-    const int src = t < rows ? int4_source(p, row0 + t) : -1;
-    a[m] = src < 0 ? nullptr : p.a + static_cast<int64_t>(src) * K;
-  }
+    for (int i = 0; i < XL; ++i)
+      if (i < live) x[d][i] = *reinterpret_cast<const u32x4*>(xa + (static_cast<uint64_t>(ao[i]) << 6));
+    const int gr = min((G < 128 ? k + 32 * g : k) / G, groups - 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[d][r] = *reinterpret_cast<const u32x4*>(wb + (wo[r] + wk));
+      sc[d][r] = sb[so[r] + gr];
+      if (zb) zr[d][r] = zb[so[r] + gr];
+    }
+  };
 
   const v4f zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
   const uint4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  v4f total[R][MT], acc[R][MT], sum[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    sum[m] = zero4;
-#pragma unroll
-    for (int r = 0; r < R; ++r) total[r][m] = acc[r][m] = zero4;
-  }
-
-  const int blocks = (K + 127) / 128;
-  const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (wave + 1) / kI4Waves);
-  for (int b = static_cast<int>(static_cast<int64_t>(blocks) * wave / kI4Waves); b < b1; ++b) {
-    uint4 c[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      c[r] = uint4{0, 0, 0, 0};
-      if (128 * b + 32 * g < K) c[r] = *reinterpret_cast<const uint4*>(w[r] + 64 * b + 16 * g);
-      // Groups of fewer than 128 columns: word j of every lane within columns 32 j .. + 31.
-      if constexpr (G < 128) c[r] = row_transpose(c[r]);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = G < 128 ? 128 * b + 32 * j + 8 * g : 128 * b + 32 * g + 8 * j;
-      uint4 x[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        x[m] = uint4{0, 0, 0, 0};
-        if (a[m] && k < K) x[m] = *reinterpret_cast<const uint4*>(a[m] + k);
-        x[m] = int4_order(x[m]);
-        sum[m] = mfma_bf16(x[m], ones, sum[m]);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const uint4 q = int4_operand(j == 0 ? c[r].x : j == 1 ? c[r].y : j == 2 ? c[r].z : c[r].w);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[r][m] = mfma_bf16(x[m], q, acc[r][m]);
-      }
-      if ((32 * (j + 1)) % G == 0) {
-        const int at = min((128 * b + 32 * j) / G, groups - 1);  // past K: sums of zeros
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float s = int4_scale(sc[r][at], p.scale_f16);
-          const float off = 16.0f + (zr[r] ? static_cast<float>(zr[r][at]) : 8.0f);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              total[r][m][v] = __builtin_fmaf(s, __builtin_fmaf(-off, sum[m][v], acc[r][m][v]), total[r][m][v]);
-            acc[r][m] = zero4;
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) sum[m] = zero4;
-      }
-    }
-  }
-
+  v4f total[R][MT];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) s_sum[wave][r][m][lane] = total[r][m];
+    for (int m = 0; m < MT; ++m) total[r][m] = zero4;
+
+  auto block = [&](auto d, int b) __attribute__((always_inline)) {
+    // Row 4 i + g, chunk col in slot col ^ row % 16: reads of a chunk of 16 rows
+    // meet no bank twice.
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      if (i < live)
+        *reinterpret_cast<uint4*>(s_x + 1024 * i + 256 * g + ((col ^ ((4 * i + g) & 15)) << 4)) =
+            int4_order(__builtin_bit_cast(uint4, x[d][i]));
+    uint4 q[R];
+    float s[R][4], off[R][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      q[r] = __builtin_bit_cast(uint4, w[d][r]);
+      const float sv = G == 128 || 128 * b + 32 * g < K ? int4_scale(sc[d][r], p.scale_f16) : 0.0f;
+      if constexpr (G == 128) {
+        s[r][3] = sv;
+        off[r][3] = 16.0f + (zb ? static_cast<float>(zr[d][r]) : 8.0f);
+      } else {
+        q[r] = row_transpose(q[r]);
+        const uint32_t v = __float_as_uint(sv);
+        const uint4 a = row_transpose(uint4{v, v, v, v});
+        s[r][0] = __uint_as_float(a.x);
+        s[r][1] = __uint_as_float(a.y);
+        s[r][2] = __uint_as_float(a.z);
+        s[r][3] = __uint_as_float(a.w);
+        if (zb) {
+          const uint32_t o = __float_as_uint(16.0f + static_cast<float>(zr[d][r]));
+          const uint4 z = row_transpose(uint4{o, o, o, o});
+          off[r][0] = __uint_as_float(z.x);
+          off[r][1] = __uint_as_float(z.y);
+          off[r][2] = __uint_as_float(z.z);
+          off[r][3] = __uint_as_float(z.w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) off[r][j] = 24.0f;
+        }
+      }
+    }
+    // (the loads' registers are free)
+    load(d, b + D);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (MT > 1 && 4 * m >= live) break;
+      v4f acc[R], sum = zero4;
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[r] = zero4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = G == 128 ? 4 * g + j : 4 * j + g;
+        const uint4 f = *reinterpret_cast<const uint4*>(s_x + 4096 * m + 256 * col + ((c ^ col) << 4));
+        sum = mfma_bf16(f, ones, sum);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          acc[r] = mfma_bf16(f, int4_operand(j == 0 ? q[r].x : j == 1 ? q[r].y : j == 2 ? q[r].z : q[r].w), acc[r]);
+        if ((32 * (j + 1)) % G == 0) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              total[r][m][v] = __builtin_fmaf(s[r][j], __builtin_fmaf(-off[r][j], sum[v], acc[r][v]), total[r][m][v]);
+            acc[r] = zero4;
+          }
+          sum = zero4;
+        }
+      }
+    }
+  };
+  if (b0 < b1) {
+    static_for<D>([&](auto d) __attribute__((always_inline)) { load(d, b0 + d); });
+    for (int b = b0; b < b1; b += D)
+      static_for<D>([&](auto d) __attribute__((always_inline)) {
+        if (b + d < b1) block(d, b + d);
+      });
+  }
+
+  v4f* const s_sum = reinterpret_cast<v4f*>(lds);  // [W][R][MT][64]
+  __syncthreads();                                 // the rows of A are read
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (MT == 1 || 4 * m < live) s_sum[((wave * R + r) * MT + m) * 64 + lane] = total[r][m];
   __syncthreads();
-  // A wave finishes the tiles (r, m) of its number; gated, both of a pair.
-  for (int i = wave; i < (GATED ? MT : R * MT); i += kI4Waves) {
-    const int m = i % MT, r = i / MT;
-    v4f v = s_sum[0][r][m][lane], u = zero4;
+  // A wave finishes the tiles (c, m) of its number; gated, both of a pair.
+  for (int i = wave; i < NC * MT; i += W) {
+    const int m = i % MT, c = i / MT;
+    if (MT > 1 && 4 * m >= live) continue;
+    v4f v = zero4, u = zero4;
 #pragma unroll
-    for (int k = 1; k < kI4Waves; ++k) v += s_sum[k][r][m][lane];
+    for (int k = 0; k < W; ++k) v += s_sum[((k * R + c) * MT + m) * 64 + lane];
     if constexpr (GATED) {
-      u = s_sum[0][1][m][lane];
 #pragma unroll
-      for (int k = 1; k < kI4Waves; ++k) u += s_sum[k][1][m][lane];
+      for (int k = 0; k < W; ++k) u += s_sum[((k * R + NC + c) * MT + m) * 64 + lane];
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = int4_gated(p.act, v[k], u[k], p.limit);
     }
-    const int n = (GATED ? tile : tile * R + r) * 16 + col;
+    const int n = 16 * (NC * tile + c) + col;
     const uint2 bits = pack_bf16x4(v);
     if (n < out_n) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int t = 16 * m + 4 * g + k;
-        const uint32_t b = k < 2 ? bits.x : bits.y;
-        if (t < rows)
-          p.c[static_cast<int64_t>(row0 + t) * out_n + n] = static_cast<uint16_t>(k & 1 ? b >> 16 : b);
+        const int r = 16 * m + 4 * g + k;
+        const uint32_t o = k < 2 ? bits.x : bits.y;
+        if (r < t.rows)
+          p.c[static_cast<int64_t>(t.row0 + r) * out_n + n] =
+              int4_source(p, t.row0 + r) < 0 ? 0 : static_cast<uint16_t>(k & 1 ? o >> 16 : o);
       }
     }
   }
 }
 
+// XL: of the launch's largest tiles; a tile with fewer rows takes a smaller form.
+// Workgroups stay and take tiles in turn: how many there are only the device knows.
+template <int G, int XL, int R, int D, int W, bool GATED>
+__global__ __launch_bounds__(64 * W, 1) void int4_stream_kernel(Int4GemmArgs p) {
+  constexpr int MT = (XL + 3) / 4;
+  constexpr int kX = W * MT * 4096, kSum = W * R * MT * 1024;
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kX > kSum ? kX : kSum];
+  const int out_n = GATED ? p.n / 2 : p.n, cols = GATED ? 8 * R : 16 * R;
+  const unsigned col_tiles = static_cast<unsigned>(out_n + cols - 1) / cols;
+  const int64_t total = int4_units<4 * XL, false>(p) * col_tiles;
+  for (int64_t task = blockIdx.x; task < total; task += gridDim.x) {
+    int64_t u;
+    int tile;
+    if (task < INT32_MAX) {  // (a 64-bit division is long)
+      u = static_cast<unsigned>(task) / col_tiles;
+      tile = static_cast<unsigned>(task) % col_tiles;
+    } else {
+      u = task / col_tiles;
+      tile = static_cast<int>(task % col_tiles);
+    }
+    Int4Unit t;
+    if (!int4_unit<4 * XL, false>(p, u, &t)) continue;
+    t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+    t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+    t.rows = __builtin_amdgcn_readfirstlane(t.rows);
+    if (XL > 4 && t.rows <= 4)
+      int4_stream_tile<G, 1, R, 4, W, GATED>(p, lds, t, tile);
+    else if (XL > 4 && t.rows <= 16)
+      int4_stream_tile<G, 4, R, 3, W, GATED>(p, lds, t, tile);
+    else
+      int4_stream_tile<G, XL, R, D, W, GATED>(p, lds, t, tile);
+    __syncthreads();  // the sums are read
+  }
+}
 
 // ---- many rows per expert: tiles of BF16 rows through LDS ---------------------
 //
@@ -215,16 +336,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
 constexpr int kTlThreads = 256;
-
-// f(integral_constant 0), .., f(integral_constant N - 1).
-template <typename F, int... I>
-__device__ __forceinline__ void static_for_seq(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_seq(f, std::make_integer_sequence<int, N>{});
-}
 
 __device__ __forceinline__ v16f mfma_bf16_32(uint4 a, uint4 b, v16f acc) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
@@ -273,56 +384,36 @@ __device__ __forceinline__ void int4_unpack(Int4Unpack& u, uint32_t c, float s9,
 // Tile of this workgroup: workgroups go round-robin over the 8 XCDs; an XCD
 // takes consecutive tiles, an expert's row tiles of one column tile first, so
 // that its L2 serves their weights and the rows' next column tiles.
-struct Int4Tile {
-  int expert, row0, rows, col_tile;
-};
 template <int TM>
-__device__ __forceinline__ bool int4_tile(const Int4GemmArgs& p, int col_tiles, Int4Tile* t) {
-  const int lane = threadIdx.x & 63;
-  int64_t units = 0;
-  if (!p.counts) {
-    units = (p.row_cap + TM - 1) / TM;
-  } else {
-    for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
-      const int e = e0 + lane;
-      int c = e < p.num_experts ? int4_rows(p, e) : 0;
-      c = c > p.few ? (c + TM - 1) / TM : 0;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d, 64);
-      units += c;
-    }
-  }
-  const int64_t total = units * col_tiles, per = (total + 7) / 8;
+__device__ __forceinline__ bool int4_tile(const Int4GemmArgs& p, int col_tiles, Int4Unit* t, int* tile) {
+  const int64_t units = int4_units<TM, true>(p), total = units * col_tiles, per = (total + 7) / 8;
   const int64_t id = flat_block(), at = (id & 7) * per + (id >> 3);
   if ((id >> 3) >= per || at >= total) return false;
+  // Tiles in order of expert, then column tile, then row tile.
   if (!p.counts) {
-    t->expert = 0;
-    t->row0 = static_cast<int>(at % units) * TM;
-    t->rows = min(TM, p.row_cap - t->row0);
-    t->col_tile = static_cast<int>(at / units);
-    return true;
+    *tile = static_cast<int>(at / units);
+    return int4_unit<TM, true>(p, at % units, t);
   }
+  const int lane = threadIdx.x & 63;
   int64_t before = 0;
   for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
-    const int e = e0 + lane;
-    const int c = e < p.num_experts ? int4_rows(p, e) : 0;
-    const int tiles = c > p.few ? (c + TM - 1) / TM : 0;
+    const int tiles = int4_tiles(p, e0 + lane, TM, true);
     int incl = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int v = __shfl_up(incl, d, 64);
       if (lane >= d) incl += v;
     }
-    const int all = __shfl(incl, 63, 64);
+    const int all = __builtin_amdgcn_readlane(incl, 63);
     if (at < (before + all) * col_tiles) {
       const int l = __builtin_ctzll(__ballot((before + incl) * col_tiles > at));
-      const int mine = __shfl(tiles, l, 64), rows = __shfl(c, l, 64);
-      const int local = static_cast<int>(at - (before + __shfl(incl, l, 64) - mine) * col_tiles);
-      t->expert = e0 + l;
-      t->row0 = local % mine * TM;
-      t->rows = min(TM, rows - t->row0);
-      t->col_tile = local / mine;
-      return true;
+      const int mine = __builtin_amdgcn_readlane(tiles, l), e = e0 + l;
+      const int local = static_cast<int>(at - (before + __builtin_amdgcn_readlane(incl, l) - mine) * col_tiles);
+      *tile = local / mine;
+      t->expert = e;
+      t->row0 = int4_seg_start(p, e) + local % mine * TM;
+      t->rows = min(TM, int4_rows(p, e) - local % mine * TM);
+      return t->rows > 0;
     }
     before += all;
   }
@@ -344,11 +435,12 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   uint8_t* const s_w = s_buf + 2 * kABytes + wave * (2 * kWBytes);
   const int r32 = lane & 31, h = lane >> 5;
   const int K = p.k, out_n = GATED ? p.n / 2 : p.n, groups = K / G;
-  Int4Tile t;
-  if (!int4_tile<TM>(p, (out_n + 128 * NC - 1) / (128 * NC), &t)) return;
+  Int4Unit t;
+  int tile;
+  if (!int4_tile<TM>(p, (out_n + 128 * NC - 1) / (128 * NC), &t, &tile)) return;
   const int expert = __builtin_amdgcn_readfirstlane(t.expert), rows = __builtin_amdgcn_readfirstlane(t.rows);
-  const int row0 = __builtin_amdgcn_readfirstlane(t.row0) + int4_seg_start(p, expert);
-  const int n0 = __builtin_amdgcn_readfirstlane(t.col_tile) * 128 * NC + wave * 32 * NC;
+  const int row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  const int n0 = __builtin_amdgcn_readfirstlane(tile) * 128 * NC + wave * 32 * NC;
   const int blocks = (K + 255) / 256;
 
   // Rows of A: thread tid loads chunk tid % 16 of row tid / 16 + 16 i. Rows
@@ -567,16 +659,25 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   }
 }
 
-template <int G, int MT, bool GATED>
+template <int G, int XL, int R, int D, int W, bool GATED>
 hipError_t stream_launch(const Int4GemmArgs& p, hipStream_t stream) {
-  constexpr int TM = 16 * MT;
-  const int out_n = GATED ? p.n / 2 : p.n, cols = GATED ? 16 : 32;
+  constexpr int TM = 4 * XL;
+  const int out_n = GATED ? p.n / 2 : p.n, cols = GATED ? 8 * R : 16 * R;
   // Every tile but an expert's last is full.
   const int64_t used = p.num_experts < p.row_cap ? p.num_experts : p.row_cap;
   const int64_t units = p.counts ? p.row_cap / TM + used : (p.row_cap + TM - 1) / TM;
-  const int64_t tasks = (out_n + cols - 1) / cols * units;
-  hipLaunchKernelGGL((int4_stream_kernel<G, MT, GATED>), flat_grid(tasks), dim3(kI4Threads), 0, stream, p);
+  const int64_t tasks = (out_n + cols - 1) / cols * units, cap = 2 * static_cast<int64_t>(device_cu_count());
+  hipLaunchKernelGGL((int4_stream_kernel<G, XL, R, D, W, GATED>), dim3(static_cast<unsigned>(tasks < cap ? tasks : cap)),
+                     dim3(64 * W), 0, stream, p);
   return hipGetLastError();
+}
+
+template <int G, bool GATED>
+hipError_t stream_rows(const Int4GemmArgs& p, int bound, hipStream_t stream) {
+  if (bound <= 4) return stream_launch<G, 1, 2, 4, 8, GATED>(p, stream);
+  if (bound <= 16) return stream_launch<G, 4, 2, 3, 8, GATED>(p, stream);
+  if (bound <= 32) return stream_launch<G, 8, 4, 2, 4, GATED>(p, stream);
+  return stream_launch<G, 16, 4, 1, 4, GATED>(p, stream);
 }
 
 template <int G, int TT, int NT, bool GATED>
@@ -597,13 +698,11 @@ hipError_t gemm_launch(Int4GemmArgs p, hipStream_t stream) {
   p.vector_out = out_n % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
   if (p.max_rows_per_expert <= kInt4FewRows) {
     p.few = INT32_MAX;  // whatever the counts say
-    if (p.max_rows_per_expert <= 16) return stream_launch<G, 1, GATED>(p, stream);
-    if (p.max_rows_per_expert <= 32) return stream_launch<G, 2, GATED>(p, stream);
-    return stream_launch<G, 4, GATED>(p, stream);
+    return stream_rows<G, GATED>(p, p.max_rows_per_expert, stream);
   }
   p.few = kInt4FewRows;
   if (p.counts) {
-    const hipError_t e = stream_launch<G, 4, GATED>(p, stream);
+    const hipError_t e = stream_rows<G, GATED>(p, kInt4FewRows, stream);
     if (e != hipSuccess) return e;
   }
   return tiled_launch<G, 4, 4, GATED>(p, stream);
