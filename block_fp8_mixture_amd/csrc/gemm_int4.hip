@@ -7,6 +7,7 @@
 // holds row l % 16 and the K values 8 (l / 16) .. + 7) and weight rows as its
 // second (alike); lane l of the result holds weight row l % 16 and rows of A
 // 4 (l / 16) + v, so a lane needs one row's scales.
+#include <cstdlib>
 #include <utility>
 
 #include "int4_device.h"
@@ -24,106 +25,129 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_seq(f, std::make_integer_sequence<int, N>{});
 }
 
-// The expert and the row tile of work unit u, units being the TM-row tiles, in
-// order, of the experts that have rows and `many` more than p.few (or not). Every
-// wave scans the counts, 256 experts at a time; *total: the units of them all, if
-// asked for.
+// Inclusive sum over the lanes up to each.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);  // lane 15 of the row before
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);  // lane 31
+}
+
+// Units of work are the TM-row tiles, in order, of the experts with more than
+// p.rows_over rows and not more than p.rows_to. Every wave scans the counts.
 struct Int4Unit {
-  int expert, row0, rows;  // first row and rows of the tile
+  int expert, row0, rows;  // first row and rows of the tile; no rows: not a segment
+  int tiles, first;        // units of the expert, and its first one's number
 };
-__device__ __forceinline__ int int4_tiles(const Int4GemmArgs& p, int e, int tm, bool many) {
+constexpr int kScan = 8;  // experts of a lane at once: their loads wait for one another's only
+__device__ __forceinline__ int int4_tiles(const Int4GemmArgs& p, int e, int tm) {
   const int c = e < p.num_experts ? min(p.counts[e], p.row_cap) : 0;
-  return c > 0 && (c > p.few) == many ? (c + tm - 1) / tm : 0;
+  return c > p.rows_over && c <= p.rows_to ? (c + tm - 1) / tm : 0;
 }
-template <int TM, bool MANY>
-__device__ __forceinline__ int64_t int4_units(const Int4GemmArgs& p) {
-  if (!p.counts) return (p.row_cap + TM - 1) / TM;
-  const int lane = threadIdx.x & 63;
-  int64_t units = 0;
-  for (int e0 = 0; e0 < p.num_experts; e0 += 256) {
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c += int4_tiles(p, e0 + 64 * i + lane, TM, MANY);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) c += __shfl_xor(c, d, 64);
-    units += c;
-  }
-  return units;
-}
-template <int TM, bool MANY>
-__device__ __forceinline__ bool int4_unit(const Int4GemmArgs& p, int64_t u, Int4Unit* t) {
+// Unit u; false past the last. *more: whether there may be one `step` on.
+template <int TM>
+__device__ __forceinline__ bool int4_find(const Int4GemmArgs& p, int u, int step, Int4Unit* t, bool* more) {
   if (!p.counts) {
-    if (u * TM >= p.row_cap) return false;
-    t->expert = 0;
-    t->row0 = static_cast<int>(u) * TM;
-    t->rows = min(TM, p.row_cap - t->row0);
-    return true;
+    t->tiles = (p.row_cap + TM - 1) / TM;
+    t->first = t->expert = 0;
+    t->row0 = u * TM;
+    t->rows = min(TM, p.row_cap - u * TM);
+    *more = u + step < t->tiles;
+    return u < t->tiles;
   }
   const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  for (int e0 = 0; e0 < p.num_experts; e0 += 256) {
-    int tiles[4];
+  int before = 0;
+  for (int e0 = 0; e0 < p.num_experts; e0 += 64 * kScan) {
+    int tiles[kScan], found = -1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tiles[i] = int4_tiles(p, e0 + 64 * i + lane, TM, MANY);
+    for (int i = 0; i < kScan; ++i) tiles[i] = int4_tiles(p, e0 + 64 * i + lane, TM);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int incl = tiles[i];
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += v;
-      }
+    for (int i = 0; i < kScan; ++i) {
+      const int incl = wave_scan(tiles[i]);
       const int all = __builtin_amdgcn_readlane(incl, 63);
-      if (u < before + all) {
+      if (u >= before && u < before + all) {
         const int l = __builtin_ctzll(__ballot(before + incl > u));
-        const int first = __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles[i], l);
-        const int e = e0 + 64 * i + l, at = static_cast<int>(u - before - first) * TM;
-        t->expert = e;
-        t->row0 = int4_seg_start(p, e) + at;
-        t->rows = min(TM, int4_rows(p, e) - at);
-        return t->rows > 0;
+        t->tiles = __builtin_amdgcn_readlane(tiles[i], l);
+        t->first = before + __builtin_amdgcn_readlane(incl, l) - t->tiles;
+        found = e0 + 64 * i + l;
       }
       before += all;
+    }
+    if (found >= 0) {
+      const int at = (u - t->first) * TM;
+      t->expert = found;
+      t->row0 = int4_seg_start(p, found) + at;
+      t->rows = min(TM, int4_rows(p, found) - at);
+      *more = u + step < before || e0 + 64 * kScan < p.num_experts;
+      return true;
     }
   }
   return false;
 }
+// Their number.
+template <int TM>
+__device__ __forceinline__ int int4_units(const Int4GemmArgs& p) {
+  if (!p.counts) return (p.row_cap + TM - 1) / TM;
+  const int lane = threadIdx.x & 63;
+  int units = 0;
+  for (int e0 = 0; e0 < p.num_experts; e0 += 64 * kScan) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) c += int4_tiles(p, e0 + 64 * i + lane, TM);
+    units += __builtin_amdgcn_readlane(wave_scan(c), 63);
+  }
+  return units;
+}
 
 // ---- few rows per expert: weights streamed, exact -------------------------------
 //
-// A wave streams 16 R weight rows over its share of K straight into operands of
-// 16x16x32 MFMAs, D blocks of 128 K values ahead (their loads, in order, hide
-// each other's latency); the rows of A of a block pass through LDS of the wave's
-// own, which turns whole-line loads into operands and needs no barrier. The waves
-// of a workgroup share K and add up their sums at the end.
+// A wave streams 16 R weight rows over its share of K into operands of 16x16x32
+// MFMAs, blocks of 128 K values, the next asked for while one is computed. Both
+// operands pass through LDS of the wave's own, without a barrier: a load takes 64
+// or 256 consecutive bytes of a row, four lanes to a line (with a lane per row, as
+// the operands have it, the address path handles a line per lane, and 1 token of
+// 4096 -> 4096 took 10 us with the weights in L2). The waves of a workgroup share K and
+// add up their sums at the end: many waves of few blocks rather than few waves
+// with many loads in flight, because a launch of a few microseconds also feels
+// how long its code takes to arrive.
 //
-// Groups of fewer than 128 columns: a lane's 16 bytes are 32 columns of one
-// group, but an instruction's 32 K values have to be of one group in every lane,
-// so the wave's four rows of lanes swap words (row_transpose), and their scales
-// likewise: row g loads group g's, and all get every group's.
+// Groups of fewer than 128 columns: an instruction's 32 K values have to be of one
+// group in every lane, so a lane reads word g of each 16 bytes of a row, else
+// 16 bytes of its own.
 
 // XL: row tiles of four rows of A. R: weight tiles of 16 rows (gated: the second
-// half up rows of the first half's columns). W: waves.
-template <int G, int XL, int R, int D, int W, bool GATED>
-__device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t* lds, const Int4Unit& t,
-                                                 int tile) {
-  constexpr int MT = (XL + 3) / 4, NC = GATED ? R / 2 : R;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// half up rows of the first half's columns; a single tile 8 rows of each). W: waves.
+template <int G, int XL, int R, int W, bool GATED>
+__device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t* lds, const Int4Unit& t) {
+  constexpr int MT = (XL + 3) / 4;
+  constexpr int NC = GATED && R > 1 ? R / 2 : R;      // tiles that hold the output's columns
+  constexpr int C = GATED ? 8 * R : 16 * R;           // these
+  constexpr int D = XL > 1 ? 1 : 2;                   // blocks ahead
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int K = p.k, out_n = GATED ? p.n / 2 : p.n, groups = K / G;
   const int blocks = (K + 127) / 128;
   const int b0 = static_cast<int>(static_cast<unsigned>(blocks * wave) / W);
   const int b1 = static_cast<int>(static_cast<unsigned>(blocks * (wave + 1)) / W);
-  uint8_t* const s_x = lds + wave * (MT * 4096);
+  uint8_t* const s_x = lds + wave * ((XL + R) * 1024);
+  uint8_t* const s_w = s_x + XL * 1024;
 
-  // Weight rows past the last take its place.
+  // Lane l loads chunk l % 4 (of 16 bytes) of row l / 4 of a tile's block, into
+  // slot l % 4: chunk c of row r is in slot c ^ r / 4 % 4, so that reads of a chunk
+  // of 16 rows meet no bank twice; and the scale of group l % 4 of it. Weight rows
+  // past the last take its place.
   const uint8_t* wb = p.w + static_cast<int64_t>(t.expert) * p.n * (K / 2);
   const uint16_t* sb = p.scales + static_cast<int64_t>(t.expert) * p.n * groups;
   const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(t.expert) * p.n * groups : nullptr;
+  const int n0 = static_cast<int>(blockIdx.x) * C, sub = lane & 3, chunk = sub ^ g;
   uint32_t wo[R], so[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = min(16 * (NC * tile + r % NC) + col, out_n - 1) + (GATED && r >= NC ? out_n : 0);
+    const int w = lane >> 2;
+    const bool up = GATED && (R > 1 ? r >= NC : w >= 8);
+    const int c = min(n0 + 16 * (r % NC) + (GATED && R == 1 ? w & 7 : w), out_n - 1) + (up ? out_n : 0);
     wo[r] = static_cast<uint32_t>(c) * static_cast<uint32_t>(K / 2);
     so[r] = static_cast<uint32_t>(c) * static_cast<uint32_t>(groups);
   }
@@ -131,30 +155,29 @@ __device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t*
   // source load one that exists; their output is zero.
   const int live = (t.rows + 3) >> 2;
   uint32_t ao[XL];  // in units of 64 bytes, of which a row is a multiple
-#pragma unroll
-  for (int i = 0; i < XL; ++i) {
-    const int r = 4 * i + g;
-    ao[i] = 0;
-    if (r < t.rows) ao[i] = static_cast<uint32_t>(max(int4_source(p, t.row0 + r), 0)) * static_cast<uint32_t>(K / 32);
-  }
 
   // Past K loads are of the row's start, and the scale is zero.
-  u32x4 w[D][R], x[D][XL];
-  uint32_t sc[D][R], zr[D][R];
-  auto load = [&](auto d, int b) __attribute__((always_inline)) {
+  struct Loaded {
+    u32x4 w[R], x[XL];
+    uint32_t sc[R], zr[R];
+  };
+  auto load_w = [&](Loaded& l, int b) __attribute__((always_inline)) {
     const int k = 128 * min(b, b1 - 1);
-    const uint32_t wk = k + 32 * g < K ? k / 2 + 16 * g : 0;
+    const uint32_t wk = k + 32 * chunk < K ? k / 2 + 16 * chunk : 0;
+    const int gr = min(k / G + sub, groups - 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l.w[r] = *reinterpret_cast<const u32x4*>(wb + (wo[r] + wk));
+      l.sc[r] = sb[so[r] + gr];
+      if (zb) l.zr[r] = zb[so[r] + gr];
+    }
+  };
+  auto load_x = [&](Loaded& l, int b) __attribute__((always_inline)) {
+    const int k = 128 * min(b, b1 - 1);
     const uint8_t* xa = reinterpret_cast<const uint8_t*>(p.a) + (k + 8 * col < K ? 2 * k + 16 * col : 0);
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      if (i < live) x[d][i] = *reinterpret_cast<const u32x4*>(xa + (static_cast<uint64_t>(ao[i]) << 6));
-    const int gr = min((G < 128 ? k + 32 * g : k) / G, groups - 1);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      w[d][r] = *reinterpret_cast<const u32x4*>(wb + (wo[r] + wk));
-      sc[d][r] = sb[so[r] + gr];
-      if (zb) zr[d][r] = zb[so[r] + gr];
-    }
+      if (i < live) l.x[i] = *reinterpret_cast<const u32x4*>(xa + (static_cast<uint64_t>(ao[i]) << 6));
   };
 
   const v4f zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -165,46 +188,48 @@ __device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t*
 #pragma unroll
     for (int m = 0; m < MT; ++m) total[r][m] = zero4;
 
-  auto block = [&](auto d, int b) __attribute__((always_inline)) {
-    // Row 4 i + g, chunk col in slot col ^ row % 16: reads of a chunk of 16 rows
-    // meet no bank twice.
+  // Row r's chunk c of 16 bytes is in slot c ^ r % 16: reads of a chunk of 16 rows
+  // meet no bank twice. A lane writes chunk col of rows 4 i + g, and reads row
+  // col's chunks 4 g + j (groups of fewer columns: 4 j + g). With four rows at most
+  // all lanes read those.
+  const int row = XL == 1 ? col & 3 : col;
+  uint32_t put = 256 * g + ((col ^ g) << 4);
+  uint32_t get = 256 * row + (((G == 128 ? 4 * g : g) ^ row) << 4);
+  const uint32_t wget = 64 * col + (((G == 128 ? g : 0) ^ (col >> 2)) << 4) + (G == 128 ? 0 : 4 * g);
+  auto block = [&](Loaded& l, int b) __attribute__((always_inline)) {
+    // Opaque: the addresses of every row would be kept in registers.
+    asm volatile("" : "+v"(put), "+v"(get));
 #pragma unroll
     for (int i = 0; i < XL; ++i)
       if (i < live)
-        *reinterpret_cast<uint4*>(s_x + 1024 * i + 256 * g + ((col ^ ((4 * i + g) & 15)) << 4)) =
-            int4_order(__builtin_bit_cast(uint4, x[d][i]));
+        *reinterpret_cast<uint4*>(s_x + (put ^ ((i & 3) << 6)) + 1024 * i) = int4_order(__builtin_bit_cast(uint4, l.x[i]));
     uint4 q[R];
     float s[R][4], off[R][4];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      q[r] = __builtin_bit_cast(uint4, w[d][r]);
-      const float sv = G == 128 || 128 * b + 32 * g < K ? int4_scale(sc[d][r], p.scale_f16) : 0.0f;
-      if constexpr (G == 128) {
-        s[r][3] = sv;
-        off[r][3] = 16.0f + (zb ? static_cast<float>(zr[d][r]) : 8.0f);
-      } else {
-        q[r] = row_transpose(q[r]);
-        const uint32_t v = __float_as_uint(sv);
-        const uint4 a = row_transpose(uint4{v, v, v, v});
-        s[r][0] = __uint_as_float(a.x);
-        s[r][1] = __uint_as_float(a.y);
-        s[r][2] = __uint_as_float(a.z);
-        s[r][3] = __uint_as_float(a.w);
-        if (zb) {
-          const uint32_t o = __float_as_uint(16.0f + static_cast<float>(zr[d][r]));
-          const uint4 z = row_transpose(uint4{o, o, o, o});
-          off[r][0] = __uint_as_float(z.x);
-          off[r][1] = __uint_as_float(z.y);
-          off[r][2] = __uint_as_float(z.z);
-          off[r][3] = __uint_as_float(z.w);
-        } else {
+    for (int r = 0; r < R; ++r) *reinterpret_cast<u32x4*>(s_w + 1024 * r + 16 * lane) = l.w[r];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) off[r][j] = 24.0f;
-        }
+    for (int r = 0; r < R; ++r) {
+      if constexpr (G == 128) {
+        q[r] = *reinterpret_cast<const uint4*>(s_w + 1024 * r + wget);
+      } else {
+        q[r].x = *reinterpret_cast<const uint32_t*>(s_w + 1024 * r + wget);
+        q[r].y = *reinterpret_cast<const uint32_t*>(s_w + 1024 * r + (wget ^ 16));
+        q[r].z = *reinterpret_cast<const uint32_t*>(s_w + 1024 * r + (wget ^ 32));
+        q[r].w = *reinterpret_cast<const uint32_t*>(s_w + 1024 * r + (wget ^ 48));
+      }
+      // Row col's scales and zero points, from the lanes that loaded them.
+      const float sv = 128 * b + G * sub < K ? int4_scale(l.sc[r], p.scale_f16) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((32 * (j + 1)) % G != 0) continue;
+        const int from = 4 * (4 * col + 32 * j / G);
+        s[r][j] = __int_as_float(__builtin_amdgcn_ds_bpermute(from, __float_as_int(sv)));
+        off[r][j] = 16.0f + (zb ? static_cast<float>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(l.zr[r]))) : 8.0f);
       }
     }
     // (the loads' registers are free)
-    load(d, b + D);
+    load_w(l, b + D);
+    load_x(l, b + D);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (MT > 1 && 4 * m >= live) break;
@@ -213,8 +238,7 @@ __device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t*
       for (int r = 0; r < R; ++r) acc[r] = zero4;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = G == 128 ? 4 * g + j : 4 * j + g;
-        const uint4 f = *reinterpret_cast<const uint4*>(s_x + 4096 * m + 256 * col + ((c ^ col) << 4));
+        const uint4 f = *reinterpret_cast<const uint4*>(s_x + (get ^ (j << (G == 128 ? 4 : 6))) + 4096 * m);
         sum = mfma_bf16(f, ones, sum);
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -230,83 +254,73 @@ __device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t*
           sum = zero4;
         }
       }
+      // (the next row tile's fragments read ahead would not fit the registers)
+      if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);
     }
   };
+  // The weights ahead of what looks up the rows of A.
+  Loaded l0, l1;
   if (b0 < b1) {
-    static_for<D>([&](auto d) __attribute__((always_inline)) { load(d, b0 + d); });
-    for (int b = b0; b < b1; b += D)
-      static_for<D>([&](auto d) __attribute__((always_inline)) {
-        if (b + d < b1) block(d, b + d);
-      });
+    load_w(l0, b0);
+    if constexpr (D > 1) load_w(l1, b0 + 1);
+  }
+#pragma unroll
+  for (int i = 0; i < XL; ++i) {
+    const int r = 4 * i + g;
+    ao[i] = 0;
+    if (r < t.rows) ao[i] = static_cast<uint32_t>(max(int4_source(p, t.row0 + r), 0)) * static_cast<uint32_t>(K / 32);
+  }
+  if (b0 < b1) {
+    load_x(l0, b0);
+    if constexpr (D > 1) load_x(l1, b0 + 1);
+  }
+  for (int b = b0; b < b1; b += D) {
+    block(l0, b);
+    if constexpr (D > 1) {
+      if (b + 1 < b1) block(l1, b + 1);
+    }
   }
 
-  v4f* const s_sum = reinterpret_cast<v4f*>(lds);  // [W][R][MT][64]
-  __syncthreads();                                 // the rows of A are read
+  float* const s_sum = reinterpret_cast<float*>(lds);  // [W][R][MT][64 lanes][4]
+  constexpr int kWave = R * MT * 256;
+  __syncthreads();  // the rows of A are read
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      if (MT == 1 || 4 * m < live) s_sum[((wave * R + r) * MT + m) * 64 + lane] = total[r][m];
+      if (MT == 1 || 4 * m < live) *reinterpret_cast<v4f*>(s_sum + wave * kWave + ((r * MT + m) * 64 + lane) * 4) = total[r][m];
   __syncthreads();
-  // A wave finishes the tiles (c, m) of its number; gated, both of a pair.
-  for (int i = wave; i < NC * MT; i += W) {
-    const int m = i % MT, c = i / MT;
-    if (MT > 1 && 4 * m >= live) continue;
-    v4f v = zero4, u = zero4;
-#pragma unroll
-    for (int k = 0; k < W; ++k) v += s_sum[((k * R + c) * MT + m) * 64 + lane];
-    if constexpr (GATED) {
-#pragma unroll
-      for (int k = 0; k < W; ++k) u += s_sum[((k * R + NC + c) * MT + m) * 64 + lane];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = int4_gated(p.act, v[k], u[k], p.limit);
+  for (int i = tid; i < t.rows * C; i += 64 * W) {
+    const int r = i / C, c = i % C;
+    const float* from = s_sum + (((c / 16) * MT + r / 16) * 64 + c % 16 + 16 * (r % 16 / 4)) * 4 + r % 4;
+    float v = 0.0f, u = 0.0f;
+#pragma unroll 4
+    for (int w = 0; w < W; ++w) {
+      v += from[w * kWave];
+      if constexpr (GATED) u += from[w * kWave + (R > 1 ? NC * MT * 256 : 32)];  // (32: eight lanes on)
     }
-    const int n = 16 * (NC * tile + c) + col;
-    const uint2 bits = pack_bf16x4(v);
-    if (n < out_n) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = 16 * m + 4 * g + k;
-        const uint32_t o = k < 2 ? bits.x : bits.y;
-        if (r < t.rows)
-          p.c[static_cast<int64_t>(t.row0 + r) * out_n + n] =
-              int4_source(p, t.row0 + r) < 0 ? 0 : static_cast<uint16_t>(k & 1 ? o >> 16 : o);
-      }
-    }
+    if constexpr (GATED) v = int4_gated(p.act, v, u, p.limit);
+    if (int4_source(p, t.row0 + r) < 0) v = 0.0f;
+    if (n0 + c < out_n)
+      p.c[static_cast<int64_t>(t.row0 + r) * out_n + n0 + c] = static_cast<uint16_t>(pack_bf16x4(v4f{v, v, v, v}).x);
   }
 }
 
-// XL: of the launch's largest tiles; a tile with fewer rows takes a smaller form.
-// Workgroups stay and take tiles in turn: how many there are only the device knows.
-template <int G, int XL, int R, int D, int W, bool GATED>
+// A workgroup takes units of a column tile in turn: how many there are only the
+// device knows.
+template <int G, int XL, int R, int W, bool GATED>
 __global__ __launch_bounds__(64 * W, 1) void int4_stream_kernel(Int4GemmArgs p) {
   constexpr int MT = (XL + 3) / 4;
-  constexpr int kX = W * MT * 4096, kSum = W * R * MT * 1024;
+  constexpr int kX = W * (XL + R) * 1024, kSum = W * R * MT * 1024;
   __shared__ __attribute__((aligned(256))) uint8_t lds[kX > kSum ? kX : kSum];
-  const int out_n = GATED ? p.n / 2 : p.n, cols = GATED ? 8 * R : 16 * R;
-  const unsigned col_tiles = static_cast<unsigned>(out_n + cols - 1) / cols;
-  const int64_t total = int4_units<4 * XL, false>(p) * col_tiles;
-  for (int64_t task = blockIdx.x; task < total; task += gridDim.x) {
-    int64_t u;
-    int tile;
-    if (task < INT32_MAX) {  // (a 64-bit division is long)
-      u = static_cast<unsigned>(task) / col_tiles;
-      tile = static_cast<unsigned>(task) % col_tiles;
-    } else {
-      u = task / col_tiles;
-      tile = static_cast<int>(task % col_tiles);
-    }
+  bool more = true;
+  for (int u = blockIdx.y; more; u += gridDim.y) {
     Int4Unit t;
-    if (!int4_unit<4 * XL, false>(p, u, &t)) continue;
+    if (!int4_find<4 * XL>(p, u, gridDim.y, &t, &more)) break;
     t.expert = __builtin_amdgcn_readfirstlane(t.expert);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     t.rows = __builtin_amdgcn_readfirstlane(t.rows);
-    if (XL > 4 && t.rows <= 4)
-      int4_stream_tile<G, 1, R, 4, W, GATED>(p, lds, t, tile);
-    else if (XL > 4 && t.rows <= 16)
-      int4_stream_tile<G, 4, R, 3, W, GATED>(p, lds, t, tile);
-    else
-      int4_stream_tile<G, XL, R, D, W, GATED>(p, lds, t, tile);
+    if (t.rows > 0) int4_stream_tile<G, XL, R, W, GATED>(p, lds, t);
     __syncthreads();  // the sums are read
   }
 }
@@ -386,38 +400,34 @@ __device__ __forceinline__ void int4_unpack(Int4Unpack& u, uint32_t c, float s9,
 // that its L2 serves their weights and the rows' next column tiles.
 template <int TM>
 __device__ __forceinline__ bool int4_tile(const Int4GemmArgs& p, int col_tiles, Int4Unit* t, int* tile) {
-  const int64_t units = int4_units<TM, true>(p), total = units * col_tiles, per = (total + 7) / 8;
+  const int64_t total = static_cast<int64_t>(int4_units<TM>(p)) * col_tiles, per = (total + 7) / 8;
   const int64_t id = flat_block(), at = (id & 7) * per + (id >> 3);
   if ((id >> 3) >= per || at >= total) return false;
-  // Tiles in order of expert, then column tile, then row tile.
-  if (!p.counts) {
-    *tile = static_cast<int>(at / units);
-    return int4_unit<TM, true>(p, at % units, t);
+  // Unit at / col_tiles is one of the expert's; its tiles go column by column.
+  int u = 0, local = 0;
+  if (at < INT32_MAX) {  // (a 64-bit division is long)
+    u = static_cast<int>(static_cast<unsigned>(at) / static_cast<unsigned>(col_tiles));
+    local = static_cast<int>(at) - u * col_tiles;
+  } else {
+    u = static_cast<int>(at / col_tiles);
+    local = static_cast<int>(at % col_tiles);
   }
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0;
-  for (int e0 = 0; e0 < p.num_experts; e0 += 64) {
-    const int tiles = int4_tiles(p, e0 + lane, TM, true);
-    int incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += v;
-    }
-    const int all = __builtin_amdgcn_readlane(incl, 63);
-    if (at < (before + all) * col_tiles) {
-      const int l = __builtin_ctzll(__ballot((before + incl) * col_tiles > at));
-      const int mine = __builtin_amdgcn_readlane(tiles, l), e = e0 + l;
-      const int local = static_cast<int>(at - (before + __builtin_amdgcn_readlane(incl, l) - mine) * col_tiles);
-      *tile = local / mine;
-      t->expert = e;
-      t->row0 = int4_seg_start(p, e) + local % mine * TM;
-      t->rows = min(TM, int4_rows(p, e) - local % mine * TM);
-      return t->rows > 0;
-    }
-    before += all;
+  bool more;
+  if (!int4_find<TM>(p, u, 1, t, &more)) return false;
+  const int64_t mine = static_cast<int64_t>(u - t->first) * col_tiles + local;
+  int row;
+  if (mine < INT32_MAX) {
+    row = static_cast<int>(static_cast<unsigned>(mine) % static_cast<unsigned>(t->tiles));
+    *tile = static_cast<int>(static_cast<unsigned>(mine) / static_cast<unsigned>(t->tiles));
+  } else {
+    row = static_cast<int>(mine % t->tiles);
+    *tile = static_cast<int>(mine / t->tiles);
   }
-  return false;
+  // From unit u's rows to row tile `row`.
+  const int rows = p.counts ? int4_rows(p, t->expert) : p.row_cap;
+  t->row0 += (row - (u - t->first)) * TM;
+  t->rows = min(TM, rows - row * TM);
+  return t->rows > 0;
 }
 
 template <int G, int TT, int NT, bool GATED>
@@ -621,12 +631,12 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   // Output, through LDS so that a row's columns leave in whole lines. A lane
   // holds weight rows 8 v + 4 h .. + 3 (v = 0 .. 3) of its row of A; a wave's
   // rows of 32 NC columns lie in chunks of 8 columns, chunk c in slot c ^ row % 16
-  // (NC = 2: of half as long rows, c ^ row / 2 % 8).
+  // (of rows half or a quarter as long c ^ row / 2 % 8, c ^ row / 4 % 4).
   constexpr int kRow = 64 * NC, kChunks = 4 * NC;
-  static_assert(4 * TM * kRow <= 2 * kABytes + 8 * kWBytes && (NC == 4 || NC == 2), "");
+  static_assert(4 * TM * kRow <= 2 * kABytes + 8 * kWBytes && (NC == 4 || NC == 2 || NC == 1), "");
   lds_barrier();  // other waves still read A's rows
   uint8_t* const s_c = s_buf + wave * (TM * kRow);
-  auto slot = [&](int c, int row) { return (c ^ (NC == 4 ? row & 15 : row >> 1 & 7)) << 4; };
+  auto slot = [&](int c, int row) { return (c ^ (NC == 4 ? row & 15 : NC == 2 ? row >> 1 & 7 : row >> 2 & 3)) << 4; };
 #pragma unroll
   for (int m = 0; m < TT; ++m) {
 #pragma unroll
@@ -659,32 +669,52 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
   }
 }
 
-template <int G, int XL, int R, int D, int W, bool GATED>
-hipError_t stream_launch(const Int4GemmArgs& p, hipStream_t stream) {
+// Experts of more than `over` and at most `to` rows.
+template <int G, int XL, int R, int W, bool GATED>
+hipError_t stream_launch(Int4GemmArgs p, int over, int to, hipStream_t stream) {
   constexpr int TM = 4 * XL;
+  p.rows_over = over;
+  p.rows_to = to;
   const int out_n = GATED ? p.n / 2 : p.n, cols = GATED ? 8 * R : 16 * R;
   // Every tile but an expert's last is full.
-  const int64_t used = p.num_experts < p.row_cap ? p.num_experts : p.row_cap;
+  const int64_t fit = p.row_cap / (over + 1), used = p.num_experts < fit ? p.num_experts : fit;
   const int64_t units = p.counts ? p.row_cap / TM + used : (p.row_cap + TM - 1) / TM;
-  const int64_t tasks = (out_n + cols - 1) / cols * units, cap = 2 * static_cast<int64_t>(device_cu_count());
-  hipLaunchKernelGGL((int4_stream_kernel<G, XL, R, D, W, GATED>), dim3(static_cast<unsigned>(tasks < cap ? tasks : cap)),
+  if (units == 0) return hipSuccess;
+  // About a workgroup of 16 waves, or two of 8, for a CU: more would wait for it
+  // only to find that there is no unit for them.
+  const int64_t tiles = (out_n + cols - 1) / cols, stay = (16 / W * device_cu_count() + tiles - 1) / tiles;
+  const int64_t y = units < stay ? units : stay;
+  hipLaunchKernelGGL((int4_stream_kernel<G, XL, R, W, GATED>), dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(y)),
                      dim3(64 * W), 0, stream, p);
   return hipGetLastError();
 }
 
+// Experts of at most `bound` rows (to: the largest count taken as such).
 template <int G, bool GATED>
-hipError_t stream_rows(const Int4GemmArgs& p, int bound, hipStream_t stream) {
-  if (bound <= 4) return stream_launch<G, 1, 2, 4, 8, GATED>(p, stream);
-  if (bound <= 16) return stream_launch<G, 4, 2, 3, 8, GATED>(p, stream);
-  if (bound <= 32) return stream_launch<G, 8, 4, 2, 4, GATED>(p, stream);
-  return stream_launch<G, 16, 4, 1, 4, GATED>(p, stream);
+hipError_t stream_rows(const Int4GemmArgs& p, int bound, int to, hipStream_t stream) {
+  const int out_n = GATED ? p.n / 2 : p.n;
+  const bool narrow = !p.counts && (out_n + (GATED ? 15 : 31)) / (GATED ? 16 : 32) < device_cu_count();
+  if (bound <= 4)
+    return narrow ? stream_launch<G, 1, 1, 16, GATED>(p, 0, to, stream) : stream_launch<G, 1, 2, 16, GATED>(p, 0, to, stream);
+  int over = 0;
+  if (bound <= 16 || p.counts) {
+    const int t = bound <= 16 ? to : 16;
+    const hipError_t e = narrow ? stream_launch<G, 4, 1, 16, GATED>(p, 0, t, stream)
+                                : stream_launch<G, 4, 2, 16, GATED>(p, 0, t, stream);
+    if (e != hipSuccess || bound <= 16) return e;
+    over = 16;
+  }
+  if (bound <= 32) return stream_launch<G, 8, 2, 8, GATED>(p, over, to, stream);
+  return stream_launch<G, 16, 1, 8, GATED>(p, over, to, stream);
 }
 
 template <int G, int TT, int NT, bool GATED>
-hipError_t tiled_launch(const Int4GemmArgs& p, hipStream_t stream) {
+hipError_t tiled_launch(Int4GemmArgs p, hipStream_t stream) {
   constexpr int TM = 32 * TT, NC = GATED ? NT / 2 : NT;
+  p.rows_over = kInt4FewRows;
+  p.rows_to = INT32_MAX;
   const int out_n = GATED ? p.n / 2 : p.n;
-  const int64_t used = p.num_experts < p.row_cap / (p.few + 1) ? p.num_experts : p.row_cap / (p.few + 1);
+  const int64_t fit = p.row_cap / (kInt4FewRows + 1), used = p.num_experts < fit ? p.num_experts : fit;
   const int64_t units = p.counts ? p.row_cap / TM + used : (p.row_cap + TM - 1) / TM;
   // A multiple of 8: every XCD's share rounded up.
   const int64_t tasks = (units * ((out_n + 128 * NC - 1) / (128 * NC)) + 7) / 8 * 8;
@@ -696,15 +726,17 @@ template <int G, bool GATED>
 hipError_t gemm_launch(Int4GemmArgs p, hipStream_t stream) {
   const int out_n = GATED ? p.n / 2 : p.n;
   p.vector_out = out_n % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
-  if (p.max_rows_per_expert <= kInt4FewRows) {
-    p.few = INT32_MAX;  // whatever the counts say
-    return stream_rows<G, GATED>(p, p.max_rows_per_expert, stream);
-  }
-  p.few = kInt4FewRows;
+  // (a count past the bound is computed all the same)
+  if (p.max_rows_per_expert <= kInt4FewRows) return stream_rows<G, GATED>(p, p.max_rows_per_expert, INT32_MAX, stream);
   if (p.counts) {
-    const hipError_t e = stream_rows<G, GATED>(p, kInt4FewRows, stream);
+    const hipError_t e = stream_rows<G, GATED>(p, kInt4FewRows, kInt4FewRows, stream);
     if (e != hipSuccess) return e;
   }
+  const char* lab = getenv("LAB_TILE");
+  if (lab && lab[0] == 's') return stream_rows<G, GATED>(p, 64, INT32_MAX, stream);
+  if (lab && lab[0] == '2') return tiled_launch<G, 2, 2, GATED>(p, stream);
+  if (lab && lab[0] == '3') return tiled_launch<G, 4, 2, GATED>(p, stream);
+  if (lab && lab[0] == '5') return tiled_launch<G, 2, 4, GATED>(p, stream);
   return tiled_launch<G, 4, 4, GATED>(p, stream);
 }
 

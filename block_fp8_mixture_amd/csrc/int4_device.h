@@ -33,25 +33,26 @@ __device__ __forceinline__ uint4 int4_order(uint4 x) {
                __builtin_amdgcn_perm(x.w, x.y, 0x05040100u), __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
 }
 
-// Transposes the 4 x 4 words that the wave's four rows of 16 lanes hold: word j
-// of row g becomes word g of row j.
-__device__ __forceinline__ uint4 row_transpose(uint4 w) {
-  auto s0 = __builtin_amdgcn_permlane16_swap(w.x, w.y, false, false);
-  auto s1 = __builtin_amdgcn_permlane16_swap(w.z, w.w, false, false);
-  auto t0 = __builtin_amdgcn_permlane32_swap(s0[0], s1[0], false, false);
-  auto t1 = __builtin_amdgcn_permlane32_swap(s0[1], s1[1], false, false);
-  return uint4{t0[0], t1[0], t0[1], t1[1]};
-}
-
 __device__ __forceinline__ float int4_scale(uint32_t bits, int f16) {
   const float h = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
   return f16 ? h : bf16_to_f32(bits);
 }
 
+// exp(-g): v_exp_f32 of the product with log2(e), and what the product's rounding
+// and the constant leave out as a factor 1 + d ln 2 (expf's code is three times as
+// long, of which short launches feel the fetching).
+__device__ __forceinline__ float exp_neg(float g) {
+  constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0cp-26f;  // log2(e)
+  const float t = -g * kHi;
+  const float d = __builtin_fmaf(-g, kHi, -t) - g * kLo;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return e + e * (d * 0.693147180559945f);
+}
+
 // SiLU(gate) * up in fp32; a NaN passes the clamps.
 __device__ __forceinline__ float int4_gated(int act, float g, float u, float lim) {
   if (act == 1) g = g > lim ? lim : g;
-  float s = g / (1.0f + expf(-g));
+  float s = g / (1.0f + exp_neg(g));
   if (act == 2) s = s > lim ? lim : s;
   if (act != 0) u = fabsf(u) > lim ? __builtin_copysignf(lim, u) : u;
   return s * u;

@@ -244,7 +244,8 @@ struct Int4GemmArgs {
   int act;                   // Act, or -1: none
   float limit;
   uint16_t* c;               // [row_cap, n], gated [row_cap, n/2]
-  int few = 0;               // set by the launcher: rows of an expert that streams
+  int rows_over = 0;         // set by the launcher: a launch's experts have more rows than this
+  int rows_to = 0;           //   and at most as many
   int vector_out = 0;        // set by the launcher: eight columns of c at once
 };
 // Experts of at most this many rows have their weights streamed, exact; more
