@@ -693,7 +693,7 @@ hipError_t stream_launch(Int4GemmArgs p, int over, int to, hipStream_t stream) {
 template <int G, bool GATED>
 hipError_t stream_rows(const Int4GemmArgs& p, int bound, int to, hipStream_t stream) {
   const int out_n = GATED ? p.n / 2 : p.n;
-  const bool narrow = !p.counts && (out_n + (GATED ? 15 : 31)) / (GATED ? 16 : 32) < device_cu_count();
+  const bool narrow = !p.counts && (out_n + (GATED ? 15 : 31)) / (GATED ? 16 : 32) <= device_cu_count() / 2;
   if (bound <= 4)
     return narrow ? stream_launch<G, 1, 1, 16, GATED>(p, 0, to, stream) : stream_launch<G, 1, 2, 16, GATED>(p, 0, to, stream);
   int over = 0;
@@ -704,8 +704,10 @@ hipError_t stream_rows(const Int4GemmArgs& p, int bound, int to, hipStream_t str
     if (e != hipSuccess || bound <= 16) return e;
     over = 16;
   }
-  if (bound <= 32) return stream_launch<G, 8, 2, 8, GATED>(p, over, to, stream);
-  return stream_launch<G, 16, 1, 8, GATED>(p, over, to, stream);
+  const char* lab = getenv("LAB_MID");
+  if (lab && lab[0] == '1') return stream_launch<G, 8, 1, 16, GATED>(p, over, to, stream);
+  if (lab && lab[0] == '2') return stream_launch<G, 8, 2, 16, GATED>(p, over, to, stream);
+  return stream_launch<G, 8, 2, 8, GATED>(p, over, to, stream);
 }
 
 template <int G, int TT, int NT, bool GATED>
