@@ -7,7 +7,7 @@
 // holds row l % 16 and the K values 8 (l / 16) .. + 7) and weight rows as its
 // second (alike); lane l of the result holds weight row l % 16 and rows of A
 // 4 (l / 16) + v, so a lane needs one row's scales.
-#include <cstdlib>
+#include <cmath>
 #include <utility>
 
 #include "int4_device.h"
@@ -309,7 +309,7 @@ __device__ __forceinline__ void int4_stream_tile(const Int4GemmArgs& p, uint8_t*
 // A workgroup takes units of a column tile in turn: how many there are only the
 // device knows.
 template <int G, int XL, int R, int W, bool GATED>
-__global__ __launch_bounds__(64 * W, 1) void int4_stream_kernel(Int4GemmArgs p) {
+__global__ __launch_bounds__(64 * W, XL == 8 ? 1 : 4) void int4_stream_kernel(Int4GemmArgs p) {
   constexpr int MT = (XL + 3) / 4;
   constexpr int kX = W * (XL + R) * 1024, kSum = W * R * MT * 1024;
   __shared__ __attribute__((aligned(256))) uint8_t lds[kX > kSum ? kX : kSum];
@@ -600,7 +600,9 @@ __global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs 
           read_w(w[(i + 1) & 1][k - TT], q < 4 ? step : step ^ 1, (i + 1) & 1, k - TT);
         // Pieces of A and of the codes, in the last block none: it reads the next
         // step's, past a barrier.
-        constexpr int kPieces = AL + WL, kHalf = NT * TT / 2;
+        constexpr int kPieces = AL + WL, kMost = 2 * ((kPieces + 6) / 7);  // slots that a block's take
+        constexpr int kHalf = NT * TT / 2 < NT * TT - kMost ? NT * TT / 2 : NT * TT - kMost;
+        static_assert(kHalf >= 0, "a block's pieces fit its slots");
         constexpr int p0 = q * kPieces / 7, p1 = q < 7 ? (q + 1) * kPieces / 7 : p0;
         constexpr int piece = p0 + (k - kHalf) / 2;
         if constexpr (k >= kHalf && piece < p1) {
@@ -699,14 +701,12 @@ hipError_t stream_rows(const Int4GemmArgs& p, int bound, int to, hipStream_t str
   int over = 0;
   if (bound <= 16 || p.counts) {
     const int t = bound <= 16 ? to : 16;
-    const hipError_t e = narrow ? stream_launch<G, 4, 1, 16, GATED>(p, 0, t, stream)
-                                : stream_launch<G, 4, 2, 16, GATED>(p, 0, t, stream);
+    const hipError_t e = narrow      ? stream_launch<G, 4, 1, 16, GATED>(p, 0, t, stream)
+                         : p.counts ? stream_launch<G, 4, 2, 8, GATED>(p, 0, t, stream)
+                                    : stream_launch<G, 4, 2, 16, GATED>(p, 0, t, stream);
     if (e != hipSuccess || bound <= 16) return e;
     over = 16;
   }
-  const char* lab = getenv("LAB_MID");
-  if (lab && lab[0] == '1') return stream_launch<G, 8, 1, 16, GATED>(p, over, to, stream);
-  if (lab && lab[0] == '2') return stream_launch<G, 8, 2, 16, GATED>(p, over, to, stream);
   return stream_launch<G, 8, 2, 8, GATED>(p, over, to, stream);
 }
 
@@ -724,21 +724,48 @@ hipError_t tiled_launch(Int4GemmArgs p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Expected time, us, of the forms that more than kInt4FewRows rows can take, by
+// the tiles that there are for each CU (r). Tiled forms: a superstep of 256 K
+// values takes 2.4 us a round of 64 x 256 tiles, 3 to 4 of 128 x 256 ones and 4.7
+// to 7.3 of 128 x 512 ones (the more the fuller the chip, whose clock falls), and
+// some 5 us go around it; streamed tiles of 32 x 32 take 2.5 us and 0.2 for every
+// 128 K values. Measured (streamed, 64 x 256, 128 x 256, 128 x 512), us, for rows,
+// K, N: 300, 6144, 1000: 30, 57, 70, 125; 70, 4096, 4096: 15, 38, 46, 79; 300,
+// 2048, 7168: 56, 24, 30, 49; 300, 7168, 4096 gated: 68, 65, 83, 144; 512, 4096,
+// 4096: -, 42, 51, 84; 1024, 4096, 4096: 134, 51, 54, 86; 1024, 2048, 7168: -, 41,
+// 36, 52; 2048, 4096, 4096: -, 85, 70, 92; 2048, 7168, 8192: -, 276, 226, 207.
+struct Int4Costs {
+  double stream, small, medium, large;
+};
+Int4Costs int4_costs(const Int4GemmArgs& p, int out_n, int gated) {
+  const double cus = device_cu_count(), blocks = (p.k + 255) / 256;
+  const double experts = p.counts ? (p.num_experts < p.row_cap ? p.num_experts : p.row_cap) : 1.0;
+  const double mean = p.row_cap / experts;
+  // Row tiles: of one expert known, of several half a tile more than they fill.
+  auto units = [&](int tm) { return p.num_experts > 1 ? experts * (mean / tm + 0.5) : ceil(p.row_cap / static_cast<double>(tm)); };
+  auto cols = [&](int c) { return ceil(out_n / static_cast<double>(gated ? c / 2 : c)); };
+  auto fill = [](double r) { return r < 1.0 ? r : 1.0; };
+  const double rs = units(32) * cols(32) / cus, r2 = units(64) * cols(256) / cus;
+  const double r4 = units(128) * cols(256) / cus, r8 = units(128) * cols(512) / cus;
+  return {ceil(rs) * (2.5 + 0.4 * blocks), 5.0 + blocks * 2.4 * ceil(r2),
+          5.0 + blocks * ceil(r4) * (3.0 + fill(r4)), 5.0 + blocks * ceil(r8) * (4.7 + 2.6 * fill(r8))};
+}
+
 template <int G, bool GATED>
 hipError_t gemm_launch(Int4GemmArgs p, hipStream_t stream) {
   const int out_n = GATED ? p.n / 2 : p.n;
   p.vector_out = out_n % 8 == 0 && (reinterpret_cast<uintptr_t>(p.c) & 15) == 0;
   // (a count past the bound is computed all the same)
   if (p.max_rows_per_expert <= kInt4FewRows) return stream_rows<G, GATED>(p, p.max_rows_per_expert, INT32_MAX, stream);
+  const Int4Costs t = int4_costs(p, out_n, GATED);
+  if (t.stream <= t.small && t.stream <= t.medium && t.stream <= t.large)
+    return stream_rows<G, GATED>(p, p.max_rows_per_expert, INT32_MAX, stream);
   if (p.counts) {
     const hipError_t e = stream_rows<G, GATED>(p, kInt4FewRows, kInt4FewRows, stream);
     if (e != hipSuccess) return e;
   }
-  const char* lab = getenv("LAB_TILE");
-  if (lab && lab[0] == 's') return stream_rows<G, GATED>(p, 64, INT32_MAX, stream);
-  if (lab && lab[0] == '2') return tiled_launch<G, 2, 2, GATED>(p, stream);
-  if (lab && lab[0] == '3') return tiled_launch<G, 4, 2, GATED>(p, stream);
-  if (lab && lab[0] == '5') return tiled_launch<G, 2, 4, GATED>(p, stream);
+  if (t.small <= t.medium && t.small <= t.large) return tiled_launch<G, 2, 2, GATED>(p, stream);
+  if (t.medium <= t.large) return tiled_launch<G, 4, 2, GATED>(p, stream);
   return tiled_launch<G, 4, 4, GATED>(p, stream);
 }
 

@@ -378,17 +378,16 @@ typedef struct {
  *   act MOE_ACT_NONE:  c[r, n] = bf16(S[r, n])
  *   otherwise, with N = n / 2 (moe_act's formulas, in fp32):
  *                      c[r, i] = bf16(act(gate = S[r, i], up = S[r, N + i]))
- * Sums are in fp32, rounded once. Up to MOE_INT4_EXACT_ROWS live rows of an
- * expert the weights are exact: a group's sum is taken as sum a (16 + q) -
- * (16 + z) sum a and scaled then (fp32 must hold 31 times a group's sum of
- * magnitudes). With more rows (and max_rows_per_expert, or the dense product's
- * rows without t_live_dev, above it) they enter the matrix cores as
- * moe_int4_dequant's BF16 values, which adds about as much as the output's own
- * rounding; scales are below 2^118 in magnitude there. A NaN in a row of
- * a makes every sum of the row NaN, an infinity makes it that or an infinity; a
- * NaN passes the clamps. Any n >= 1 (even where gated) and any number of rows. The order
- * of a sum may depend on the launch (rows, max_rows_per_expert): low bits may
- * differ between calls that differ in these; the same call gives the same bits.
+ * Sums are in fp32, rounded once. For at most MOE_INT4_EXACT_ROWS live rows of
+ * an expert, and for more where that is expected to be faster, the weights are
+ * exact: a group's sum is taken as sum a (16 + q) - (16 + z) sum a and scaled then
+ * (fp32 must hold 31 times a group's sum of magnitudes). Otherwise they enter the
+ * matrix cores as moe_int4_dequant's BF16 values, which adds about as much as the
+ * output's own rounding; scales are below 2^118 in magnitude there. Which of the
+ * two, and the order of a sum, goes by n, k, num_experts, the rows and
+ * max_rows_per_expert: the same call gives the same bits. A NaN in a row of a makes
+ * every sum of the row NaN, an infinity makes it that or an infinity; a NaN passes
+ * the clamps. Any n >= 1 (even where gated) and any number of rows.
  *
  * moe_gemm_int4: one matrix (num_experts = 1).
  *   a           device BF16 [rows, k], 16-byte aligned
