@@ -226,18 +226,18 @@ def _min_numel(t, name, n):
 def _same_device(*tensors):
     """All given tensors on one GPU (checked after every shape, so shape errors
     are reported first). Returns the device."""
-    dev = None
+    first, index = None, -1
     for t in tensors:
         if t is None:
             continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+        if first is None:
+            first, index = t, t.get_device()  # -1 off the GPUs; cheaper than t.device
+        elif t.get_device() != index:
             devs = {t.device for t in tensors if t is not None}
             raise ValueError(f"tensors live on different devices: {sorted(map(str, devs))}")
-    if dev is None or dev.type != "cuda":
+    if index < 0:
         raise ValueError("tensors must be GPU tensors")
-    return dev
+    return first.device
 
 
 def _fmt(fmt):
@@ -279,6 +279,13 @@ def _live(t_live):
 def _bf16(t, name):
     """BF16 values or their bits (int16); only the address is used."""
     return _need(t, name, torch.bfloat16 if t.dtype == torch.bfloat16 else torch.int16)
+
+
+def _bf16_exact(t, name, shape):
+    """_bf16 and _shape (a tuple), at once where they hold."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and t.is_contiguous():
+        return t
+    return _shape(_bf16(t, name), name, shape)
 
 
 def moe_min_row_cap(t_cap, topk, num_experts, align_rows):
@@ -357,35 +364,38 @@ def moe_rmsnorm_quant(x, weight, eps=1e-6, fmt="fp32", residual=None, t_live=Non
     lib = load_library()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")
-    if x.dtype not in (torch.bfloat16, torch.int16):
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.int16:
         raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError("x must be [t_cap, hidden]")
-    t_cap, hidden = x.shape
+    shape = t_cap, hidden = tuple(x.shape)
     if (t_cap | hidden) >> 31:
         raise ValueError(_PAST_INT32)
-    ld = x.stride(0) if t_cap > 1 else hidden
-    if (hidden > 1 and x.stride(1) != 1) or ld < hidden:
+    ld, step = x.stride()
+    if t_cap <= 1:
+        ld = hidden
+    if (hidden > 1 and step != 1) or ld < hidden:
         raise ValueError("the columns of x must be contiguous and its rows apart")
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, torch.bfloat16):
+    weight_type = weight.dtype if isinstance(weight, torch.Tensor) else None
+    if weight_type is not torch.bfloat16 and weight_type is not torch.float32:
         raise TypeError("weight must be a float32 or bfloat16 tensor")
-    _exact(weight, "weight", weight.dtype, (hidden,))
+    _exact(weight, "weight", weight_type, (hidden,))
     eps = float(eps)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("eps must be finite and not negative")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if residual is not None:
-        _shape(_bf16(residual, "residual"), "residual", (t_cap, hidden))
+        _bf16_exact(residual, "residual", shape)
         if residual_out is None:
-            residual_out = torch.empty((t_cap, hidden), dtype=torch.bfloat16, device=x.device)
-        _shape(_bf16(residual_out, "residual_out"), "residual_out", (t_cap, hidden))
+            residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        _bf16_exact(residual_out, "residual_out", shape)
     if y is None:
-        y = torch.empty((t_cap, hidden), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
     elif y is False:
         y = None
     if y is not None:
-        _shape(_bf16(y, "y"), "y", (t_cap, hidden))
+        _bf16_exact(y, "y", shape)
     if fmt is None:
         if xq is not None or xs is not None:
             raise ValueError("xq and xs need a fmt")
@@ -393,14 +403,15 @@ def moe_rmsnorm_quant(x, weight, eps=1e-6, fmt="fp32", residual=None, t_live=Non
             raise ValueError("without y there must be a fmt")
     else:
         _fmt(fmt)
+        codes, scales, scale_type = (t_cap, _code_cols(hidden, fmt)), _scale_shape(t_cap, hidden, fmt), _scale_dtype(fmt)
         if xq is None:
-            xq = torch.empty((t_cap, _code_cols(hidden, fmt)), dtype=torch.uint8, device=x.device)
+            xq = torch.empty(codes, dtype=torch.uint8, device=x.device)
         if xs is None:
-            xs = torch.empty(_scale_shape(t_cap, hidden, fmt), dtype=_scale_dtype(fmt), device=x.device)
-        _exact(xq, "xq", torch.uint8, (t_cap, _code_cols(hidden, fmt)))
-        _exact(xs, "xs", _scale_dtype(fmt), _scale_shape(t_cap, hidden, fmt))
+            xs = torch.empty(scales, dtype=scale_type, device=x.device)
+        _exact(xq, "xq", torch.uint8, codes)
+        _exact(xs, "xs", scale_type, scales)
     dev = _same_device(x, weight, residual, residual_out, y, xq, xs, t_live)
-    _enqueue("moe_rmsnorm_quant", dev, _ptr(x), ld, _ptr(residual), _ptr(weight), ELEM_TYPES[weight.dtype],
+    _enqueue("moe_rmsnorm_quant", dev, _ptr(x), ld, _ptr(residual), _ptr(weight), ELEM_TYPES[weight_type],
              eps, t_cap, _live(t_live), hidden, _fmt(fmt or "fp32"), _rounding(rounding),
              _ptr(residual_out), _ptr(y), _ptr(xq), _ptr(xs))
     return y, xq, xs, residual_out
@@ -415,9 +426,10 @@ def _int4_group(cols, groups, name):
 
 
 def _int4_scale_type(scales, name):
-    if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.bfloat16, torch.float16):
+    dtype = scales.dtype if isinstance(scales, torch.Tensor) else None
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
-    return ELEM_TYPES[scales.dtype]
+    return ELEM_TYPES[dtype]
 
 
 def moe_int4_quant(w, group=128, symmetric=True, scale_dtype=torch.bfloat16, codes=None, scales=None,
@@ -481,16 +493,19 @@ def moe_int4_dequant(codes, scales, zeros=None, out=None):
     return out
 
 
-def _int4_weights(w, scales, zeros, num_experts, n):
-    """The C structure of checked weights whose leading shape is ``w.shape[:-1]``."""
-    k = 2 * w.shape[-1]
+def _int4_weights(w, scales, zeros, num_experts, n, shape):
+    """The C structure of checked weights whose shape is ``shape`` (a tuple)."""
+    k = 2 * shape[-1]
     scale_type = _int4_scale_type(scales, "w_scales")
-    if scales.dim() != w.dim():
+    got = tuple(scales.shape)
+    if len(got) != len(shape):
         raise ValueError("w_scales must be [..., N, K / group]")
-    group = _int4_group(k, scales.shape[-1], "w")
-    _exact(scales, "w_scales", scales.dtype, tuple(w.shape[:-1]) + (k // group,))
+    group = _int4_group(k, got[-1], "w")
+    want = shape[:-1] + got[-1:]
+    if got != want or not scales.is_contiguous():
+        _exact(scales, "w_scales", scales.dtype, want)
     if zeros is not None:
-        _exact(zeros, "w_zeros", torch.uint8, tuple(w.shape[:-1]) + (k // group,))
+        _exact(zeros, "w_zeros", torch.uint8, want)
     if (n | k) >> 31:
         raise ValueError(_PAST_INT32)
     return _Int4Weights(_ptr(w), _ptr(scales), _ptr(zeros), scale_type, group, num_experts, n, k)
@@ -519,16 +534,16 @@ def moe_gemm_int4(x, w, w_scales, w_zeros=None, act=None, clamp_limit=float("inf
         raise ValueError("x must be [T, K]")
     _need(w, "w", torch.uint8, ndim=2)
     rows, k = xb.shape
-    n = w.shape[0]
-    if 2 * w.shape[1] != k:
+    n, k2 = shape = tuple(w.shape)
+    if 2 * k2 != k:
         raise ValueError("x and w disagree on K")
     if rows >> 31:
         raise ValueError(_PAST_INT32)
-    weights = _int4_weights(w, w_scales, w_zeros, 1, n)
+    weights = _int4_weights(w, w_scales, w_zeros, 1, n, shape)
     act_value, out_n = _gate(act, n)
     if out is None:
         out = torch.empty((rows, out_n), dtype=torch.bfloat16, device=xb.device)
-    ob = _shape(_bf16(out, "out"), "out", (rows, out_n))
+    ob = _bf16_exact(out, "out", (rows, out_n))
     if t_live is not None:
         _exact(t_live, "t_live", torch.int32, (1,))
     dev = _same_device(xb, w, w_scales, w_zeros, ob, t_live)
@@ -551,11 +566,11 @@ def moe_grouped_gemm_int4(a, w, w_scales, counts, offsets=None, row_cap=None, w_
     if ab.dim() != 2:
         raise ValueError("a must be [a_rows, K]")
     _need(w, "w", torch.uint8, ndim=3)
-    num_experts, n, k2 = w.shape
-    a_rows = ab.shape[0]
-    if ab.shape[1] != 2 * k2:
+    num_experts, n, k2 = shape = tuple(w.shape)
+    a_rows, k = ab.shape
+    if k != 2 * k2:
         raise ValueError("a and w disagree on K")
-    weights = _int4_weights(w, w_scales, w_zeros, num_experts, n)
+    weights = _int4_weights(w, w_scales, w_zeros, num_experts, n, shape)
     act_value, out_n = _gate(act, n)
     _exact(counts, "counts", torch.int32, (num_experts,))
     expert_cap, a_row_div, max_rows = int(expert_cap), int(a_row_div), int(max_rows_per_expert)
