@@ -325,7 +325,8 @@ static moe_status gemm_int4_checked(moe::Int4GemmArgs* g, const moe_int4_weights
       ((act == MOE_ACT_SWIGLU_CLAMP || act == MOE_ACT_SWIGLU_CLAMP_AFTER_SILU) && !(clamp_limit > 0.0f)))
     return MOE_ERR_INVALID_ARG;
   if (w->num_experts > moe::kMaxExperts || w->k > moe::kMaxInt4K ||
-      static_cast<int64_t>(w->n) * w->k >= (int64_t{1} << 32))
+      w->n > moe::kMaxInt4N || static_cast<int64_t>(w->n) * w->k >= (int64_t{1} << 32) ||
+      static_cast<int64_t>(g->a_rows) * w->k >= (int64_t{1} << 37))  // 32-bit offsets, of a in 64 bytes
     return MOE_ERR_UNSUPPORTED;
   if (g->row_cap == 0) return MOE_OK;
   if (!g->a || g->a_rows < 1 || !g->c || !w->codes || !w->scales || !aligned(g->a, 16) ||

@@ -27,23 +27,26 @@ __device__ __forceinline__ void static_for(F&& f) {
 
 // Inclusive sum over the lanes up to each.
 __device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr 1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);  // lane 15 of the row before
-  return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);  // lane 31
+  auto add = [&](int u) { v = static_cast<int>(static_cast<unsigned>(v) + static_cast<unsigned>(u)); };
+  add(__builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true));  // row_shr 1, 2, 4, 8
+  add(__builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true));
+  add(__builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true));  // lane 15 of the row before
+  add(__builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true));  // lane 31
+  return v;
 }
 
 // Units of work are the TM-row tiles, in order, of the experts with more than
-// p.rows_over rows and not more than p.rows_to. Every wave scans the counts.
+// p.rows_over rows and not more than p.rows_to. Every wave scans the counts. (Counts
+// whose sum overflows are no align's: they wrap, and may find nothing.)
 struct Int4Unit {
   int expert, row0, rows;  // first row and rows of the tile; no rows: not a segment
   int tiles, first;        // units of the expert, and its first one's number
 };
 constexpr int kScan = 8;  // experts of a lane at once: their loads wait for one another's only
 __device__ __forceinline__ int int4_tiles(const Int4GemmArgs& p, int e, int tm) {
-  const int c = e < p.num_experts ? min(p.counts[e], p.row_cap) : 0;
+  const int c = e < p.num_experts ? min(p.counts[e], p.seg_cap > 0 ? p.seg_cap : p.row_cap) : 0;
   return c > p.rows_over && c <= p.rows_to ? (c + tm - 1) / tm : 0;
 }
 // Unit u; false past the last. *more: whether there may be one `step` on.
@@ -58,29 +61,33 @@ __device__ __forceinline__ bool int4_find(const Int4GemmArgs& p, int u, int step
     return u < t->tiles;
   }
   const int lane = threadIdx.x & 63;
-  int before = 0;
+  unsigned before = 0;
+  const unsigned want = static_cast<unsigned>(u);
   for (int e0 = 0; e0 < p.num_experts; e0 += 64 * kScan) {
     int tiles[kScan], found = -1;
 #pragma unroll
     for (int i = 0; i < kScan; ++i) tiles[i] = int4_tiles(p, e0 + 64 * i + lane, TM);
 #pragma unroll
     for (int i = 0; i < kScan; ++i) {
-      const int incl = wave_scan(tiles[i]);
-      const int all = __builtin_amdgcn_readlane(incl, 63);
-      if (u >= before && u < before + all) {
-        const int l = __builtin_ctzll(__ballot(before + incl > u));
+      const unsigned incl = static_cast<unsigned>(wave_scan(tiles[i]));
+      const unsigned all = static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(incl), 63));
+      const uint64_t lanes = __ballot(want - before < incl);
+      if (want - before < all && lanes != 0) {
+        const int l = __builtin_ctzll(lanes);
         t->tiles = __builtin_amdgcn_readlane(tiles[i], l);
-        t->first = before + __builtin_amdgcn_readlane(incl, l) - t->tiles;
+        t->first = static_cast<int>(before + static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(incl), l)) -
+                                    static_cast<unsigned>(t->tiles));
         found = e0 + 64 * i + l;
       }
       before += all;
     }
     if (found >= 0) {
+      if (want - static_cast<unsigned>(t->first) >= static_cast<unsigned>(t->tiles)) return false;
       const int at = (u - t->first) * TM;
       t->expert = found;
       t->row0 = int4_seg_start(p, found) + at;
       t->rows = min(TM, int4_rows(p, found) - at);
-      *more = u + step < before || e0 + 64 * kScan < p.num_experts;
+      *more = want + step < before || e0 + 64 * kScan < p.num_experts;
       return true;
     }
   }

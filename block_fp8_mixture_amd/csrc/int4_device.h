@@ -45,8 +45,8 @@ __device__ __forceinline__ float exp_neg(float g) {
   constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0cp-26f;  // log2(e)
   const float t = -g * kHi;
   const float d = __builtin_fmaf(-g, kHi, -t) - g * kLo;
-  const float e = __builtin_amdgcn_exp2f(t);
-  return e + e * (d * 0.693147180559945f);
+  const float e = __builtin_amdgcn_exp2f(t), r = __builtin_fmaf(e, d * 0.693147180559945f, e);
+  return e > 0.0f && e < __builtin_inff() ? r : e;  // (0 and infinity times d may be NaN)
 }
 
 // SiLU(gate) * up in fp32; a NaN passes the clamps.

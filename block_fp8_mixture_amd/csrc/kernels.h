@@ -223,6 +223,7 @@ hipError_t launch_int4_dequant(const uint8_t* codes, const uint16_t* scales, int
 
 // Products of BF16 rows with such weights.
 constexpr int kMaxInt4K = 131072;
+constexpr int kMaxInt4N = 1 << 25;  // in tiles of 16 by workgroups of 1024: 2^31 threads of a grid's dimension
 struct Int4GemmArgs {
   const uint16_t* a;
   int a_rows;
@@ -248,8 +249,8 @@ struct Int4GemmArgs {
   int rows_to = 0;           //   and at most as many
   int vector_out = 0;        // set by the launcher: eight columns of c at once
 };
-// Experts of at most this many rows have their weights streamed, exact; more
-// rows multiply weights rounded to BF16.
+// Experts of at most this many rows have their weights streamed, exact; more rows
+// may multiply weights rounded to BF16.
 constexpr int kInt4FewRows = 64;
 hipError_t launch_gemm_int4(const Int4GemmArgs& a, hipStream_t stream);
 

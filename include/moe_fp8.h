@@ -405,7 +405,8 @@ typedef struct {
  * Errors: INVALID_ARG (sizes, null or misaligned pointers, another group,
  * scale_type or act, an odd n or, for the clamped activations, a clamp_limit
  * that is not > 0 where gated, the layouts' as moe_grouped_gemm_mxfp4),
- * UNSUPPORTED (num_experts above 1024, k above 131072, n * k at or above 2^32). */
+ * UNSUPPORTED (num_experts above 1024, k above 131072, n above 2^25, n * k at or
+ * above 2^32, a_rows * k at or above 2^37). */
 moe_status moe_gemm_int4(const uint16_t* a, int32_t rows, const int32_t* t_live_dev,
                          const moe_int4_weights* w, moe_act act, float clamp_limit, uint16_t* c,
                          void* stream);

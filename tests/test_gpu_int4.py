@@ -318,6 +318,39 @@ def test_nan_and_infinity_stay_in_their_rows(act, rows):
     assert torch.equal(out.view(torch.int16)[:, keep], clean.view(torch.int16)[:, keep])
 
 
+@pytest.mark.parametrize("rows", [4, 12, 40, 300])
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_gates_of_any_size(act, rows):
+    """The exponential's overflow and underflow: SiLU goes to 0 and to its argument."""
+    values = [0.0, 1e-30, 1.0, 20.0, 87.0, 88.5, 89.0, 100.0, 104.0, 127.0, 128.0, 150.0, 1e4, 1e15]
+    values = [x for v in values for x in (v, -v)]
+    lim = 1e3
+    codes, bits, s, z = _weights(_rng(416), (), 8, 64, 32, False, "bf16", exact=True)
+    codes[:] = 0x99  # 1
+    bits[:], s[:] = 0x3F80, 1.0
+    av = np.zeros((rows, 64))
+    for r in range(rows):
+        av[r, r * 7 % 64] = values[r % len(values)]
+    ab = _bf16(av)
+    out = moe.moe_gemm_int4(up(ab), up(codes), _scales(bits, "bf16"), act=act, clamp_limit=lim)
+    a = oracle.bf16_bits_to_f64(ab)
+    x = a.sum(1, keepdims=True)
+    gate = np.minimum(x, lim) if act == "swiglu_clamp" else x
+    with np.errstate(over="ignore"):
+        ref = gate / (1.0 + np.exp(-gate))
+    if act == "swiglu_clamp_after_silu":
+        ref = np.minimum(ref, lim)
+    u = x if act == "swiglu" else np.clip(x, -lim, lim)
+    ref = np.repeat(ref * u, 4, 1)
+    # The sums are exact; the exponential's argument is off by 2**-24 of itself at most.
+    # In fp32 it is infinite for gates below -128 ln 2 = -88.7, and SiLU zero: there
+    # |g| e**g, falling, is at most 88.8 * 2**-128 < 2**-121, times up.
+    got = oracle.bf16_bits_to_f64(down(out.view(torch.int16)))
+    bound = np.abs(ref) * (2.0 ** -8 + 2.0 ** -20 + 2.0 ** -23 * np.minimum(np.abs(gate), 200)) + 2.0 ** -126
+    bound = bound + np.where(gate < -88.7, 2.0 ** -121 * np.abs(u), 0.0)
+    assert (np.abs(got - ref) <= bound).all(), np.argwhere(~(np.abs(got - ref) <= bound))[:4]
+
+
 # ---- per expert ------------------------------------------------------------------
 
 def _aligned(counts, align):
@@ -398,6 +431,13 @@ def test_grouped_batched_layout(counts, cap):
     g = _rng(421, cap)
     _grouped(g, counts, 1, 256, 64, 64, cap=cap, zeros=True)
     _grouped(g, counts, 1, 256, 64, 32, cap=cap, act="swiglu", gather=2)
+
+
+@pytest.mark.parametrize("k,n", [(256, 64), (96, 3100)])
+def test_grouped_batched_counts_far_past_the_capacity(k, n):
+    """Every expert has its capacity's rows then, the last one too."""
+    _grouped(_rng(425, n), [9, 5000, 1 << 30, 200, 128, 130], 1, k, n, 32, cap=128, zeros=True)
+    _grouped(_rng(426, n), [5000] * 40 + [3], 1, k, n, 32, cap=66)
 
 
 @pytest.mark.parametrize("bound", [0, 1, 16, 17, 64, 65, 300])

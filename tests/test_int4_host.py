@@ -107,6 +107,8 @@ def test_gemm_validation(lib):
         assert call(**bad) == INVALID, bad
     assert call(k=131072 + 64) == UNSUPPORTED
     assert call(k=131072, n=32768) == UNSUPPORTED
+    assert call(k=64, n=(1 << 25) + 1) == UNSUPPORTED
+    assert call(k=131072, rows=1 << 20) == UNSUPPORTED
     assert call(rows=0, a=None, c=None) == OK
     assert lib.moe_gemm_int4(_p(BASE), 4, NULL, None, -1, 1.0, _p(BASE), NULL) == INVALID
 
@@ -121,6 +123,7 @@ def test_grouped_gemm_validation(lib):
                                   dict(act=0, n=63), dict(act=1, lim=0.0), dict(rc=(1 << 31) - 1)]:
         assert call(**bad) == INVALID, bad
     assert call(e=1025) == UNSUPPORTED
+    assert call(k=131072, ar=1 << 20) == UNSUPPORTED
     assert call(rc=0, a=None, c=None) == OK
     assert call(ec=0, rc=0) == OK
     # moe_act's extra value is a product's alone
