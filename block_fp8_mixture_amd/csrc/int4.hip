@@ -76,10 +76,9 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
-// Bits of the largest magnitude among the group's values with their sign bit flipped
-// by `flip` that are not negative then (0 if there is none), as a float. Floats that
-// are not negative order as their bits do, with infinity and NaN last, and negative
-// ones are negative integers, below the 0 to begin with.
+// The largest of the group's values, as a float's bits and 0 if all are negative,
+// after `flip` turned their signs or MASK took them away. Floats that are not negative
+// order as their bits do, infinity and NaN last; negative ones are negative integers.
 template <int TYPE, int LANES, typename T, uint32_t MASK>
 __device__ __forceinline__ uint32_t group_top(const Weights8<TYPE>& x, uint32_t flip) {
   T m = __builtin_bit_cast(T, (x.raw[0] ^ flip) & MASK);
