@@ -293,6 +293,11 @@ moe_status moe_int4_quant(const void* w, moe_elem_type type, int64_t rows, int32
   if (rows == 0) return MOE_OK;
   if (!w || !codes || !scales || !aligned(w, 16) || !aligned(codes, 4) || !aligned(scales, 2))
     return MOE_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(rows) * cols, w_bytes = n * (type == MOE_ELEM_FP32 ? 4 : 2);
+  if (overlap(w, w_bytes, codes, n / 2) || overlap(w, w_bytes, scales, n / group * 2) ||
+      overlap(w, w_bytes, zeros, n / group) || overlap(codes, n / 2, scales, n / group * 2) ||
+      overlap(codes, n / 2, zeros, n / group) || overlap(scales, n / group * 2, zeros, n / group))
+    return MOE_ERR_INVALID_ARG;
   moe::Int4QuantArgs a;
   a.w = w;
   a.type = type;
@@ -314,6 +319,10 @@ moe_status moe_int4_dequant(const uint8_t* codes, const uint16_t* scales, moe_el
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !out || !aligned(codes, 8) || !aligned(scales, 2) || !aligned(out, 16))
     return MOE_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(rows) * cols;
+  if (overlap(out, 2 * n, codes, n / 2) || overlap(out, 2 * n, scales, n / group * 2) ||
+      overlap(out, 2 * n, zeros, n / group))
+    return MOE_ERR_INVALID_ARG;
   return from_hip(moe::launch_int4_dequant(codes, scales, scale_type == MOE_ELEM_FP16, zeros, rows, cols,
                                            group, out, as_stream(stream)));
 }
@@ -331,6 +340,14 @@ static moe_status gemm_int4_checked(moe::Int4GemmArgs* g, const moe_int4_weights
   if (g->row_cap == 0) return MOE_OK;
   if (!g->a || g->a_rows < 1 || !g->c || !w->codes || !w->scales || !aligned(g->a, 16) ||
       !aligned(w->codes, 16) || !aligned(w->scales, 2) || !aligned(g->c, 2))
+    return MOE_ERR_INVALID_ARG;
+  const size_t nk = static_cast<size_t>(w->num_experts) * w->n * w->k, rows = g->row_cap;
+  const size_t c_bytes = 2 * rows * (act == MOE_ACT_NONE ? w->n : w->n / 2);
+  if (overlap(g->c, c_bytes, g->a, static_cast<size_t>(g->a_rows) * w->k * 2) ||
+      overlap(g->c, c_bytes, w->codes, nk / 2) || overlap(g->c, c_bytes, w->scales, nk / w->group * 2) ||
+      overlap(g->c, c_bytes, w->zeros, nk / w->group) || overlap(g->c, c_bytes, g->a_row_map, rows * sizeof(int32_t)) ||
+      overlap(g->c, c_bytes, g->counts, w->num_experts * sizeof(int32_t)) ||
+      overlap(g->c, c_bytes, g->offsets, (w->num_experts + size_t{1}) * sizeof(int32_t)))
     return MOE_ERR_INVALID_ARG;
   g->w = w->codes;
   g->scales = w->scales;

@@ -351,7 +351,8 @@ moe_status moe_rmsnorm_quant(const uint16_t* x, int64_t ld, const uint16_t* resi
  * moe_int4_dequant gives back their BF16 values, rounded once.
  *   codes 8-byte, out 16-byte aligned
  * Errors: INVALID_ARG (rows < 0, cols not a positive multiple of group, another
- * group, type or scale_type, null or misaligned pointers). */
+ * group, type or scale_type, null or misaligned pointers, an output that overlaps
+ * an input or another output). */
 moe_status moe_int4_quant(const void* w, moe_elem_type type, int64_t rows, int32_t cols, int32_t group,
                           moe_elem_type scale_type, uint8_t* codes, uint16_t* scales, uint8_t* zeros,
                           void* stream);
@@ -404,8 +405,8 @@ typedef struct {
  *               written
  * Errors: INVALID_ARG (sizes, null or misaligned pointers, another group,
  * scale_type or act, an odd n or, for the clamped activations, a clamp_limit
- * that is not > 0 where gated, the layouts' as moe_grouped_gemm_mxfp4),
- * UNSUPPORTED (num_experts above 1024, k above 131072, n above 2^25, n * k at or
+ * that is not > 0 where gated, the layouts' as moe_grouped_gemm_mxfp4, a c that
+ * overlaps an input), UNSUPPORTED (num_experts above 1024, k above 131072, n above 2^25, n * k at or
  * above 2^32, a_rows * k at or above 2^37). */
 moe_status moe_gemm_int4(const uint16_t* a, int32_t rows, const int32_t* t_live_dev,
                          const moe_int4_weights* w, moe_act act, float clamp_limit, uint16_t* c,

@@ -64,46 +64,48 @@ def test_norm_limits(lib):
 
 def test_int4_quant_validation(lib):
     f = lib.moe_int4_quant
-    a, odd = _p(BASE), _p(BASE + 2)
+    odd = _p(2 * BASE + 2)
 
-    def call(w=a, type=1, rows=4, cols=256, group=64, st=1, codes=a, scales=a, zeros=None):
+    def call(w=_p(BASE), type=1, rows=4, cols=256, group=64, st=1, codes=_p(2 * BASE), scales=_p(3 * BASE), zeros=None):
         return f(w, type, rows, cols, group, st, codes, scales, zeros, NULL)
     for bad in (dict(type=3), dict(type=-1), dict(rows=-1), dict(cols=0), dict(cols=96), dict(group=16),
                 dict(group=256), dict(group=0), dict(st=0), dict(st=3), dict(w=None), dict(codes=None),
-                dict(scales=None), dict(w=_p(BASE + 8)), dict(codes=odd), dict(scales=_p(BASE + 1)),
-                dict(rows=1 << 62)):
+                dict(scales=None), dict(w=_p(BASE + 8)), dict(codes=odd), dict(scales=_p(3 * BASE + 1)),
+                dict(rows=1 << 62), dict(codes=_p(BASE + 2044)), dict(w=_p(2 * BASE), type=0),
+                dict(scales=_p(BASE)), dict(zeros=_p(BASE)), dict(zeros=_p(2 * BASE + 511)), dict(zeros=_p(3 * BASE + 31)),
+                dict(scales=_p(2 * BASE + 510)), dict(codes=_p(BASE + 4092), type=0)):
         assert call(**bad) == INVALID, bad
     assert call(rows=0, w=None, codes=None, scales=None) == OK
 
 
 def test_int4_dequant_validation(lib):
     f = lib.moe_int4_dequant
-    a = _p(BASE)
-
-    def call(codes=a, scales=a, st=1, zeros=None, rows=4, cols=256, group=64, out=a):
+    def call(codes=_p(BASE), scales=_p(2 * BASE), st=1, zeros=None, rows=4, cols=256, group=64, out=_p(3 * BASE)):
         return f(codes, scales, st, zeros, rows, cols, group, out, NULL)
     for bad in (dict(rows=-1), dict(cols=0), dict(cols=96), dict(group=48), dict(st=0), dict(codes=None),
-                dict(scales=None), dict(out=None), dict(codes=_p(BASE + 4)), dict(out=_p(BASE + 8)),
-                dict(scales=_p(BASE + 1)), dict(rows=1 << 62)):
+                dict(scales=None), dict(out=None), dict(codes=_p(BASE + 4)), dict(out=_p(3 * BASE + 8)),
+                dict(scales=_p(2 * BASE + 1)), dict(rows=1 << 62), dict(out=_p(BASE)), dict(codes=_p(3 * BASE + 2040)),
+                dict(scales=_p(3 * BASE + 2046)), dict(zeros=_p(3 * BASE + 2047))):
         assert call(**bad) == INVALID, bad
     assert call(rows=0, codes=None, scales=None, out=None) == OK
 
 
-def _weights(codes=BASE, scales=BASE, zeros=None, st=1, group=64, e=1, n=64, k=256):
+def _weights(codes=BASE, scales=2 * BASE, zeros=None, st=1, group=64, e=1, n=64, k=256):
     return B._Int4Weights(codes, scales, zeros, st, group, e, n, k)
 
 
-WEIGHTS_INVALID = [dict(codes=None), dict(scales=None), dict(codes=BASE + 8), dict(scales=BASE + 1), dict(st=0),
+WEIGHTS_INVALID = [dict(codes=None), dict(scales=None), dict(codes=BASE + 8), dict(scales=2 * BASE + 1), dict(st=0),
                    dict(group=16), dict(group=96), dict(n=0), dict(k=0), dict(k=96), dict(e=0)]
 
 
 def test_gemm_validation(lib):
-    def call(a=_p(BASE), rows=4, act=-1, lim=1.0, c=_p(BASE), w=None, **over):
+    def call(a=_p(3 * BASE), rows=4, act=-1, lim=1.0, c=_p(4 * BASE), w=None, **over):
         return lib.moe_gemm_int4(a, rows, NULL, ctypes.byref(w or _weights(**over)), act, lim, c, NULL)
-    for bad in WEIGHTS_INVALID + [dict(a=None), dict(c=None), dict(a=_p(BASE + 8)), dict(c=_p(BASE + 1)), dict(rows=-1),
+    for bad in WEIGHTS_INVALID + [dict(a=None), dict(c=None), dict(a=_p(3 * BASE + 8)), dict(c=_p(4 * BASE + 1)), dict(rows=-1),
                                   dict(act=3), dict(act=-2), dict(act=0, n=63), dict(act=1, lim=0.0),
                                   dict(act=2, lim=float("nan")), dict(act=1, lim=-1.0), dict(e=2),
-                                  dict(rows=(1 << 31) - 1)]:
+                                  dict(rows=(1 << 31) - 1), dict(c=_p(3 * BASE + 2046)), dict(c=_p(BASE)),
+                                  dict(c=_p(2 * BASE + 510)), dict(zeros=4 * BASE + 511)]:
         assert call(**bad) == INVALID, bad
     assert call(k=131072 + 64) == UNSUPPORTED
     assert call(k=131072, n=32768) == UNSUPPORTED
@@ -114,13 +116,14 @@ def test_gemm_validation(lib):
 
 
 def test_grouped_gemm_validation(lib):
-    def call(a=_p(BASE), ar=64, div=1, counts=_p(BASE), offsets=_p(BASE), ec=0, rc=64, mr=0, act=-1, lim=1.0,
-             c=_p(BASE), e=4, **over):
+    def call(a=_p(3 * BASE), ar=64, div=1, counts=_p(5 * BASE), offsets=_p(6 * BASE), ec=0, rc=64, mr=0, act=-1, lim=1.0,
+             c=_p(4 * BASE), e=4, **over):
         return lib.moe_grouped_gemm_int4(a, ar, NULL, div, ctypes.byref(_weights(e=e, **over)), counts, offsets, ec,
                                          rc, mr, act, lim, c, NULL)
     for bad in WEIGHTS_INVALID + [dict(a=None), dict(c=None), dict(ar=-1), dict(ar=0), dict(div=0), dict(counts=None),
                                   dict(offsets=None), dict(ec=-1), dict(ec=8), dict(rc=-1), dict(mr=-1), dict(act=7),
-                                  dict(act=0, n=63), dict(act=1, lim=0.0), dict(rc=(1 << 31) - 1)]:
+                                  dict(act=0, n=63), dict(act=1, lim=0.0), dict(rc=(1 << 31) - 1), dict(c=_p(3 * BASE)),
+                                  dict(c=_p(5 * BASE + 14)), dict(c=_p(6 * BASE + 18)), dict(c=_p(BASE + 32766))]:
         assert call(**bad) == INVALID, bad
     assert call(e=1025) == UNSUPPORTED
     assert call(k=131072, ar=1 << 20) == UNSUPPORTED
