@@ -10,7 +10,6 @@
 #include "kernels.h"
 
 static_assert(MOE_MXFP4_FEW_PAIRS == moe::kL4MaxPairs);
-static_assert(MOE_INT4_EXACT_ROWS == moe::kInt4FewRows);
 static_assert(MOE_DECODE_MAX_PAIRS == moe::kDcMaxPairs && MOE_DECODE_FC2_ROW_BYTES == moe::kDcTokBytes &&
                   MOE_DECODE_FC2_MAX_SCALES == moe::kDcMaxScales &&
                   MOE_DECODE_LAYER_TOKEN_BYTES == moe::kF1TokBytesWide &&

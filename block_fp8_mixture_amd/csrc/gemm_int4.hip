@@ -69,6 +69,7 @@ __device__ __forceinline__ bool int4_find(const Int4GemmArgs& p, int u, int step
     for (int i = 0; i < kScan; ++i) tiles[i] = int4_tiles(p, e0 + 64 * i + lane, TM);
 #pragma unroll
     for (int i = 0; i < kScan; ++i) {
+      if (e0 + 64 * i >= p.num_experts) break;
       const unsigned incl = static_cast<unsigned>(wave_scan(tiles[i]));
       const unsigned all = static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(incl), 63));
       const uint64_t lanes = __ballot(want - before < incl);
@@ -339,75 +340,107 @@ __global__ __launch_bounds__(64 * W, XL == 8 ? 1 : 4) void int4_stream_kernel(In
 
 // ---- many rows per expert: tiles of BF16 rows through LDS ---------------------
 //
-// Here the matrix cores bound the product, and a sum per group outside them
-// would cost as many instructions as they have to spare. So the weights enter
-// them as the BF16 values bf16(s (q - z)) that moe_int4_dequant gives, made in
-// registers as they are needed: each rounding is 2^-9 of its weight, over K
-// weights a random error of about what the output's own rounding is.
+// The weights enter the matrix cores as the integers q - z, which BF16 holds exactly
+// (-255 .. 15). A group's sum starts from zero and is scaled into a total in fp32, so
+// what a row gets does not depend on how many other rows its expert has, but for the
+// order of a sum. (Weights rounded to BF16 before the product need no second set of
+// accumulators: 32 x 32 tiles of 16 registers in a wave's 64 or 128 rows; their error of
+// 2^-9 each made the output's 0.0022 of its root mean square, gated 0.0027, where its
+// own rounding is 0.0017.)
 //
-// A code becomes a float by v_cvt_pk_f32_fp8: the E4M3 byte 0 .. 15 stands for
-// q 2^-9. fma(q 2^-9, 2^9 s, -s z) is exact, two at a time rounded to BF16: 19
-// instructions for 8 codes, against four 32x32x16 MFMAs of 32 cycles each that
-// use them.
+// A SIMD has two waves: one alone issues an instruction of the vector unit every 4
+// cycles at most, so that those beside an MFMA of 32 cycles soon show (with registers
+// alone, 15.0 ns an MFMA; with 6 FMAs beside each 22 in one wave, 17.7 in two). Beside
+// an MFMA there are here 3.5 for the weights (4.75 with zero points), 2 for the scale in
+// groups of 128, 8 in groups of 32, and one or two for addresses.
 //
-// A workgroup of four waves owns 32 TT rows of A and 128 NT weight rows (gated: 64
-// NT columns), a wave all of the rows and 32 NT of the weight rows: a tile of few rows
-// of A and many weight rows moves the least, a weight being a quarter of an activation.
-// Both pass through LDS, the rows of A in buffers that the workgroup shares, a wave's
-// codes in its own, two steps of 128 K values each. K order: the lanes of half h hold
-// the 128 K values from 128 h of 256, so that a lane needs few scales and a row's
-// 128-byte lines are loaded whole.
+// A workgroup of eight waves owns 32 TT rows of A and 256 weight rows (gated: 128
+// columns, of a wave's 32 rows 16 gates and their 16 ups), a wave all of the rows and 32
+// of the weight rows. Both pass through LDS in steps of 128 K values, two buffers, the
+// rows of A shared, the codes a wave's own; the loads of the step after next are in
+// registers meanwhile. A step's K values are taken 32 at a time, of them 16 h + 8 t ..
+// + 7 by the lanes of half h in the t-th MFMA. The loop ends with the last group: no K
+// value past it is multiplied. A tile of at most half its rows has a loop of its own.
 //
-// Bound by the matrix cores at the clock they are left (1.7 GHz with all of them
-// busy): 2048 rows, K 7168, N 8192 take 207 us, 4096 rows to 16384 columns 773 us (1.24
-// PF; a BF16 product of the same sizes by the library 193 and 650 us).
+// Bound by the power that MFMAs, conversions and LDS reads take together (1.6 to 1.75
+// GHz, matrix cores busy 0.56): 2048 rows, K 7168, N 8192 in groups of 128 take 245
+// us, in groups of 32 with zero points 290, 4096 rows to 16384 columns 905 us (1.06 PF;
+// a BF16 product of the same sizes by the library 193 and 650 us).
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));
 
-constexpr int kTlThreads = 256;
+constexpr int kTlWaves = 8, kTlThreads = 64 * kTlWaves;
 
-__device__ __forceinline__ v16f mfma_bf16_32(uint4 a, uint4 b, v16f acc) {
+__device__ __forceinline__ v16f mfma_bf16_32(u32x4 a, uint4 b, v16f acc) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
                                                  acc, 0, 0, 0);
 }
 
-// The eight weights of a word, s9 = 2^9 s, sz = -s z, in four steps that go between
-// MFMAs.
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), bf16x2));
+}
+// The eight integers q - z of a word as BF16, in four steps that go between MFMAs.
+// ZEROS: the E4M3 byte 0 .. 15 stands for q 2^-9, and fma(q 2^-9, 2^9, -z) is exact: 19
+// instructions. Otherwise z is 8, and v_cvt_off_f32_i4 makes (q - 8) / 16 of the four
+// bits q ^ 8 in a byte's lower half: 14, and the totals are a sixteenth.
 struct Int4Unpack {
   uint32_t even, odd;
   v2f e0, e1, o0, o1;
   uint4 f;
 };
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), bf16x2));
+template <int I>
+__device__ __forceinline__ float int4_off(uint32_t c) {
+  return __builtin_amdgcn_cvt_off_f32_i4(static_cast<int>(I == 1 ? c >> 8 & 0xFFu : c >> (8 * I)));
 }
-template <int STEP>
-__device__ __forceinline__ void int4_unpack(Int4Unpack& u, uint32_t c, float s9, float sz) {
-  auto w = [&](float q) { return __builtin_fmaf(q, s9, sz); };
-  if constexpr (STEP == 0) {
-    u.even = c & 0x0F0F0F0Fu;
-    u.odd = c >> 4 & 0x0F0F0F0Fu;
-    u.e0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.even), false);
-    u.o0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.odd), false);
-  } else if constexpr (STEP == 1) {
-    u.e1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.even), true);
-    u.o1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.odd), true);
-    u.e0[0] = w(u.e0[0]);
-    u.o0[0] = w(u.o0[0]);
-    u.e0[1] = w(u.e0[1]);
-  } else if constexpr (STEP == 2) {
-    u.o0[1] = w(u.o0[1]);
-    u.f.x = pack_bf16x2(u.e0[0], u.o0[0]);
-    u.e1[0] = w(u.e1[0]);
-    u.o1[0] = w(u.o1[0]);
-    u.f.y = pack_bf16x2(u.e0[1], u.o0[1]);
+template <bool ZEROS, int STEP>
+__device__ __forceinline__ void int4_unpack(Int4Unpack& u, uint32_t c, float z) {
+  if constexpr (ZEROS) {
+    auto w = [&](float q) { return __builtin_fmaf(q, 512.0f, -z); };
+    if constexpr (STEP == 0) {
+      u.even = c & 0x0F0F0F0Fu;
+      u.odd = c >> 4 & 0x0F0F0F0Fu;
+      u.e0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.even), false);
+      u.o0 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.odd), false);
+    } else if constexpr (STEP == 1) {
+      u.e1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.even), true);
+      u.o1 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(u.odd), true);
+      u.e0[0] = w(u.e0[0]);
+      u.o0[0] = w(u.o0[0]);
+      u.e0[1] = w(u.e0[1]);
+    } else if constexpr (STEP == 2) {
+      u.o0[1] = w(u.o0[1]);
+      u.f.x = pack_bf16x2(u.e0[0], u.o0[0]);
+      u.e1[0] = w(u.e1[0]);
+      u.o1[0] = w(u.o1[0]);
+      u.f.y = pack_bf16x2(u.e0[1], u.o0[1]);
+    } else {
+      u.e1[1] = w(u.e1[1]);
+      u.o1[1] = w(u.o1[1]);
+      u.f.z = pack_bf16x2(u.e1[0], u.o1[0]);
+      u.f.w = pack_bf16x2(u.e1[1], u.o1[1]);
+    }
   } else {
-    u.e1[1] = w(u.e1[1]);
-    u.o1[1] = w(u.o1[1]);
-    u.f.z = pack_bf16x2(u.e1[0], u.o1[0]);
-    u.f.w = pack_bf16x2(u.e1[1], u.o1[1]);
+    if constexpr (STEP == 0) {
+      u.even = c ^ 0x88888888u;
+      u.odd = __builtin_amdgcn_alignbit(u.even, u.even, 4);  // (a shift would be one with those of the bytes)
+      u.e0[0] = int4_off<0>(u.even);
+      u.o0[0] = int4_off<0>(u.odd);
+    } else if constexpr (STEP == 1) {
+      u.e0[1] = int4_off<1>(u.even);
+      u.o0[1] = int4_off<1>(u.odd);
+      u.f.x = pack_bf16x2(u.e0[0], u.o0[0]);
+    } else if constexpr (STEP == 2) {
+      u.e1[0] = int4_off<2>(u.even);
+      u.o1[0] = int4_off<2>(u.odd);
+      u.f.y = pack_bf16x2(u.e0[1], u.o0[1]);
+      u.e1[1] = int4_off<3>(u.even);
+    } else {
+      u.o1[1] = int4_off<3>(u.odd);
+      u.f.z = pack_bf16x2(u.e1[0], u.o1[0]);
+      u.f.w = pack_bf16x2(u.e1[1], u.o1[1]);
+    }
   }
 }
 
@@ -446,235 +479,271 @@ __device__ __forceinline__ bool int4_tile(const Int4GemmArgs& p, int col_tiles, 
   return t->rows > 0;
 }
 
-template <int G, int TT, int NT, bool GATED>
-__global__ __launch_bounds__(kTlThreads, 1) void int4_tiled_kernel(Int4GemmArgs p) {
+template <int G, int TT, bool GATED, bool ZEROS>
+__global__ __launch_bounds__(kTlThreads, 2) void int4_tiled_kernel(Int4GemmArgs p) {
   constexpr int TM = 32 * TT;               // rows of A
-  constexpr int NC = GATED ? NT / 2 : NT;   // 32-column tiles of the output per wave
-  constexpr int AL = TM * 16 / kTlThreads;  // 16-byte loads of A per thread and step
-  constexpr int WL = 2 * NT;                // and of codes
-  constexpr int NS = 128 / G;               // scales of a lane and weight row per 256 K values
-  constexpr int kABytes = TM * 256, kWBytes = NT * 2048;  // of a step; codes: of one wave
-  __shared__ __attribute__((aligned(256))) uint8_t s_buf[2 * kABytes + 8 * kWBytes];
+  constexpr int WC = GATED ? 16 : 32;       // columns of the output per wave
+  constexpr int TN = kTlWaves * WC;
+  constexpr int NG = 128 / G;               // groups of a step
+  constexpr int kABytes = TM * 256, kWBytes = 2048;  // of a step; codes: of one wave
+  __shared__ __attribute__((aligned(256))) uint8_t s_buf[2 * kABytes + 2 * kTlWaves * kWBytes];
   __shared__ uint8_t s_some[TM];
-  uint8_t* const s_a = s_buf;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  uint8_t* const s_a = s_buf;
   uint8_t* const s_w = s_buf + 2 * kABytes + wave * (2 * kWBytes);
   const int r32 = lane & 31, h = lane >> 5;
   const int K = p.k, out_n = GATED ? p.n / 2 : p.n, groups = K / G;
   Int4Unit t;
   int tile;
-  if (!int4_tile<TM>(p, (out_n + 128 * NC - 1) / (128 * NC), &t, &tile)) return;
+  if (!int4_tile<TM>(p, (out_n + TN - 1) / TN, &t, &tile)) return;
   const int expert = __builtin_amdgcn_readfirstlane(t.expert), rows = __builtin_amdgcn_readfirstlane(t.rows);
   const int row0 = __builtin_amdgcn_readfirstlane(t.row0);
-  const int n0 = __builtin_amdgcn_readfirstlane(tile) * 128 * NC + wave * 32 * NC;
-  const int blocks = (K + 255) / 256;
+  const int n0 = __builtin_amdgcn_readfirstlane(tile) * TN;
+  const int steps = (K + 127) / 128;
 
-  // Rows of A: thread tid loads chunk tid % 16 of row tid / 16 + 16 i. Rows
-  // without a source load one that exists; their output is zero.
-  const uint16_t* a[AL];
+  // Rows of A: thread tid loads chunk tid % 16 (of 8 K values) of row tid / 16 + 32 i
+  // into slot chunk ^ row % 16: reads of a chunk of 16 rows meet no bank twice. Rows without a source load one that exists; their
+  // output is zero. Past K loads are of the row's start, unused.
+  int src[TT];
 #pragma unroll
-  for (int i = 0; i < AL; ++i) {
-    const int r = (tid >> 4) + 16 * i;
-    const int src = r < rows ? int4_source(p, row0 + r) : -1;
-    a[i] = p.a + static_cast<int64_t>(max(src, 0)) * K;
-    if ((tid & 15) == 0) s_some[r] = src >= 0;
+  for (int i = 0; i < TT; ++i) {
+    const int r = (tid >> 4) + 32 * i;
+    src[i] = r < rows ? int4_source(p, row0 + r) : -1;
   }
   const int chunk = tid & 15;
-  const int ak = 128 * (chunk >> 3) + 8 * (chunk & 7);  // its first K value of 256, in the first step
-  u32x4 ra[AL];
-  auto at_a = [&](int b, int step) {  // (past K: the row's start)
-    const int k = 256 * min(b, blocks - 1) + 64 * step + ak;
-    return k < K ? k : 0;
-  };
-  auto load_a = [&](int at, int i) { ra[i] = *reinterpret_cast<const u32x4*>(a[i] + at); };
   const int put = (tid >> 4) * 256 + ((chunk ^ ((tid >> 4) & 15)) << 4);
-  auto store_a = [&](int step, int i) {
-    *reinterpret_cast<u32x4*>(s_a + step * kABytes + put + 4096 * i) = ra[i];
-  };
-  // Fragments of A's rows of block q: K values 8 q .. of both halves' 64.
-  const int get = r32 * 256;
-  auto read_a = [&](u32x4& x, int step, int q, int m) {
-    const int at = get + (((8 * h + q) ^ (r32 & 15)) << 4);
-    x = *reinterpret_cast<const u32x4*>(s_a + step * kABytes + at + 8192 * m);
-  };
-
-  // Codes go through LDS too, each wave its own: four neighbouring lanes load 64
-  // bytes of a row, 16 rows a load (a lane with a row of its own, as the operand
-  // has it, asks for 64 lines). Chunk 2 h' + i' of a row's step, the 32 K values
-  // 128 h' + 64 step + 32 i', is in slot chunk ^ (row / 4 % 4): 16 rows' reads
-  // of a chunk meet no bank twice. Weight rows past the last take its place.
+  // Codes: four neighbouring lanes load 64 bytes of a row, 16 rows a load. Chunk c (of
+  // 32 K values) of a row is in slot c ^ (row / 4 % 4): 16 rows' reads of a chunk meet
+  // no bank twice. Weight rows past the last take its place.
   const uint8_t* wb = p.w + static_cast<int64_t>(expert) * p.n * (K / 2);
-  auto weight_row = [&](int n, int r) {
-    return static_cast<uint32_t>(min(n0 + 32 * (n % NC) + r, out_n - 1) + (GATED && n >= NC ? out_n : 0));
+  auto weight_row = [&](int r) {
+    const int col = min(n0 + WC * wave + (GATED ? r & 15 : r), out_n - 1);
+    return static_cast<uint32_t>(GATED && r >= 16 ? col + out_n : col);
   };
-  uint32_t wo[WL];
+  uint32_t wo[2];
 #pragma unroll
-  for (int k = 0; k < WL; ++k) wo[k] = weight_row(k >> 1, 16 * (k & 1) + (lane >> 2)) * static_cast<uint32_t>(K / 2);
+  for (int k = 0; k < 2; ++k) wo[k] = weight_row(16 * k + (lane >> 2)) * static_cast<uint32_t>(K / 2);
   const int wchunk = (lane & 3) ^ (lane >> 4);
-  u32x4 rw[WL];
-  auto at_w = [&](int b, int step) {  // (past K: the row's start)
-    const uint32_t at = 128 * min(b, blocks - 1) + 32 * step + 64 * (wchunk >> 1) + 16 * (wchunk & 1);
-    return 2 * at < static_cast<uint32_t>(K) ? at : 0u;
-  };
-  auto load_w = [&](uint32_t at, int k) { rw[k] = *reinterpret_cast<const u32x4*>(wb + (wo[k] + at)); };
-  auto store_w = [&](int step, int k) {
-    *reinterpret_cast<u32x4*>(s_w + step * kWBytes + 1024 * k + 16 * lane) = rw[k];
-  };
-  u32x4 w[2][NT];  // by the chunk's parity
-  auto read_w = [&](u32x4& to, int step, int ii, int n) {
-    const int at = r32 * 64 + (((2 * h + ii) ^ (r32 >> 2 & 3)) << 4);
-    to = *reinterpret_cast<const u32x4*>(s_w + step * kWBytes + 2048 * n + at);
-  };
-
-  // A lane's scale in use, and the next as stored. Columns past K have the scale
-  // zero: A's row is read from its start there. Selects go by masks: branches
-  // would cut the MFMAs' schedule. Without zero points the loads read bytes of
-  // the scales, unused.
   const uint16_t* sb = p.scales + static_cast<int64_t>(expert) * p.n * groups;
-  const uint8_t* zb = p.zeros ? p.zeros + static_cast<int64_t>(expert) * p.n * groups
-                              : reinterpret_cast<const uint8_t*>(sb);
-  uint32_t so[NT], sc[NT], zr[NT];
-  float s9[NT], sz[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) so[n] = weight_row(n, r32) * static_cast<uint32_t>(groups);
-  uint32_t is_f16 = p.scale_f16 ? ~0u : 0u, has_z = p.zeros ? ~0u : 0u;
-  asm volatile("" : "+v"(is_f16), "+v"(has_z));
-  auto load_s = [&](int n, int k) {
-    const uint32_t at = so[n] + min((k + 128 * h) / G, groups - 1);
-    sc[n] = sb[at];
-    zr[n] = zb[at];
+  const uint8_t* zb = ZEROS ? p.zeros + static_cast<int64_t>(expert) * p.n * groups : nullptr;
+  const uint32_t so = weight_row(r32) * static_cast<uint32_t>(groups);
+  const uint16_t* a[TT];
+  u32x4 ra[TT], rw[2];
+  int ka = 0;
+  uint32_t kw = 0;
+  auto at = [&](int step) __attribute__((always_inline)) {
+    const int k = 128 * min(step, steps - 1);
+    ka = k + 8 * chunk < K ? k + 8 * chunk : 0;
+    kw = k + 32 * wchunk < K ? k / 2 + 16 * wchunk : 0;
   };
-  auto use_s = [&](int n, int k) {
-    const uint32_t half = __float_as_uint(static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(sc[n]))));
-    const uint32_t bits = (half & is_f16) | (sc[n] << 16 & ~is_f16);
-    const uint32_t keep = static_cast<uint32_t>((k + 128 * h - K) >> 31);
-    const float s = __uint_as_float(bits & keep);
-    s9[n] = s * 512.0f;
-    sz[n] = -s * static_cast<float>((zr[n] & has_z) | (8u & ~has_z));
+  // Pieces of a step: TT of the rows, two of the codes.
+  auto load = [&](int i) __attribute__((always_inline)) {
+    if (i < TT) ra[i] = *reinterpret_cast<const u32x4*>(a[i] + ka);
+    else rw[i - TT] = *reinterpret_cast<const u32x4*>(wb + (wo[i - TT] + kw));
+  };
+  auto store = [&](int buf, int i) __attribute__((always_inline)) {
+    if (i < TT) *reinterpret_cast<u32x4*>(s_a + buf * kABytes + put + 8192 * i) = ra[i];
+    else *reinterpret_cast<u32x4*>(s_w + buf * kWBytes + 1024 * (i - TT) + 16 * lane) = rw[i - TT];
+  };
+  // Scales and zero points as stored, of a whole step's groups at once: the address path
+  // handles a line for every weight row, however few of its bytes are asked for (a load
+  // per group: 300 rows 7168 -> 4096 gated in groups of 32 with zero points 136 us).
+  struct Scales {
+    uint32_t s[(NG + 1) / 2], z;
+  };
+  const int whole = K / 128;
+  uint32_t is_f16 = p.scale_f16 ? ~0u : 0u;  // (branches would cut the MFMAs' schedule)
+  asm volatile("" : "+v"(is_f16));
+  auto load_s = [&](Scales& to, int step) __attribute__((always_inline)) {
+    const uint32_t g = so + min(step, whole - 1) * NG;
+    if constexpr (NG == 1) {
+      to.s[0] = sb[g];
+      if constexpr (ZEROS) to.z = zb[g];
+    } else {
+      __builtin_memcpy(to.s, sb + g, 2 * NG);
+      if constexpr (ZEROS) __builtin_memcpy(&to.z, zb + g, NG);
+    }
+  };
+  auto scale_of = [&](uint32_t bits) __attribute__((always_inline)) {
+    const uint32_t half = __float_as_uint(static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits))));
+    return __uint_as_float((half & is_f16) | (bits << 16 & ~is_f16));
+  };
+  auto scale = [&](const Scales& r, int i) __attribute__((always_inline)) { return scale_of(r.s[i / 2] >> (16 * (i & 1))); };
+  auto zero = [&](const Scales& r, int i) __attribute__((always_inline)) {
+    return ZEROS ? static_cast<float>(r.z >> (8 * i) & 0xFFu) : 0.0f;
+  };
+  // K values 16 j .. of a step lie in chunks 4 (j / 2) + 2 h + j % 2: the slot's bits of j
+  // are one exclusive or with the first one's.
+  const uint32_t fa = r32 * 256 + (((2 * h) ^ (r32 & 15)) << 4), fw = r32 * 64 + ((r32 >> 2 & 3) << 4) + 8 * h;
+  auto codes = [&](int buf, int c) __attribute__((always_inline)) {
+    return *reinterpret_cast<const uint2*>(s_w + ((fw + buf * kWBytes) ^ (c << 4)));
+  };
+  auto fragment = [&](int buf, int j, int m) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(s_a + ((fa + buf * kABytes) ^ ((4 * (j >> 1) + (j & 1)) << 4)) + 8192 * m);
   };
 
-  v16f acc[NT][TT];
+  constexpr int KS = G / 16;  // MFMAs of a group and row tile
+  v16f total[TT], acc[TT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int m = 0; m < TT; ++m) total[m] = acc[m] = v16f{};
+  auto add = [&](int m, float s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int m = 0; m < TT; ++m) acc[n][m] = v16f{};
+    for (int v = 0; v < 16; ++v) total[m][v] = __builtin_fmaf(s, acc[m][v], total[m][v]);
+  };
 
-  int aa = at_a(0, 0);
-  uint32_t aw = at_w(0, 0);
+  // The weights ahead of what waits for the rows' numbers.
+  at(0);
 #pragma unroll
-  for (int i = 0; i < AL; ++i) load_a(aa, i);
+  for (int i = TT; i < TT + 2; ++i) load(i);
+  Scales now{}, next{};
+  if (whole > 0) load_s(now, 0);
 #pragma unroll
-  for (int k = 0; k < WL; ++k) load_w(aw, k);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) load_s(n, 0);
-  aa = at_a(0, 1);
-  aw = at_w(0, 1);
-#pragma unroll
-  for (int i = 0; i < AL; ++i) {
-    store_a(0, i);
-    load_a(aa, i);
+  for (int i = 0; i < TT; ++i) {
+    a[i] = p.a + static_cast<int64_t>(max(src[i], 0)) * K;
+    if ((tid & 15) == 0) s_some[(tid >> 4) + 32 * i] = src[i] >= 0;
+    load(i);
   }
+  at(1);
 #pragma unroll
-  for (int k = 0; k < WL; ++k) {
-    store_w(0, k);
-    load_w(aw, k);
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    use_s(n, 0);
-    load_s(n, NS > 1 ? G : 256);
+  for (int i = 0; i < TT + 2; ++i) {
+    store(0, i);
+    load(i);
   }
   lds_barrier();
-  u32x4 x[2][TT];
+  // The first LT row tiles have rows.
+  auto sums = [&](auto live_tiles) __attribute__((always_inline)) {
+    constexpr int LT = live_tiles;
+    float s_done = 0.0f, s_now = scale(now, 0), z = zero(now, 0);
+    if (whole > 0) load_s(next, 1);
+    u32x4 x[2][LT];
 #pragma unroll
-  for (int m = 0; m < TT; ++m) read_a(x[0][m], 0, 0, m);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) read_w(w[0][n], 0, 0, n);
-  Int4Unpack u[2];  // the weights in use and the next tile's
-  static_for<4>([&](auto k) __attribute__((always_inline)) { int4_unpack<k>(u[0], w[0][0][0], s9[0], sz[0]); });
-  for (int b = 0; b < blocks; ++b) {
-    // 16 blocks of 8 K values per half, 8 a step: the MFMAs of a weight tile go
-    // between the instructions that make the next tile's weights, so that neither
-    // waits for the other. The loads and LDS writes are spread over the blocks
-    // (in bursts the waves wait for each other's, with the matrix cores idle): a
-    // register is written to the next step's buffer and loaded for the step after
-    // it (past the end: the last ones again, unused).
-    static_for<16>([&](auto block) __attribute__((always_inline)) {
-      constexpr int step = block / 8, q = block % 8, i = block / 4, j = block % 4;
-      if constexpr (q == 0) {
-        aa = at_a(b + 1, step);
-        aw = at_w(b + 1, step);
-      }
-      if constexpr (q == 7) lds_barrier();
-      // Slot k: an MFMA and what goes beside it, in this order.
-      static_for<NT * TT>([&](auto k) __attribute__((always_inline)) {
-        constexpr int n = k / TT, m = k % TT, slot = block * NT + n;
-        acc[n][m] = mfma_bf16_32(u[slot & 1].f, __builtin_bit_cast(uint4, x[q & 1][m]), acc[n][m]);
-        // The rows' fragments of the next block, and the next chunk of codes.
-        if constexpr (k < TT) read_a(x[(q + 1) & 1][k], q == 7 ? step ^ 1 : step, (q + 1) & 7, k);
-        if constexpr (j == 3 && k >= TT && k < TT + NT)
-          read_w(w[(i + 1) & 1][k - TT], q < 4 ? step : step ^ 1, (i + 1) & 1, k - TT);
-        // Pieces of A and of the codes, in the last block none: it reads the next
-        // step's, past a barrier.
-        constexpr int kPieces = AL + WL, kMost = 2 * ((kPieces + 6) / 7);  // slots that a block's take
-        constexpr int kHalf = NT * TT / 2 < NT * TT - kMost ? NT * TT / 2 : NT * TT - kMost;
-        static_assert(kHalf >= 0, "a block's pieces fit its slots");
-        constexpr int p0 = q * kPieces / 7, p1 = q < 7 ? (q + 1) * kPieces / 7 : p0;
-        constexpr int piece = p0 + (k - kHalf) / 2;
-        if constexpr (k >= kHalf && piece < p1) {
-          if constexpr ((k - kHalf) % 2 == 0) {
-            if constexpr (piece < AL) store_a(step ^ 1, piece);
-            else store_w(step ^ 1, piece - AL);
+    for (int m = 0; m < LT; ++m) x[0][m] = fragment(0, 0, m);
+    uint2 q[2] = {codes(0, 0), uint2{0, 0}};
+    Int4Unpack u[2];
+    static_for<4>([&](auto k) __attribute__((always_inline)) { int4_unpack<ZEROS, k>(u[0], q[0].x, z); });
+    for (int step = 0; step < whole; ++step) {
+      const int buf = step & 1;
+      at(step + 2);  // (past the end: the last ones again, unused)
+      static_for<8>([&](auto jj) __attribute__((always_inline)) {
+        constexpr int j = jj;
+        // The next step's rows are in the other buffer, and this one's read.
+        if constexpr (j == 7) lds_barrier();
+        static_for<LT>([&](auto mm) __attribute__((always_inline)) {
+          constexpr int m = mm;
+          // The group before this one is complete: its sums, scaled.
+          if constexpr (j % KS == 0) {
+            add(m, s_done);
+            acc[m] = mfma_bf16_32(x[j & 1][m], u[j & 1].f, v16f{});
           } else {
-            if constexpr (piece < AL) load_a(aa, piece);
-            else load_w(aw, piece - AL);
+            acc[m] = mfma_bf16_32(x[j & 1][m], u[j & 1].f, acc[m]);
           }
-        }
-        // The last of a scale's weights were made in the slot before: the next
-        // scale, and the load of the one after it.
-        if constexpr (m == 0 && j == 3 && (i + 1) % (4 / NS) == 0) {
-          constexpr int to = (i + 1) / (4 / NS), after = to + 1;
-          use_s(n, 256 * (b + to / NS) + G * (to % NS));
-          load_s(n, 256 * (b + after / NS) + G * (after % NS));
-        }
-        constexpr int nn = (n + 1) % NT, ni = n + 1 < NT ? i : (i + (j == 3)) & 3, nj = n + 1 < NT ? j : (j + 1) & 3;
-        static_for<4 / TT>([&](auto l) __attribute__((always_inline)) {
-          int4_unpack<4 / TT * m + l>(u[(slot + 1) & 1], w[ni & 1][nn][nj], s9[nn], sz[nn]);
+          x[(j + 1) & 1][m] = fragment(j == 7 ? buf ^ 1 : buf, (j + 1) & 7, m);
+          if constexpr (j % 2 == 0 && m == 0) q[(j / 2 + 1) & 1] = codes(j == 6 ? buf ^ 1 : buf, (j / 2 + 1) & 3);
+          // The scale of the next group, and the load of those two steps on.
+          if constexpr ((j + 1) % KS == 0 && m == 0) {
+            constexpr int g = (j + 1) / KS % NG;
+            if constexpr (g == 0 && NG > 1) {
+              now = next;
+              // (copies, before the registers are loaded again: else the load would be
+              // waited for, to be copied)
+              for (uint32_t& w : now.s) asm volatile("" : "+v"(w));
+              if constexpr (ZEROS) asm volatile("" : "+v"(now.z));
+            }
+            s_done = s_now;
+            s_now = scale(NG > 1 ? now : next, g);
+            z = zero(NG > 1 ? now : next, g);
+            if constexpr (g == 0) load_s(next, step + 2);
+          }
+          constexpr int half = ((j + 1) / 2) & 1;
+          static_for<4 / LT>([&](auto l) __attribute__((always_inline)) {
+            int4_unpack<ZEROS, 4 / LT * m + l>(u[(j + 1) & 1], (j + 1) & 1 ? q[half].y : q[half].x, z);
+          });
+          // A piece of the next step's data, and its register's next load.
+          constexpr int piece = j < LT ? j : j - LT + TT;
+          if constexpr (piece < TT + 2 && m == (LT == 4 ? 1 : 0)) store(buf ^ 1, piece);
+          if constexpr (piece < TT + 2 && m == (LT == 4 ? 2 : LT - 1)) load(piece);
+          __builtin_amdgcn_sched_barrier(0);
         });
-        __builtin_amdgcn_sched_barrier(0);
       });
-    });
-  }
+    }
+#pragma unroll
+    for (int m = 0; m < LT; ++m) add(m, s_done);
+    // The last groups, where they are not a whole step.
+    if constexpr (NG > 1) {
+      const int buf = whole & 1;
+      for (int g = whole * NG; g < groups; ++g) {
+        const float s = scale_of(sb[so + g]);
+        if constexpr (ZEROS) z = static_cast<float>(zb[so + g]);
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          const int at_j = (g - whole * NG) * KS + j;
+          const uint2 w = codes(buf, at_j >> 1);
+          static_for<4>([&](auto k) __attribute__((always_inline)) { int4_unpack<ZEROS, k>(u[0], at_j & 1 ? w.y : w.x, z); });
+#pragma unroll
+          for (int m = 0; m < LT; ++m) acc[m] = mfma_bf16_32(fragment(buf, at_j, m), u[0].f, j == 0 ? v16f{} : acc[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < LT; ++m) add(m, s);
+      }
+    }
+  };
+  if (rows > 16 * TT)
+    sums(std::integral_constant<int, TT>{});
+  else
+    sums(std::integral_constant<int, TT / 2>{});
 
-  // Output, through LDS so that a row's columns leave in whole lines. A lane
-  // holds weight rows 8 v + 4 h .. + 3 (v = 0 .. 3) of its row of A; a wave's
-  // rows of 32 NC columns lie in chunks of 8 columns, chunk c in slot c ^ row % 16
-  // (of rows half or a quarter as long c ^ row / 2 % 8, c ^ row / 4 % 4).
-  constexpr int kRow = 64 * NC, kChunks = 4 * NC;
-  static_assert(4 * TM * kRow <= 2 * kABytes + 8 * kWBytes && (NC == 4 || NC == 2 || NC == 1), "");
-  lds_barrier();  // other waves still read A's rows
-  uint8_t* const s_c = s_buf + wave * (TM * kRow);
-  auto slot = [&](int c, int row) { return (c ^ (NC == 4 ? row & 15 : NC == 2 ? row >> 1 & 7 : row >> 2 & 3)) << 4; };
+  // Output, through LDS so that a row's columns leave in whole lines. A lane holds its
+  // column's rows 8 v + 4 h + k of 32 (v, k = 0 .. 3). Gated: lanes 0 .. 15 and 32 ..
+  // hold gates, the others ups of the same columns; of two rows, the first half gets
+  // the first's gate and up, the second half the second's. Then neighbouring columns
+  // exchange one of two rows, so that a lane writes two columns of one. Chunk c of 8
+  // columns of a row is in slot c ^ 4 f, f telling apart the four rows of a write.
+  constexpr int kRow = 2 * TN;
+  static_assert(TM * kRow <= 2 * kABytes, "");
+  uint8_t* const s_c = s_buf;
+  lds_barrier();  // the rows are read
+  auto write = [&](int row, int col, float v0, float v1) __attribute__((always_inline)) {
+    // v0, v1: this column's values of rows row and row + step of the pair
+    const bool odd = lane & 1;
+    const float other = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(odd ? v0 : v1), 0xB1, 0xF, 0xF, false));
+    const uint32_t two = odd ? pack_bf16x2(other, v1) : pack_bf16x2(v0, other);
+    const int r = row + (odd ? (GATED ? 2 : 1) : 0), f = (GATED ? r >> 1 & 1 : r & 1) | (GATED ? (r & 1) << 1 : r >> 1 & 2);
+    const int at = 2 * (col & ~1);
+    *reinterpret_cast<uint32_t*>(s_c + r * kRow + ((at >> 4 ^ (f << 2)) << 4) + (at & 15)) = two;
+  };
 #pragma unroll
   for (int m = 0; m < TT; ++m) {
+    if (32 * m >= rows) break;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
+    for (int v = 0; v < 4; ++v) {
+      float o[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        v4f o;
+      for (int k = 0; k < 4; ++k) o[k] = ZEROS ? total[m][4 * v + k] : 16.0f * total[m][4 * v + k];
+      const int row = 32 * m + 8 * v + 4 * h;
+      if constexpr (GATED) {
+        float g[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          o[k] = acc[n][m][4 * v + k];
-          if constexpr (GATED) o[k] = int4_gated(p.act, o[k], acc[n + NC][m][4 * v + k], p.limit);
+        for (int k = 0; k < 2; ++k) {
+          const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(o[2 * k]), __float_as_uint(o[2 * k + 1]), false, false);
+          g[k] = int4_gated(p.act, __uint_as_float(both[0]), __uint_as_float(both[1]), p.limit);
         }
-        *reinterpret_cast<uint2*>(s_c + (32 * m + r32) * kRow + slot(4 * n + v, r32) + 8 * h) = pack_bf16x4(o);
+        write(row + (r32 >> 4), 16 * wave + (r32 & 15), g[0], g[1]);
+      } else {
+        write(row, 32 * wave + r32, o[0], o[1]);
+        write(row + 2, 32 * wave + r32, o[2], o[3]);
       }
     }
   }
-  const int c = lane % kChunks, col = n0 + 8 * c;
-  for (int r = lane / kChunks; r < rows; r += 64 / kChunks) {
-    uint4 bits = *reinterpret_cast<const uint4*>(s_c + r * kRow + slot(c, r));
+  lds_barrier();
+  constexpr int kChunks = TN / 8;
+  const int c = tid % kChunks, col = n0 + 8 * c;
+#pragma unroll
+  for (int i = 0; i < TM * kChunks / kTlThreads; ++i) {
+    const int r = tid / kChunks + i * (kTlThreads / kChunks);
+    const int f = (GATED ? r >> 1 & 1 : r & 1) | (GATED ? (r & 1) << 1 : r >> 1 & 2);
+    uint4 bits = *reinterpret_cast<const uint4*>(s_c + r * kRow + ((c ^ (f << 2)) << 4));
     if (!s_some[r]) bits = uint4{0, 0, 0, 0};
+    if (r >= rows) continue;
     uint16_t* to = p.c + static_cast<int64_t>(row0 + r) * out_n + col;
     if (p.vector_out) {
       if (col < out_n) *reinterpret_cast<uint4*>(to) = bits;
@@ -726,32 +795,37 @@ hipError_t stream_rows(const Int4GemmArgs& p, int bound, int to, hipStream_t str
   return stream_launch<G, 8, 2, 8, GATED>(p, over, to, stream);
 }
 
-template <int G, int TT, int NT, bool GATED>
+template <int G, int TT, bool GATED>
 hipError_t tiled_launch(Int4GemmArgs p, hipStream_t stream) {
-  constexpr int TM = 32 * TT, NC = GATED ? NT / 2 : NT;
+  constexpr int TM = 32 * TT, TN = kTlWaves * (GATED ? 16 : 32);
   p.rows_over = kInt4FewRows;
   p.rows_to = INT32_MAX;
   const int out_n = GATED ? p.n / 2 : p.n;
   const int64_t fit = p.row_cap / (kInt4FewRows + 1), used = p.num_experts < fit ? p.num_experts : fit;
   const int64_t units = p.counts ? p.row_cap / TM + used : (p.row_cap + TM - 1) / TM;
   // A multiple of 8: every XCD's share rounded up.
-  const int64_t tasks = (units * ((out_n + 128 * NC - 1) / (128 * NC)) + 7) / 8 * 8;
-  hipLaunchKernelGGL((int4_tiled_kernel<G, TT, NT, GATED>), flat_grid(tasks), dim3(kTlThreads), 0, stream, p);
+  const int64_t tasks = (units * ((out_n + TN - 1) / TN) + 7) / 8 * 8;
+  if (p.zeros)
+    hipLaunchKernelGGL((int4_tiled_kernel<G, TT, GATED, true>), flat_grid(tasks), dim3(kTlThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((int4_tiled_kernel<G, TT, GATED, false>), flat_grid(tasks), dim3(kTlThreads), 0, stream, p);
   return hipGetLastError();
 }
 
 // Expected time, us, of the forms that more than kInt4FewRows rows can take, by
 // the tiles that there are for each CU (r). Tiled forms: a superstep of 256 K
-// values takes 2.4 us a round of 64 x 256 tiles, 3 to 4 of 128 x 256 ones and 4.7
-// to 7.3 of 128 x 512 ones (the more the fuller the chip, whose clock falls), and
-// some 5 us go around it; streamed tiles of 32 x 32 take 2.5 us and 0.2 for every
-// 128 K values. Measured (streamed, 64 x 256, 128 x 256, 128 x 512), us, for rows,
-// K, N: 300, 6144, 1000: 30, 57, 70, 125; 70, 4096, 4096: 15, 38, 46, 79; 300,
-// 2048, 7168: 56, 24, 30, 49; 300, 7168, 4096 gated: 68, 65, 83, 144; 512, 4096,
-// 4096: -, 42, 51, 84; 1024, 4096, 4096: 134, 51, 54, 86; 1024, 2048, 7168: -, 41,
-// 36, 52; 2048, 4096, 4096: -, 85, 70, 92; 2048, 7168, 8192: -, 276, 226, 207.
+// values takes 1.8 to 2.25 us a round of 64 x 256 tiles, 2.65 to 3.85 of 128 x 256
+// ones (the more the fuller the chip, whose clock falls), and 6 or 7 us go around it;
+// streamed tiles of 32 x 32 take 2.5 us and 0.2 for every 128 K values. Over several
+// experts the last tiles are of fewer rows: a last round costs what it holds. Measured
+// (streamed, 64 x 256, 128 x 256), us, for rows, K, N in groups of 128: 300, 6144, 1000:
+// 26, 48, 73; 70, 4096, 4096: 18, 35, 51; 300, 2048, 7168: 58, 22, 30; 300, 7168, 4096
+// gated: 70, 57, 87; 512, 4096, 4096: 79, 38, 53; 1024, 4096, 4096: 137, 42, 55; 1024,
+// 2048, 7168: -, 43, 36; 2048, 4096, 4096: 261, 87, 70; 2048, 7168, 8192: -, 306, 251.
+// Smaller groups and zero points take all three longer alike: groups of 32 with zero
+// points by a third to a half.
 struct Int4Costs {
-  double stream, small, medium, large;
+  double stream, small, medium;
 };
 Int4Costs int4_costs(const Int4GemmArgs& p, int out_n, int gated) {
   const double cus = device_cu_count(), blocks = (p.k + 255) / 256;
@@ -761,10 +835,11 @@ Int4Costs int4_costs(const Int4GemmArgs& p, int out_n, int gated) {
   auto units = [&](int tm) { return p.num_experts > 1 ? experts * (mean / tm + 0.5) : ceil(p.row_cap / static_cast<double>(tm)); };
   auto cols = [&](int c) { return ceil(out_n / static_cast<double>(gated ? c / 2 : c)); };
   auto fill = [](double r) { return r < 1.0 ? r : 1.0; };
+  auto rounds = [&](double r) { return p.num_experts > 1 ? (r + 0.3 > 1.0 ? r + 0.3 : 1.0) : ceil(r); };
   const double rs = units(32) * cols(32) / cus, r2 = units(64) * cols(256) / cus;
-  const double r4 = units(128) * cols(256) / cus, r8 = units(128) * cols(512) / cus;
-  return {ceil(rs) * (2.5 + 0.4 * blocks), 5.0 + blocks * 2.4 * ceil(r2),
-          5.0 + blocks * ceil(r4) * (3.0 + fill(r4)), 5.0 + blocks * ceil(r8) * (4.7 + 2.6 * fill(r8))};
+  const double r4 = units(128) * cols(256) / cus;
+  return {ceil(rs) * (2.5 + 0.4 * blocks), 6.0 + blocks * rounds(r2) * (1.8 + 0.45 * fill(r2)),
+          7.0 + blocks * rounds(r4) * (2.65 + 1.2 * fill(r4))};
 }
 
 template <int G, bool GATED>
@@ -774,15 +849,13 @@ hipError_t gemm_launch(Int4GemmArgs p, hipStream_t stream) {
   // (a count past the bound is computed all the same)
   if (p.max_rows_per_expert <= kInt4FewRows) return stream_rows<G, GATED>(p, p.max_rows_per_expert, INT32_MAX, stream);
   const Int4Costs t = int4_costs(p, out_n, GATED);
-  if (t.stream <= t.small && t.stream <= t.medium && t.stream <= t.large)
+  if (t.stream <= t.small && t.stream <= t.medium)
     return stream_rows<G, GATED>(p, p.max_rows_per_expert, INT32_MAX, stream);
   if (p.counts) {
     const hipError_t e = stream_rows<G, GATED>(p, kInt4FewRows, kInt4FewRows, stream);
     if (e != hipSuccess) return e;
   }
-  if (t.small <= t.medium && t.small <= t.large) return tiled_launch<G, 2, 2, GATED>(p, stream);
-  if (t.medium <= t.large) return tiled_launch<G, 4, 2, GATED>(p, stream);
-  return tiled_launch<G, 4, 4, GATED>(p, stream);
+  return t.small <= t.medium ? tiled_launch<G, 2, GATED>(p, stream) : tiled_launch<G, 4, GATED>(p, stream);
 }
 
 template <int G>

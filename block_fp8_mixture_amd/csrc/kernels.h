@@ -249,8 +249,8 @@ struct Int4GemmArgs {
   int rows_to = 0;           //   and at most as many
   int vector_out = 0;        // set by the launcher: eight columns of c at once
 };
-// Experts of at most this many rows have their weights streamed, exact; more rows
-// may multiply weights rounded to BF16.
+// Experts of at most this many rows have their weights streamed; more rows may be
+// computed in tiles.
 constexpr int kInt4FewRows = 64;
 hipError_t launch_gemm_int4(const Int4GemmArgs& a, hipStream_t stream);
 

@@ -372,23 +372,23 @@ typedef struct {
   int32_t k;                /* a multiple of group */
 } moe_int4_weights;
 
-#define MOE_INT4_EXACT_ROWS 64
+/* Live rows of an expert up to which the products' weights are exact: any number. */
+#define MOE_INT4_EXACT_ROWS INT32_MAX
 
 /* Product of BF16 rows with 4-bit integer weights (not quantizing the rows):
  *   S[r, n] = sum_g s[n, g] * sum_{j in group g} a[r, j] * (q[n, j] - z[n, g])
  *   act MOE_ACT_NONE:  c[r, n] = bf16(S[r, n])
  *   otherwise, with N = n / 2 (moe_act's formulas, in fp32):
  *                      c[r, i] = bf16(act(gate = S[r, i], up = S[r, N + i]))
- * Sums are in fp32, rounded once. For at most MOE_INT4_EXACT_ROWS live rows of
- * an expert, and for more where that is expected to be faster, the weights are
- * exact: a group's sum is taken as sum a (16 + q) - (16 + z) sum a and scaled then
- * (fp32 must hold 31 times a group's sum of magnitudes). Otherwise they enter the
- * matrix cores as moe_int4_dequant's BF16 values, which adds about as much as the
- * output's own rounding; scales are below 2^118 in magnitude there. Which of the
- * two, and the order of a sum, goes by n, k, num_experts, the rows and
- * max_rows_per_expert: the same call gives the same bits. A NaN in a row of a makes
- * every sum of the row NaN, an infinity makes it that or an infinity; a NaN passes
- * the clamps. Any n >= 1 (even where gated) and any number of rows.
+ * The weights are exact whatever the number of rows; sums are in fp32, a group's before
+ * it is scaled, and rounded once. For at most 64 live rows of an expert, and for more
+ * where that is expected to be faster, a group's sum is taken as sum a (16 + q) - (16 +
+ * z) sum a (fp32 must hold 31 times a group's sum of magnitudes, and an infinity in a
+ * makes it a NaN), otherwise as it stands. Which of the two, and the order of a sum,
+ * goes by n, k, num_experts, the rows and max_rows_per_expert: the same call gives the
+ * same bits. A NaN in a row of a makes every sum of the row NaN, an infinity makes it
+ * that or an infinity; a NaN passes the clamps. Any n >= 1 (even where gated) and any
+ * number of rows.
  *
  * moe_gemm_int4: one matrix (num_experts = 1).
  *   a           device BF16 [rows, k], 16-byte aligned
