@@ -358,9 +358,9 @@ def moe_rmsnorm_quant(x, weight, eps=1e-6, fmt="fp32", residual=None, t_live=Non
     """RMS norm of x [t_cap, H] BF16 (columns contiguous, rows a multiple of 8
     elements apart) with the residual's addition and the quantization of its
     output. Returns (y BF16 [t_cap, H], xq, xs, residual_out): xq and xs as
-    moe_act_quant(y, fmt) (None with ``fmt=None``), residual_out BF16 x + residual
-    (None without a residual). ``y=False``: no BF16 output (None). residual_out
-    may be ``residual`` itself."""
+    moe_act_quant(y, fmt) (None with ``fmt=None``; FP8 codes keep a NaN here),
+    residual_out BF16 x + residual (None without a residual). ``y=False``: no BF16
+    output (None). residual_out may be ``residual`` itself."""
     lib = load_library()
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a tensor")

@@ -3,9 +3,10 @@
 // without a residual),
 //   y = bf16( fl32( h / sqrt(mean(h^2) + eps) * weight ) ),
 // the middle in 64 bits, and the codes and scales of y as moe_act_quant makes
-// them. The norm is of the stored sum and the codes are of the stored y, so the
-// fused pass gives what the three passes in a row give; in 64 bits the order of
-// the row's sum does not reach y's rounding.
+// them (but for NaN, which FP8 codes keep here). The norm is of the stored sum and the
+// codes are of the stored y, so the fused pass gives what the three passes in a row
+// give where y is finite; in 64 bits the order of the row's sum does not reach y's
+// rounding.
 //
 // A workgroup owns a row. A thread holds 8-column vectors in registers, so the
 // row is read once; 16 neighbouring lanes hold a 128-column group, as in the

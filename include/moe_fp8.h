@@ -301,9 +301,13 @@ moe_status moe_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_
  *   (xq, xs) = moe_act_quant(y, fmt, rounding)
  * The addition is in fp32; the mean, the root and the products in double,
  * rounded once to fp32 and then to BF16. y is what its codes are made of, so
- * the results are those of an addition, a norm and moe_act_quant in a row. A
- * row with a NaN or an infinity in h gives NaN where the formula does; in FP8
- * a NaN gets E4M3's NaN code (the group's scale goes by the other values).
+ * the results are those of an addition, a norm and moe_act_quant in a row,
+ * but for what is not finite in y and quantized to FP8: a NaN gets E4M3's NaN
+ * code here and a finite one in moe_act_quant, and so may every value of a
+ * group with an infinity, whose scale is infinite (what its codes stand for is
+ * NaN or an infinity either way). Scales are the same; a group's goes by its
+ * values that are no NaN. A row with a NaN or an infinity in h gives NaN where
+ * the formula does.
  *
  *   x            device BF16 [t_cap, hidden], rows `ld` elements apart
  *   residual     device BF16 [t_cap, hidden] or NULL
