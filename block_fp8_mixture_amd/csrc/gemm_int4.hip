@@ -122,7 +122,7 @@ __device__ __forceinline__ int int4_units(const Int4GemmArgs& p) {
 // how long its code takes to arrive.
 //
 // Bound by latency up to some 20 MB of weights (a launch, the first loads, LDS, the
-// sums), beyond by the weights' bytes: 1 row 7168 -> 4096 gated 9 us, 16 rows 2048 ->
+// sums), beyond by the weights' bytes; captured, with cold weights: 1 row 7168 -> 4096 gated 9 us, 16 rows 2048 ->
 // 7168 8 us, 1 token's 8 experts 4096 -> 1024 12.5 us, 64 tokens' 256 experts 6144 ->
 // 512 (417 MB) 71 us, 5.9 TB/s (a copy of 1 GiB 5.15).
 //
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * W, XL == 8 ? 1 : 4) void int4_stream_kernel(In
 // Bound by the power that MFMAs, conversions and LDS reads take together (1.6 to 1.75
 // GHz, matrix cores busy 0.56): 2048 rows, K 7168, N 8192 in groups of 128 take 245
 // us, in groups of 32 with zero points 290, 4096 rows to 16384 columns 905 us (1.06 PF;
-// a BF16 product of the same sizes by the library 193 and 650 us).
+// a BF16 product of the same sizes by the library 178 to 193 and 650 to 685 us).
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float v2f __attribute__((ext_vector_type(2)));

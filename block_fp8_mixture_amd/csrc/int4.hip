@@ -125,11 +125,10 @@ __device__ __forceinline__ float over(float x) {
   return __builtin_fmaf(__builtin_fmaf(-q, static_cast<float>(D), x), kInv, q);
 }
 
-// Bound by memory: 32768 x 7168 BF16 in groups of 128 without zero points 125 us (4.7
-// TB/s, as a copy), FP32 in groups of 64 231 us; groups of 32 with zero points 145 us
-// (4.2 TB/s: two extrema and a division for every four lanes show). Extrema of 16-bit
-// values two to a word and rounding without a remainder's test per value took these
-// from 165 and 203 us.
+// Bound by memory: 32768 x 7168 BF16 in groups of 128 without zero points 123 us, in
+// groups of 32 with zero points 125 (4.7 TB/s, as a copy), FP32 in groups of 64 223;
+// right behind another kernel's writes 154 to 160. Extrema of 16-bit values two to a word
+// and rounding without a remainder's test per value: with neither, 165 and 203 us.
 template <int TYPE, int G, bool ZEROS>
 __global__ __launch_bounds__(kI4Threads) void int4_quant_kernel(const void* __restrict__ w, int64_t chunks,
                                                                 int scale_f16, uint32_t* __restrict__ codes,
@@ -195,7 +194,7 @@ __global__ __launch_bounds__(kI4Threads) void int4_quant_kernel(const void* __re
 
 // 8 columns per thread and step, so that a wave stores 1 KiB without gaps (with 16
 // a thread, two stores of every other 16 bytes, 32768 x 7168 took 163 to 168 us), and
-// four steps' loads issued before any is used: 127 to 129 us, 4.7 TB/s. A scale has at most 11 significant
+// four steps' loads issued before any is used: 124 to 128 us, 4.7 TB/s. A scale has at most 11 significant
 // bits and q - z at most 9: the product is exact in float, and rounded once.
 __global__ __launch_bounds__(kI4Threads) void int4_dequant_kernel(const uint32_t* __restrict__ codes,
                                                                   const uint16_t* __restrict__ scales,
