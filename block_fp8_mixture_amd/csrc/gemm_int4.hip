@@ -122,9 +122,9 @@ __device__ __forceinline__ int int4_units(const Int4GemmArgs& p) {
 // how long its code takes to arrive.
 //
 // Bound by latency up to some 20 MB of weights (a launch, the first loads, LDS, the
-// sums), beyond by the weights' bytes; captured, with cold weights: 1 row 7168 -> 4096 gated 9 us, 16 rows 2048 ->
-// 7168 8 us, 1 token's 8 experts 4096 -> 1024 12.5 us, 64 tokens' 256 experts 6144 ->
-// 512 (417 MB) 71 us, 5.9 TB/s (a copy of 1 GiB 5.15).
+// sums), beyond by the weights' bytes; captured, with cold weights: 1 row 7168 -> 4096
+// gated 9 us, 16 rows 2048 -> 7168 8 us, 1 token's 8 experts 4096 -> 1024 12.5 us, 64
+// tokens' 256 experts 6144 -> 512 (417 MB) 71 us, 5.9 TB/s (a copy of 1 GiB 5.15).
 //
 // Groups of fewer than 128 columns: an instruction's 32 K values have to be of one
 // group in every lane, so a lane reads word g of each 16 bytes of a row, else
@@ -703,7 +703,7 @@ __global__ __launch_bounds__(kTlThreads, 2) void int4_tiled_kernel(Int4GemmArgs 
   uint8_t* const s_c = s_buf;
   lds_barrier();  // the rows are read
   auto write = [&](int row, int col, float v0, float v1) __attribute__((always_inline)) {
-    // v0, v1: this column's values of rows row and row + step of the pair
+    // v0, v1: this column's values of rows row and row + 1 (gated: row + 2)
     const bool odd = lane & 1;
     const float other = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(odd ? v0 : v1), 0xB1, 0xF, 0xF, false));
     const uint32_t two = odd ? pack_bf16x2(other, v1) : pack_bf16x2(v0, other);
